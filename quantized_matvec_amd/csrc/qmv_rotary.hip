@@ -1,0 +1,216 @@
+// Rotary positions: the table of cosines and sines, and the rotation of
+// queries and keys by it, forward and inverse.
+//
+// A pair (a, b) of a head's elements at position p, with (c, s) the table's
+// entry of p and of the pair, becomes (a c - b s, b c + a s).  The rotation is
+// orthogonal (times the table's gain), so its backward is the rotation by
+// (c, -s).  Products and sums are rounded one by one in fp32 (no fused
+// multiply-add), so the result is a function of the operands alone and the
+// cache append gets the same bits; the one rounding to the heads' type comes
+// last.
+#include <algorithm>
+
+#include "qmv_attention.hpp"
+
+#pragma clang fp contract(off)
+
+namespace qmv {
+
+struct Freqs {
+  double f[128];
+};
+
+// Angles in float64: at position 2^20 an fp32 angle would be off by 2^-4.
+__global__ __launch_bounds__(256) void rope_table_kernel(Freqs fr, int half, int64_t n, double gain,
+                                                         float2 *__restrict__ table) {
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+    const int64_t pos = i / half;
+    double s, c;
+    sincos((double)pos * fr.f[i - pos * half], &s, &c);
+    table[i] = make_float2((float)(gain * c), (float)(gain * s));
+  }
+}
+
+hipError_t launch_rope_table(const double *freqs, int half, int64_t max_pos, double gain,
+                             float *table, hipStream_t st) {
+  Freqs fr{};
+  for (int i = 0; i < half; ++i) fr.f[i] = freqs[i];
+  const int64_t n = max_pos * half;
+  const unsigned grid = (unsigned)std::min<int64_t>((n + 255) / 256, 16384);
+  hipLaunchKernelGGL(rope_table_kernel, dim3(grid), dim3(256), 0, st, fr, half, n, gain,
+                     reinterpret_cast<float2 *>(table));
+  return hipGetLastError();
+}
+
+// ---------------------------------------------------------------------------
+// rotary
+//
+// Bound by memory: every element is read and written once.  A unit of work is
+// what one thread loads and stores: V pairs as two runs of V elements (halves),
+// V / 2 pairs as one run (interleaved), or V elements that are only copied.
+// Each unit reads its own elements only, so the output may be the input.
+// V is the widest run that the pair count allows: 8 elements, else 4 (half of
+// the rotated part a multiple of 4), else single pairs.
+// ---------------------------------------------------------------------------
+template <int DT, int V>
+__device__ __forceinline__ void load_run(const void *base, int64_t at, float (&x)[V]) {
+  if constexpr (DT == kF32) {
+    const float *p = static_cast<const float *>(base) + at;
+    if constexpr (V % 4 == 0) {
+#pragma unroll
+      for (int i = 0; i < V / 4; ++i) {
+        const float4 v = reinterpret_cast<const float4 *>(p)[i];
+        x[4 * i] = v.x, x[4 * i + 1] = v.y, x[4 * i + 2] = v.z, x[4 * i + 3] = v.w;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) x[i] = p[i];
+    }
+  } else {
+    const uint16_t *p = static_cast<const uint16_t *>(base) + at;
+    if constexpr (V == 1) {
+      x[0] = bits16_to_f32<DT>(p[0]);
+    } else {
+      typedef uint32_t words __attribute__((ext_vector_type(V / 2)));
+      uint32_t w[V / 2];
+      __builtin_memcpy(w, __builtin_assume_aligned(p, sizeof(words)), sizeof(words));
+#pragma unroll
+      for (int i = 0; i < V / 2; ++i) {
+        x[2 * i] = bits16_to_f32<DT>(w[i] & 0xffffu);
+        x[2 * i + 1] = bits16_to_f32<DT>(w[i] >> 16);
+      }
+    }
+  }
+}
+
+template <int DT, int V>
+__device__ __forceinline__ void store_run(void *base, int64_t at, const float (&x)[V]) {
+  if constexpr (DT == kF32) {
+    float *p = static_cast<float *>(base) + at;
+    if constexpr (V % 4 == 0) {
+#pragma unroll
+      for (int i = 0; i < V / 4; ++i)
+        reinterpret_cast<float4 *>(p)[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) p[i] = x[i];
+    }
+  } else {
+    uint16_t *p = static_cast<uint16_t *>(base) + at;
+    if constexpr (V == 1) {
+      store_elem<DT>(p, 0, x[0]);
+    } else {
+      uint32_t w[V / 2];
+#pragma unroll
+      for (int i = 0; i < V / 2; ++i) w[i] = cvt_pair<DT>(x[2 * i], x[2 * i + 1]);
+      __builtin_memcpy(__builtin_assume_aligned(p, 2 * V), w, sizeof(w));
+    }
+  }
+}
+
+struct RotaryArgs {
+  Heads q, qo, k, ko;
+  Rope rope;
+  const int64_t *positions;
+  int64_t tokens;
+  int dim;
+  int per_head;  // units of a head
+  int per_token; // units of a token: heads * per_head
+};
+
+template <int DT, int V, bool INTER>
+__global__ __launch_bounds__(256) void rotary_kernel(RotaryArgs a, float sign) {
+  const int64_t base = (int64_t)blockIdx.x * 256;
+  const int64_t t0 = base / a.per_token;
+  const uint32_t u = (uint32_t)(base - t0 * a.per_token) + threadIdx.x;
+  const int64_t t = t0 + u / (uint32_t)a.per_token;
+  if (t >= a.tokens) return;
+  const uint32_t w = u % (uint32_t)a.per_token;
+  int h = (int)(w / (uint32_t)a.per_head);
+  const int i = (int)(w % (uint32_t)a.per_head);
+  const bool isk = h >= a.q.heads;
+  if (isk) h -= a.q.heads;
+  const Heads &x = isk ? a.k : a.q;
+  const Heads &y = isk ? a.ko : a.qo;
+  const int64_t xo = t * x.ts + h * x.hs, yo = t * y.ts + h * y.hs;
+  const int half = a.rope.half;
+  const int64_t pos = a.positions[t];
+  const bool there = pos >= 0 && pos < a.rope.max_pos;
+  const float2 *cs = a.rope.table + (there ? pos : 0) * half;
+
+  constexpr int NP = INTER ? V / 2 : V;  // pairs of a unit
+  const int turned = half / NP;          // units that turn
+  if (i < turned) {
+    float c[NP], s[NP];
+#pragma unroll
+    for (int j = 0; j < NP; ++j) {
+      const float2 v = cs[i * NP + j];
+      c[j] = v.x;
+      s[j] = sign * v.y;
+    }
+    if constexpr (INTER) {
+      float e[V], r[V];
+      load_run<DT, V>(x.p, xo + i * V, e);
+#pragma unroll
+      for (int j = 0; j < NP; ++j) {
+        r[2 * j] = there ? e[2 * j] * c[j] - e[2 * j + 1] * s[j] : 0.f;
+        r[2 * j + 1] = there ? e[2 * j + 1] * c[j] + e[2 * j] * s[j] : 0.f;
+      }
+      store_run<DT, V>(y.p, yo + i * V, r);
+    } else {
+      float e[V], f[V], r[V], g[V];
+      load_run<DT, V>(x.p, xo + i * V, e);
+      load_run<DT, V>(x.p, xo + half + i * V, f);
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        r[j] = there ? e[j] * c[j] - f[j] * s[j] : 0.f;
+        g[j] = there ? f[j] * c[j] + e[j] * s[j] : 0.f;
+      }
+      store_run<DT, V>(y.p, yo + i * V, r);
+      store_run<DT, V>(y.p, yo + half + i * V, g);
+    }
+  } else {
+    const int at = 2 * half + (i - turned) * V;
+    float e[V];
+    load_run<DT, V>(x.p, xo + at, e);
+#pragma unroll
+    for (int j = 0; j < V; ++j) e[j] = there ? e[j] : 0.f;
+    store_run<DT, V>(y.p, yo + at, e);
+  }
+}
+
+template <int DT, int V, bool INTER>
+static void launch_rotary_t(RotaryArgs &a, float sign, hipStream_t st) {
+  const int half = a.rope.half;
+  a.per_head = half / (INTER ? V / 2 : V) + (a.dim - 2 * half) / V;
+  a.per_token = a.per_head * (a.q.heads + a.k.heads);
+  const int64_t units = a.tokens * a.per_token;
+  hipLaunchKernelGGL((rotary_kernel<DT, V, INTER>), dim3((unsigned)((units + 255) / 256)), dim3(256),
+                     0, st, a, sign);
+}
+
+template <int DT>
+static void launch_rotary_d(RotaryArgs &a, float sign, hipStream_t st) {
+  const int half = a.rope.half;
+  if (a.rope.interleaved) {
+    if (half % 4 == 0) launch_rotary_t<DT, 8, true>(a, sign, st);
+    else launch_rotary_t<DT, 2, true>(a, sign, st);
+  } else {
+    if (half % 8 == 0) launch_rotary_t<DT, 8, false>(a, sign, st);
+    else if (half % 4 == 0) launch_rotary_t<DT, 4, false>(a, sign, st);
+    else launch_rotary_t<DT, 1, false>(a, sign, st);
+  }
+}
+
+hipError_t launch_rotary(const Heads &q, const Heads &qo, const Heads &k, const Heads &ko, int dt,
+                         int64_t tokens, int dim, const int64_t *positions, const Rope &rope,
+                         bool inverse, hipStream_t st) {
+  RotaryArgs a{q, qo, k, ko, rope, positions, tokens, dim, 0, 0};
+  const float sign = inverse ? -1.f : 1.f;
+  if (dt == kF32) launch_rotary_d<kF32>(a, sign, st);
+  else if (dt == kF16) launch_rotary_d<kF16>(a, sign, st);
+  else launch_rotary_d<kBF16>(a, sign, st);
+  return hipGetLastError();
+}
+
+}  // namespace qmv
