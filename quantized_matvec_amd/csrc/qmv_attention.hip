@@ -4,29 +4,9 @@
 // running maximum of the scores; m and both sums are fp32.
 #include <algorithm>
 
-#include "qmv_attention.hpp"
+#include "qmv_attention_mfma.hpp"
 
 namespace qmv {
-
-struct AttnArgs {
-  KVCache c;
-  KVBatch kb;
-  Heads q, out;
-  int group;        // query heads of a cache head
-  float scale_log2; // scale * log2(e)
-  int64_t max_kv;
-  int window;       // 0: none
-  bool causal;
-};
-
-// Keys [lo, hi) that token i of the sequence sees.
-__device__ __forceinline__ void key_range(const AttnArgs &a, const SeqRange &s, int i, int &lo,
-                                          int &hi) {
-  const int pos = s.pos0 + i;
-  const int len = (int)(s.len < a.max_kv ? s.len : a.max_kv);
-  hi = a.causal ? (pos + 1 < len ? pos + 1 : len) : len;
-  lo = a.window > 0 && pos >= a.window ? pos - a.window + 1 : 0;
-}
 
 __device__ __forceinline__ float wave_max(float v) {
 #pragma unroll
@@ -44,7 +24,7 @@ __device__ __forceinline__ float wave_sum(float v) {
 // key, then each lane sums over the keys for two pairs of elements.
 // ---------------------------------------------------------------------------
 template <int DT>
-__global__ __launch_bounds__(64) void attention_rows_kernel(AttnArgs a, int qt) {
+__global__ __launch_bounds__(64) void attention_rows_kernel(AttnArgs a, float scale_log2) {
   __shared__ float2 lut[256];
   __shared__ float qs[256];
   __shared__ float w[8][64];     // p_j a_j of each value block
@@ -57,11 +37,11 @@ __global__ __launch_bounds__(64) void attention_rows_kernel(AttnArgs a, int qt) 
   if (i >= s.n || i >= a.kb.max_q) return;
   const int kh = h / a.group;
   const int dim = a.c.dim, nb = dim / a.c.bs, ps = 1 << a.c.log2page;
-  const uint32_t *tb = table_bits(qt);
+  const uint32_t *tb = table_bits(a.qt);
   for (int e = lane; e < 256; e += 64)
     lut[e] = make_float2(__uint_as_float(tb[e >> 4]), __uint_as_float(tb[e & 15]));
   const uint16_t *qrow = static_cast<const uint16_t *>(a.q.p) + (s.row0 + i) * a.q.ts + h * a.q.hs;
-  for (int e = lane; e < dim; e += 64) qs[e] = bits16_to_f32<DT>(qrow[e]) * a.scale_log2;
+  for (int e = lane; e < dim; e += 64) qs[e] = bits16_to_f32<DT>(qrow[e]) * scale_log2;
   __syncthreads();
 
   int lo, hi;
@@ -136,17 +116,30 @@ __global__ __launch_bounds__(64) void attention_rows_kernel(AttnArgs a, int qt) 
   }
 }
 
-size_t attention_workspace_bytes(const KVCache &, const KVBatch &, int, int64_t, int64_t) { return 0; }
+hipError_t launch_attention_rows(const AttnArgs &a, int dt, hipStream_t st) {
+  const dim3 grid((unsigned)(a.kb.max_q * a.q.heads), (unsigned)a.kb.batch);
+  const float sl = a.scale * 1.44269504088896340736f;
+  if (dt == kBF16) hipLaunchKernelGGL((attention_rows_kernel<kBF16>), grid, dim3(64), 0, st, a, sl);
+  else hipLaunchKernelGGL((attention_rows_kernel<kF16>), grid, dim3(64), 0, st, a, sl);
+  return hipGetLastError();
+}
+
+size_t attention_workspace_bytes(const KVCache &c, const KVBatch &kb, int q_heads, int64_t max_kv,
+                                 int64_t window) {
+  const int64_t rows = (int64_t)kb.max_q * (q_heads / c.heads);
+  if (rows <= 16 && decode_eligible(c, (int)rows))
+    return decode_workspace_bytes(c, kb, (int)rows, max_kv, window);
+  return 0;
+}
 
 hipError_t launch_attention(const KVCache &c, int dt, int qt, const KVBatch &kb, const Heads &q,
                             int64_t max_kv, float scale, bool causal, int64_t window,
                             const Heads &out, void *ws, hipStream_t st) {
-  AttnArgs a{c, kb, q, out, q.heads / c.heads, scale * 1.44269504088896340736f, max_kv,
-             (int)std::min<int64_t>(window, INT32_MAX), causal};
-  const dim3 grid((unsigned)(kb.max_q * q.heads), (unsigned)kb.batch);
-  if (dt == kBF16) hipLaunchKernelGGL((attention_rows_kernel<kBF16>), grid, dim3(64), 0, st, a, qt);
-  else hipLaunchKernelGGL((attention_rows_kernel<kF16>), grid, dim3(64), 0, st, a, qt);
-  return hipGetLastError();
+  const AttnArgs a{c, kb, q, out, q.heads / c.heads, scale, (int)max_kv,
+                   (int)std::min<int64_t>(window, INT32_MAX), causal, qt};
+  const int64_t rows = (int64_t)kb.max_q * a.group;
+  if (rows <= 16 && decode_eligible(c, (int)rows)) return launch_attention_decode(a, dt, ws, st);
+  return launch_attention_rows(a, dt, st);
 }
 
 }  // namespace qmv

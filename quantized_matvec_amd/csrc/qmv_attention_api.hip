@@ -17,7 +17,7 @@ int launch_status(hipError_t e) { return e == hipSuccess ? QMV_OK : QMV_ERR_LAUN
 
 // The strides of a dimension of one count for nothing.
 int check_heads(const qmv_heads *h, int64_t tokens, int size, Heads *out) {
-  if (!h || !h->data || h->heads <= 0 || h->heads > 65536) return QMV_ERR_INVALID_ARG;
+  if (!h || !h->data || h->heads <= 0 || h->heads > 65535) return QMV_ERR_INVALID_ARG;
   Heads v{h->data, tokens > 1 ? h->token_stride : 0, h->heads > 1 ? h->head_stride : 0, h->heads};
   if (v.ts < 0 || v.hs < 0) return QMV_ERR_INVALID_ARG;
   if (v.ts > INT64_MAX / (kMost * 8) || v.hs > INT64_MAX / (kMost * 8)) return QMV_ERR_INVALID_ARG;
@@ -38,7 +38,7 @@ int check_rope(const qmv_rope *r, int32_t head_dim, Rope *out) {
 
 // Sizes of the cache, and whether its arrays are there where `arrays` is set.
 int check_cache(const qmv_kv_cache *c, bool arrays, KVCache *out) {
-  if (!c || c->num_pages <= 0 || c->num_pages > INT32_MAX || c->heads <= 0 || c->heads > 65536)
+  if (!c || c->num_pages <= 0 || c->num_pages > INT32_MAX || c->heads <= 0 || c->heads > 65535)
     return QMV_ERR_INVALID_ARG;
   if (c->quant_type != QMV_NF4 && c->quant_type != QMV_FP4) return QMV_ERR_INVALID_ARG;
   if (c->dtype != QMV_F32 && c->dtype != QMV_F16 && c->dtype != QMV_BF16) return QMV_ERR_INVALID_ARG;
@@ -47,9 +47,8 @@ int check_cache(const qmv_kv_cache *c, bool arrays, KVCache *out) {
   if (c->head_dim < 32 || c->head_dim > 256 || c->head_dim % 32) return QMV_ERR_UNSUPPORTED;
   if (!is_pow2(c->blocksize) || c->blocksize < 32 || c->head_dim % c->blocksize)
     return QMV_ERR_UNSUPPORTED;
-  // every byte offset of the arrays fits in 64 bits
-  if (c->num_pages > INT64_MAX / ((int64_t)c->heads * c->page_size * c->head_dim))
-    return QMV_ERR_INVALID_ARG;
+  // offsets inside a page fit in 31 bits (num_pages < 2^31: all of them in 64)
+  if ((int64_t)c->heads * c->page_size * c->head_dim >= kMost) return QMV_ERR_TOO_LARGE;
   if (arrays) {
     if (!c->k_codes || !c->v_codes || !c->k_scales || !c->v_scales) return QMV_ERR_INVALID_ARG;
     if (!aligned(c->k_codes, 16) || !aligned(c->v_codes, 16) || !aligned(c->k_scales, 16) ||
@@ -227,7 +226,7 @@ size_t qmv_attention_4bit_workspace(const qmv_kv_cache *cache, const qmv_kv_batc
   KVBatch kb;
   if (check_cache(cache, false, &c) != QMV_OK || check_batch(batch, tokens, false, &kb) != QMV_OK)
     return 0;
-  if (q_heads <= 0 || q_heads > 65536 || q_heads % c.heads || max_kv < 0 || window < 0) return 0;
+  if (q_heads <= 0 || q_heads > 65535 || q_heads % c.heads || max_kv < 0 || window < 0) return 0;
   return attention_workspace_bytes(c, kb, q_heads, reach(c, kb, max_kv), window);
 }
 
@@ -247,6 +246,8 @@ int qmv_attention_4bit(const qmv_heads *q, const qmv_kv_cache *cache, const qmv_
     return QMV_ERR_INVALID_ARG;
   if (kb.max_q > (kMost - 1) / hq.heads) return QMV_ERR_TOO_LARGE;
   const int64_t most = reach(c, kb, max_kv);
+  // steps of 64 tokens over all sequences and heads are counted in 31 bits
+  if ((most / 64 + 2) * c.heads >= kMost / kb.batch) return QMV_ERR_TOO_LARGE;
   const size_t need = attention_workspace_bytes(c, kb, hq.heads, most, window);
   if (need && (!workspace || workspace_bytes < need)) return QMV_ERR_WORKSPACE;
   if (need && !aligned(workspace, 16)) return QMV_ERR_ALIGNMENT;
