@@ -169,7 +169,7 @@ struct StepPages {
 
 // Waves of a workgroup, which has a compute unit to itself: three waves of a
 // SIMD share its registers, or two where rows are long.
-__host__ __device__ constexpr int decode_waves(int D) { return D <= 128 ? 12 : 8; }
+__host__ __device__ constexpr int decode_waves(int D) { return D <= 96 ? 12 : 8; }
 
 template <int D, int CB, int RJ, int DT, bool LO>
 __global__ __launch_bounds__(64 * decode_waves(D), decode_waves(D) / 4) void attention_decode_kernel(DecodeArgs da) {
@@ -194,10 +194,8 @@ __global__ __launch_bounds__(64 * decode_waves(D), decode_waves(D) / 4) void att
   };
   __shared__ Start starts[kWaves];
   const AttnArgs &a = da.a;
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int r = lane & 15, g = lane >> 4;
-  const uint32_t copy = lut_copy<LO>(lane);
+  const int tid = threadIdx.x;
+  const int wave = uniform(tid >> 6);
 
   // this wave's steps [cur, end) of the order (sequence, head, step): the
   // lengths are summed up, and the thread whose sequence holds a wave's first
@@ -236,49 +234,40 @@ __global__ __launch_bounds__(64 * decode_waves(D), decode_waves(D) / 4) void att
   const int wave_run = runs.wave_from<kWaves>(blockIdx.x, wave);
   const int end = runs.wave_from<kWaves>(blockIdx.x, wave + 1);
   int cur = wave_run;
-  q = uniform(starts[wave].q);  // means nothing where cur == end
-  int b = uniform(starts[wave].b);
-  int first = uniform(starts[wave].first);
   // whether the run lies in one head, and which
   const int run_steps = uniform(starts[0].q.steps), run_first = uniform(starts[0].first);
   const int run_h = (run_from - run_first) / run_steps;
   const int run_head0 = run_first + run_h * run_steps;
   const bool joined = run_to <= run_head0 + run_steps;
-  auto unit = [&](int ev) { return ldexpf(1.f / half_factor(a.qt), -ev); };
-  auto out_row = [&](const SeqSteps &q, int h, int row) {
-    return static_cast<uint16_t *>(a.out.p) + (q.s.row0 + row / a.group) * a.out.ts +
-           (h * a.group + row % a.group) * a.out.hs;
-  };
-  f32x4_t acc[KU][2];
-  float m[RJ], l[RJ];
-  int ev = 100;  // weights are scaled by 2^ev
-  auto clear = [&] {
-#pragma unroll
-    for (int c = 0; c < KU; ++c) acc[c][0] = acc[c][1] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int j = 0; j < RJ; ++j) m[j] = kNoScore, l[j] = 0.f;
-    ev = 100;
-  };
-  clear();
-
+  // (a wave of a joined run takes part in it also without a step of its own)
+  if (!joined && cur >= end) return;
+  const Start &start = starts[joined ? 0 : wave];
+  q = uniform(start.q);
+  int b = uniform(start.b), first = uniform(start.first);
   const int ps = 1 << a.c.log2page;
-  int koff[KU];  // of key load L: (score tile i, k-step c) = 4 L + g
-#pragma unroll
-  for (int L = 0; L < KU; ++L) {
-    const int i = (4 * L + g) / KU, c = 4 * L + g - i * KU;
-    koff[L] = (4 * (r & 3) + i) * row_bytes + 16 * c;
-  }
   // a page's bytes fit in 31 bits (checked on the host), its number times them
   // does not
   const uint32_t page_codes = (uint32_t)(heads << a.c.log2page) * row_bytes;
   const uint32_t page_scales = (uint32_t)(heads << a.c.log2page) * (2 * NB);
 
-  while (cur < end && b < a.kb.batch) {
-    if (q.steps == 0) {
-      if (++b < a.kb.batch) q = uniform(seq_steps(a, b));
-      continue;
+  for (;;) {
+    while (q.steps == 0) {  // sequences without tokens
+      if (++b >= a.kb.batch) return;
+      q = uniform(seq_steps(a, b));
     }
-    const int h = (cur - first) / q.steps;
+    // what depends on the lane is found anew for each segment: kept over the
+    // loop, its registers are spilled
+    int lane = tid & 63;
+    asm volatile("" : "+v"(lane));
+    const int r = lane & 15, g = lane >> 4;
+    const uint32_t copy = lut_copy<LO>(lane);
+    int koff[KU];  // of key load L: (score tile i, k-step c) = 4 L + g
+#pragma unroll
+    for (int L = 0; L < KU; ++L) {
+      const int i = (4 * L + g) / KU, c = 4 * L + g - i * KU;
+      koff[L] = (4 * (r & 3) + i) * row_bytes + 16 * c;
+    }
+    const int h = joined ? run_h : (cur - first) / q.steps;
     const int head0 = first + h * q.steps;
     const int t_from = cur - head0;
     const int t_to = end - head0 < q.steps ? end - head0 : q.steps;
@@ -327,7 +316,7 @@ __global__ __launch_bounds__(64 * decode_waves(D), decode_waves(D) / 4) void att
     };
 
     int t = t_from;
-    const int t_last = t_to - 1;
+    const int t_last = t_to > t_from ? t_to - 1 : t_from;
     StepPages p = pages(t);
     StepPages pn = pages(t + 1 < t_last ? t + 1 : t_last);
     // ---- queries: tile row r, 8 elements of each k-step, in fp16; the scale
@@ -342,8 +331,6 @@ __global__ __launch_bounds__(64 * decode_waves(D), decode_waves(D) / 4) void att
     uint4 raw[KU];
 #pragma unroll
     for (int c = 0; c < KU; ++c) raw[c] = *reinterpret_cast<const uint4 *>(qrow + 32 * c + 8 * g);
-    load_keys(t, p);
-    load_values(t, p);
     float big = 0.f;
     f16x8_t qf[KU];
     {
@@ -384,8 +371,16 @@ __global__ __launch_bounds__(64 * decode_waves(D), decode_waves(D) / 4) void att
     key_range(a, q.s, 0, unused, all_hi);        // every row sees keys below all_hi
     key_range(a, q.s, q.n - 1, all_lo, unused);  // and from all_lo on
 
-    clear();
 
+    load_keys(t, p);
+    load_values(t, p);
+    f32x4_t acc[KU][2];
+#pragma unroll
+    for (int c = 0; c < KU; ++c) acc[c][0] = acc[c][1] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    float m[RJ], l[RJ];
+#pragma unroll
+    for (int j = 0; j < RJ; ++j) m[j] = kNoScore, l[j] = 0.f;
+    int ev = 100;  // weights are scaled by 2^ev
     {
       for (; t < t_to; ++t) {
         const int t0 = q.lo + t * kStep;
@@ -546,85 +541,83 @@ __global__ __launch_bounds__(64 * decode_waves(D), decode_waves(D) / 4) void att
         jl[wave][g * RJ + j] = l[j];
       }
     }
-    if (!joined) {
-      const bool whole = t_from == 0 && t_to == q.steps;
-      const float sum = jl[wave][r % QR];
-      const float f = unit(ev) * (whole ? (sum > 0.f ? 1.f / sum : 0.f) : 1.f);
-      const int part = 2 * (kWaves * blockIdx.x + wave) + (cur == wave_run ? 0 : 1);
-      if (r < rows) {
+    const float unit = ldexpf(1.f / half_factor(a.qt), -ev);
+    auto out_row = [&](int row) {
+      return static_cast<uint16_t *>(a.out.p) + (q.s.row0 + row / a.group) * a.out.ts +
+             (h * a.group + row % a.group) * a.out.hs;
+    };
+    if (joined) {
+      // ---- the run lies in this head: its waves' sums together, 32 elements
+      // at a time ----
+      const bool whole = run_from == head0 && run_to == head0 + q.steps;
+      __syncthreads();
+      float top = kNoScore;
 #pragma unroll
-        for (int c = 0; c < KU; ++c) {
-          const float o[8] = {acc[c][0][0] * f, acc[c][1][0] * f, acc[c][0][1] * f, acc[c][1][1] * f,
-                              acc[c][0][2] * f, acc[c][1][2] * f, acc[c][0][3] * f, acc[c][1][3] * f};
+      for (int w = 0; w < kWaves; ++w) top = fmaxf(top, jm[w][r % QR]);
+      const float f = unit * __builtin_amdgcn_exp2f(jm[wave][r % QR] - top);
+      const int64_t part = (int64_t)(2 * kWaves) * blockIdx.x * QR;
+#pragma unroll
+      for (int c = 0; c < KU; ++c) {
+        if (r < QR) {
+          float4 *dst = reinterpret_cast<float4 *>(&sh.join[wave][r][8 * g]);
+          dst[0] = make_float4(acc[c][0][0] * f, acc[c][1][0] * f, acc[c][0][1] * f, acc[c][1][1] * f);
+          dst[1] = make_float4(acc[c][0][2] * f, acc[c][1][2] * f, acc[c][0][3] * f, acc[c][1][3] * f);
+        }
+        __syncthreads();
+        const int row = tid >> 3, d = 4 * (tid & 7);
+        if (row < rows) {
+          float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+          float mx = kNoScore, sum = 0.f;
+#pragma unroll
+          for (int w = 0; w < kWaves; ++w) {
+            const float4 y = *reinterpret_cast<const float4 *>(&sh.join[w][row][d]);
+            o.x += y.x, o.y += y.y, o.z += y.z, o.w += y.w;
+            mx = fmaxf(mx, jm[w][row]);
+          }
+#pragma unroll
+          for (int w = 0; w < kWaves; ++w) sum += jl[w][row] * __builtin_amdgcn_exp2f(jm[w][row] - mx);
           if (whole) {
-            *reinterpret_cast<uint4 *>(out_row(q, h, r) + 32 * c + 8 * g) =
-                make_uint4(cvt_pair<DT>(o[0], o[1]), cvt_pair<DT>(o[2], o[3]), cvt_pair<DT>(o[4], o[5]),
-                           cvt_pair<DT>(o[6], o[7]));
+            const float inv = sum > 0.f ? 1.f / sum : 0.f;
+            *reinterpret_cast<uint2 *>(out_row(row) + 32 * c + d) =
+                make_uint2(cvt_pair<DT>(o.x * inv, o.y * inv), cvt_pair<DT>(o.z * inv, o.w * inv));
           } else {
-            float4 *dst = reinterpret_cast<float4 *>(da.part.o + ((int64_t)part * QR + r) * D + 32 * c + 8 * g);
-            dst[0] = make_float4(o[0], o[1], o[2], o[3]);
-            dst[1] = make_float4(o[4], o[5], o[6], o[7]);
+            *reinterpret_cast<float4 *>(da.part.o + (part + row) * D + 32 * c + d) = o;
+            if (c == 0 && d == 0) da.part.ml[part + row] = make_float2(mx, sum);
           }
         }
-        if (!whole && g == 0) da.part.ml[(int64_t)part * QR + r] = make_float2(jm[wave][r], sum);
+        __syncthreads();
       }
+      return;
+    }
+    // ---- the wave writes them itself ----
+    const bool whole = t_from == 0 && t_to == q.steps;
+    const float sum = jl[wave][r % QR];
+    const float f = unit * (whole ? (sum > 0.f ? 1.f / sum : 0.f) : 1.f);
+    const int part = 2 * (kWaves * blockIdx.x + wave) + (cur == wave_run ? 0 : 1);
+    if (r < rows) {
+#pragma unroll
+      for (int c = 0; c < KU; ++c) {
+        const float o[8] = {acc[c][0][0] * f, acc[c][1][0] * f, acc[c][0][1] * f, acc[c][1][1] * f,
+                            acc[c][0][2] * f, acc[c][1][2] * f, acc[c][0][3] * f, acc[c][1][3] * f};
+        if (whole) {
+          *reinterpret_cast<uint4 *>(out_row(r) + 32 * c + 8 * g) =
+              make_uint4(cvt_pair<DT>(o[0], o[1]), cvt_pair<DT>(o[2], o[3]), cvt_pair<DT>(o[4], o[5]),
+                         cvt_pair<DT>(o[6], o[7]));
+        } else {
+          float4 *dst = reinterpret_cast<float4 *>(da.part.o + ((int64_t)part * QR + r) * D + 32 * c + 8 * g);
+          dst[0] = make_float4(o[0], o[1], o[2], o[3]);
+          dst[1] = make_float4(o[4], o[5], o[6], o[7]);
+        }
+      }
+      if (!whole && g == 0) da.part.ml[(int64_t)part * QR + r] = make_float2(jm[wave][r], sum);
     }
     cur = head0 + t_to;
+    if (cur >= end) return;
     if (cur == first + q.steps * heads) {
       first = cur;
-      if (++b < a.kb.batch) q = uniform(seq_steps(a, b));
+      if (++b >= a.kb.batch) return;
+      q = uniform(seq_steps(a, b));
     }
-  }
-  if (!joined) return;
-
-  // ---- the run lies in one head: the waves' sums together, 32 elements at a
-  // time (a wave without a step has the sums it began with) ----
-  const SeqSteps sq = uniform(starts[0].q);
-  const int rows = sq.n * a.group;
-  const bool whole = run_from == run_head0 && run_to == run_head0 + run_steps;
-  if (r == 0) {
-#pragma unroll
-    for (int j = 0; j < RJ; ++j) {
-      jm[wave][g * RJ + j] = m[j];
-      jl[wave][g * RJ + j] = l[j];
-    }
-  }
-  __syncthreads();
-  float top = kNoScore;
-#pragma unroll
-  for (int w = 0; w < kWaves; ++w) top = fmaxf(top, jm[w][r % QR]);
-  const float f = unit(ev) * __builtin_amdgcn_exp2f(jm[wave][r % QR] - top);
-  const int64_t part = (int64_t)(2 * kWaves) * blockIdx.x * QR;
-#pragma unroll
-  for (int c = 0; c < KU; ++c) {
-    if (r < QR) {
-      float4 *dst = reinterpret_cast<float4 *>(&sh.join[wave][r][8 * g]);
-      dst[0] = make_float4(acc[c][0][0] * f, acc[c][1][0] * f, acc[c][0][1] * f, acc[c][1][1] * f);
-      dst[1] = make_float4(acc[c][0][2] * f, acc[c][1][2] * f, acc[c][0][3] * f, acc[c][1][3] * f);
-    }
-    __syncthreads();
-    const int row = tid >> 3, d = 4 * (tid & 7);
-    if (row < rows) {
-      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-      float mx = kNoScore, sum = 0.f;
-#pragma unroll
-      for (int w = 0; w < kWaves; ++w) {
-        const float4 y = *reinterpret_cast<const float4 *>(&sh.join[w][row][d]);
-        o.x += y.x, o.y += y.y, o.z += y.z, o.w += y.w;
-        mx = fmaxf(mx, jm[w][row]);
-      }
-#pragma unroll
-      for (int w = 0; w < kWaves; ++w) sum += jl[w][row] * __builtin_amdgcn_exp2f(jm[w][row] - mx);
-      if (whole) {
-        const float inv = sum > 0.f ? 1.f / sum : 0.f;
-        *reinterpret_cast<uint2 *>(out_row(sq, run_h, row) + 32 * c + d) =
-            make_uint2(cvt_pair<DT>(o.x * inv, o.y * inv), cvt_pair<DT>(o.z * inv, o.w * inv));
-      } else {
-        *reinterpret_cast<float4 *>(da.part.o + (part + row) * D + 32 * c + d) = o;
-        if (c == 0 && d == 0) da.part.ml[part + row] = make_float2(mx, sum);
-      }
-    }
-    __syncthreads();
   }
 }
 
