@@ -21,7 +21,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libqmv.so")
 SOURCES = ["qmv_api.hip", "qmv_codec.hip", "qmv_blockwise.hip", "qmv_embedding.hip", "qmv_gemv.hip",
            "qmv_gemm.hip", "qmv_probe.hip", "qmv_rotary.hip", "qmv_kv.hip", "qmv_attention.hip",
-           "qmv_attention_decode.hip", "qmv_attention_api.hip"]
+           "qmv_attention_decode.hip", "qmv_attention_prompt.hip", "qmv_attention_api.hip"]
 ARCH = "gfx950"
 
 HIPCC = shutil.which("hipcc") or "/opt/rocm/bin/hipcc"

@@ -129,7 +129,7 @@ size_t attention_workspace_bytes(const KVCache &c, const KVBatch &kb, int q_head
   const int64_t rows = (int64_t)kb.max_q * (q_heads / c.heads);
   if (rows <= 16 && decode_eligible(c, (int)rows))
     return decode_workspace_bytes(c, kb, (int)rows, max_kv, window);
-  return 0;
+  return prompt_eligible(c) ? prompt_workspace_bytes(c, kb, q_heads, max_kv, window) : 0;
 }
 
 hipError_t launch_attention(const KVCache &c, int dt, int qt, const KVBatch &kb, const Heads &q,
@@ -139,7 +139,7 @@ hipError_t launch_attention(const KVCache &c, int dt, int qt, const KVBatch &kb,
                    (int)std::min<int64_t>(window, INT32_MAX), causal, qt};
   const int64_t rows = (int64_t)kb.max_q * a.group;
   if (rows <= 16 && decode_eligible(c, (int)rows)) return launch_attention_decode(a, dt, ws, st);
-  return launch_attention_rows(a, dt, st);
+  return prompt_eligible(c) ? launch_attention_prompt(a, dt, ws, st) : launch_attention_rows(a, dt, st);
 }
 
 }  // namespace qmv

@@ -215,5 +215,9 @@ hipError_t launch_attention_rows(const AttnArgs &a, int dt, hipStream_t st);
 bool decode_eligible(const KVCache &c, int rows);
 size_t decode_workspace_bytes(const KVCache &c, const KVBatch &kb, int rows, int64_t max_kv, int64_t window);
 hipError_t launch_attention_decode(const AttnArgs &a, int dt, void *ws, hipStream_t st);
+// Any number of query rows.
+bool prompt_eligible(const KVCache &c);
+size_t prompt_workspace_bytes(const KVCache &c, const KVBatch &kb, int q_heads, int64_t max_kv, int64_t window);
+hipError_t launch_attention_prompt(const AttnArgs &a, int dt, void *ws, hipStream_t st);
 
 }  // namespace qmv
