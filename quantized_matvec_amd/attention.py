@@ -25,7 +25,7 @@ from typing import Optional
 
 import torch
 
-from .qmv import _DT, _QT, _check, _stream, lib as _lib
+from .qmv import _DT, _QT, _check, _stream as _stream_of, lib as _lib
 
 __all__ = ["KVCache4bit", "attention_4bit", "kv_append_4bit", "kv_dequantize_4bit",
            "rope_frequencies", "rope_table", "rotary", "rotary_backward"]
@@ -82,52 +82,66 @@ def lib() -> ctypes.CDLL:
 
 # --------------------------------------------------------------------------
 # operands
+#
+# A decode step is a handful of calls on small tensors, where the host decides:
+# each attribute of a tensor is asked for once, and a descriptor is made from it.
 # --------------------------------------------------------------------------
-def _rows(t: torch.Tensor, name: str, dtype=None, shape=None) -> torch.Tensor:
-    """A GPU tensor [tokens, heads, head_dim] that the kernels take as it is:
-    unit stride in head_dim, the others multiples of 16 bytes (a copy where
-    they are not)."""
+_SIZE = {torch.float32: 4, torch.float16: 2, torch.bfloat16: 2}
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_ref = ctypes.byref
+
+
+def _stream(t: torch.Tensor) -> int:
+    return _stream_of(t) if _raw_stream is None else _raw_stream(t.get_device())
+
+
+def _rows(t: torch.Tensor, name: str, dtype=None):
+    """A GPU tensor [tokens, heads, head_dim] as the kernels take it (unit
+    stride in head_dim, the others multiples of 16 bytes; a copy where they are
+    not), and its descriptor."""
     if not t.is_cuda:
         raise ValueError(f"{name} must be a GPU tensor")
-    if t.dim() != 3:
-        raise ValueError(f"{name} must be [tokens, heads, head_dim], got {tuple(t.shape)}")
-    if dtype is not None and t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
-    if not _fits(t):
+    shape = t.shape
+    if len(shape) != 3:
+        raise ValueError(f"{name} must be [tokens, heads, head_dim], got {tuple(shape)}")
+    dt = t.dtype
+    if dtype is not None and dt != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {dt}")
+    if dt not in _SIZE:
+        raise ValueError(f"{name} must be fp32, fp16 or bf16, got {dt}")
+    ts, hs, es = t.stride()
+    p = t.data_ptr()
+    if es != 1 or (((ts | hs) * _SIZE[dt]) | p) & 15:
         t = t.contiguous()
         if t.data_ptr() % 16:
             t = t.clone()
-    return t
+        ts, hs, _ = t.stride()
+        p = t.data_ptr()
+    return t, _Heads(p, ts, hs, shape[1])
 
 
-def _fits(t: torch.Tensor) -> bool:
-    ts, hs, es = t.stride()
-    size = t.element_size()
-    return es == 1 and ts * size % 16 == 0 and hs * size % 16 == 0 and t.data_ptr() % 16 == 0 \
-        and (ts > 0 or t.shape[0] == 1) and (hs > 0 or t.shape[1] == 1)
-
-
-def _out(t: Optional[torch.Tensor], like: torch.Tensor, name: str) -> torch.Tensor:
+def _out(t: Optional[torch.Tensor], like: torch.Tensor, name: str):
+    """The output tensor (a new one for None) and its descriptor."""
+    shape = like.shape
     if t is None:
-        return torch.empty(like.shape, dtype=like.dtype, device=like.device)
-    if t.shape != like.shape or t.dtype != like.dtype or t.device != like.device or not _fits(t):
+        t = torch.empty_like(like, memory_format=torch.contiguous_format)
+        return t, _Heads(t.data_ptr(), shape[1] * shape[2], shape[2], shape[1])
+    ts, hs, es = t.stride() if t.dim() == 3 else (0, 0, 0)
+    p = t.data_ptr()
+    if t.shape != shape or t.dtype != like.dtype or t.device != like.device or es != 1 or \
+            (((ts | hs) * _SIZE[t.dtype]) | p) & 15 or (ts == 0 and shape[0] > 1) or (hs == 0 and shape[1] > 1):
         raise ValueError(f"{name} must have the shape, type and device of its input, unit stride in "
                          "head_dim and 16-byte aligned rows")
-    return t
-
-
-def _heads(t: torch.Tensor) -> _Heads:
-    return _Heads(t.data_ptr(), t.stride(0), t.stride(1), t.shape[1])
+    return t, _Heads(p, ts, hs, shape[1])
 
 
 def _rope(table: torch.Tensor, interleaved: bool, device) -> _Rope:
-    if table.dim() != 3 or table.shape[2] != 2 or table.dtype != torch.float32 or \
+    shape = table.shape
+    if len(shape) != 3 or shape[2] != 2 or table.dtype != torch.float32 or \
             not table.is_contiguous() or table.device != device:
         raise ValueError("table must be a contiguous fp32 [max_pos, rot_dim / 2, 2] tensor on the "
                          "operands' device")
-    return _Rope(table.data_ptr(), table.shape[0], 2 * table.shape[1], int(interleaved))
+    return _Rope(table.data_ptr(), shape[0], 2 * shape[1], int(interleaved))
 
 
 class KVCache4bit:
@@ -185,10 +199,13 @@ class KVCache4bit:
 
 def _batch(cache: KVCache4bit, block_table, kv_len, cu_q, max_q, tokens: int) -> _Batch:
     dev = cache.device
-    if block_table.dim() != 2 or block_table.dtype != torch.int32 or block_table.device != dev or \
-            block_table.stride(1) != 1:
+    shape = block_table.shape
+    if len(shape) != 2 or block_table.dtype != torch.int32 or block_table.device != dev:
         raise ValueError("block_table must be int32 [batch, max_pages] with unit stride, on the cache's device")
-    n, pages = block_table.shape
+    n, pages = shape
+    stride, unit = block_table.stride()
+    if unit != 1 and pages > 1:
+        raise ValueError("block_table must have unit stride along its pages")
     if kv_len.shape != (n,) or kv_len.dtype != torch.int32 or kv_len.device != dev or not kv_len.is_contiguous():
         raise ValueError(f"kv_len must be contiguous int32 [{n}] on the cache's device")
     cu = None
@@ -201,7 +218,7 @@ def _batch(cache: KVCache4bit, block_table, kv_len, cu_q, max_q, tokens: int) ->
             raise ValueError(f"cu_q must be contiguous int32 [{n + 1}] on the cache's device")
         cu = cu_q.data_ptr()
         max_q = tokens if max_q is None else max_q
-    return _Batch(block_table.data_ptr(), block_table.stride(0), kv_len.data_ptr(), cu, n, pages, max_q)
+    return _Batch(block_table.data_ptr(), stride, kv_len.data_ptr(), cu, n, pages, max_q)
 
 
 # --------------------------------------------------------------------------
@@ -232,26 +249,26 @@ def rope_table(freqs, max_pos: int, gain: float = 1.0, device="cuda") -> torch.T
 
 
 def _rotary(q, k, table, positions, interleaved, q_out, k_out, inverse, name):
-    q = _rows(q, "q")
-    if q.dtype not in _DT:
-        raise ValueError(f"q must be fp32, fp16 or bf16, got {q.dtype}")
+    q, hq = _rows(q, "q")
     tokens, _, dim = q.shape
-    q_out = _out(q_out, q, "q_out")
+    dev = q.device
+    q_out, hqo = _out(q_out, q, "q_out")
     hk = hko = None
     if k is not None:
-        k = _rows(k, "k", q.dtype)
-        if k.shape[0] != tokens or k.shape[2] != dim or k.device != q.device:
+        k, hk = _rows(k, "k", q.dtype)
+        if k.shape[0] != tokens or k.shape[2] != dim or k.device != dev:
             raise ValueError("k must have the tokens, head_dim and device of q")
-        k_out = _out(k_out, k, "k_out")
-        hk, hko = ctypes.byref(_heads(k)), ctypes.byref(_heads(k_out))
-    if positions.shape != (tokens,) or positions.dtype != torch.int64 or positions.device != q.device \
+        k_out, hko = _out(k_out, k, "k_out")
+        hk, hko = _ref(hk), _ref(hko)
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    if positions.shape != (tokens,) or positions.dtype != torch.int64 or positions.device != dev \
             or not positions.is_contiguous():
         raise ValueError(f"positions must be contiguous int64 [{tokens}] on the operands' device")
-    rope = _rope(table, interleaved, q.device)
+    rope = _rope(table, interleaved, dev)
     if tokens:
-        _check(lib().qmv_rotary(ctypes.byref(_heads(q)), ctypes.byref(_heads(q_out)), hk, hko, _DT[q.dtype],
-                                tokens, dim, positions.data_ptr(), ctypes.byref(rope), inverse, _stream(q)),
-               name)
+        _check(lib().qmv_rotary(_ref(hq), _ref(hqo), hk, hko, _DT[q.dtype], tokens, dim, positions.data_ptr(),
+                                _ref(rope), inverse, _stream(q)), name)
     return q_out, k_out
 
 
@@ -281,29 +298,27 @@ def kv_append_4bit(cache: KVCache4bit, k: torch.Tensor, v: torch.Tensor, block_t
     """Writes the new tokens' keys and values [tokens, heads, head_dim] into
     the cache, the keys turned by their positions when ``table`` is given.
     With ``q`` the queries are turned in the same launch and returned."""
-    k = _rows(k, "k", cache.dtype)
+    dev = cache.device
+    k, hk = _rows(k, "k", cache.dtype)
+    v, hv = _rows(v, "v", cache.dtype)
     tokens = k.shape[0]
-    if k.shape[1:] != (cache.heads, cache.head_dim) or k.device != cache.device:
-        raise ValueError(f"k must be [tokens, {cache.heads}, {cache.head_dim}] on the cache's device")
-    v = _rows(v, "v", cache.dtype, k.shape)
-    if v.device != cache.device:
-        raise ValueError("v must be on the cache's device")
+    if k.shape[1:] != (cache.heads, cache.head_dim) or k.shape != v.shape or k.device != dev or v.device != dev:
+        raise ValueError(f"k and v must be [tokens, {cache.heads}, {cache.head_dim}] on the cache's device")
     kb = _batch(cache, block_table, kv_len, cu_q, max_q, tokens)
-    rope = None if table is None else ctypes.byref(_rope(table, interleaved, cache.device))
+    rope = None if table is None else _ref(_rope(table, interleaved, dev))
     hq = hqo = None
     if q is not None:
         if table is None:
             raise ValueError("q is turned by the table: give both or neither")
-        q = _rows(q, "q", cache.dtype)
-        if q.shape[0] != tokens or q.shape[2] != cache.head_dim or q.device != cache.device:
+        q, hq = _rows(q, "q", cache.dtype)
+        if q.shape[0] != tokens or q.shape[2] != cache.head_dim or q.device != dev:
             raise ValueError("q must have the tokens, head_dim and device of k")
-        q_out = _out(q_out, q, "q_out")
-        hq, hqo = ctypes.byref(_heads(q)), ctypes.byref(_heads(q_out))
+        q_out, hqo = _out(q_out, q, "q_out")
+        hq, hqo = _ref(hq), _ref(hqo)
     elif q_out is not None:
         raise ValueError("q_out without q")
     if tokens:
-        _check(lib().qmv_kv_append_4bit(ctypes.byref(cache._c), ctypes.byref(kb), tokens,
-                                        ctypes.byref(_heads(k)), ctypes.byref(_heads(v)), rope, hq, hqo,
+        _check(lib().qmv_kv_append_4bit(_ref(cache._c), _ref(kb), tokens, _ref(hk), _ref(hv), rope, hq, hqo,
                                         _stream(k)), "kv_append_4bit")
     return q_out
 
@@ -314,17 +329,16 @@ def kv_dequantize_4bit(cache: KVCache4bit, block_table: torch.Tensor, kv_len: to
     """The last tokens of each sequence (one each, or by ``cu_q``) as the
     cache holds them: (k, v), each [tokens, heads, head_dim]."""
     kb = _batch(cache, block_table, kv_len, cu_q, max_q, tokens)
-    like = torch.empty((tokens, cache.heads, cache.head_dim), dtype=cache.dtype, device=cache.device) \
-        if k_out is None else k_out
-    if like.shape != (tokens, cache.heads, cache.head_dim) or like.dtype != cache.dtype or \
-            like.device != cache.device:
+    shape = (tokens, cache.heads, cache.head_dim)
+    if k_out is None:
+        k_out = torch.empty(shape, dtype=cache.dtype, device=cache.device)
+    elif k_out.shape != shape or k_out.dtype != cache.dtype or k_out.device != cache.device:
         raise ValueError("k_out must be [tokens, heads, head_dim] of the cache's type and device")
-    k_out = _out(like, like, "k_out")
-    v_out = _out(v_out, k_out, "v_out")
+    k_out, hk = _out(k_out, k_out, "k_out")
+    v_out, hv = _out(v_out, k_out, "v_out")
     if tokens:
-        _check(lib().qmv_kv_dequantize_4bit(ctypes.byref(cache._c), ctypes.byref(kb), tokens,
-                                            ctypes.byref(_heads(k_out)), ctypes.byref(_heads(v_out)),
-                                            _stream(k_out)), "kv_dequantize_4bit")
+        _check(lib().qmv_kv_dequantize_4bit(_ref(cache._c), _ref(kb), tokens, _ref(hk), _ref(hv), _stream(k_out)),
+               "kv_dequantize_4bit")
     return k_out, v_out
 
 
@@ -356,21 +370,20 @@ def attention_4bit(q: torch.Tensor, cache: KVCache4bit, block_table: torch.Tenso
     h / (q_heads / heads)).  ``scale`` defaults to head_dim ** -0.5, ``max_kv``
     is a host-side upper bound of kv_len, ``window`` > 0 keeps the last
     ``window`` keys of each token.  A token that sees no key gets zeros."""
-    q = _rows(q, "q", cache.dtype)
-    tokens, hq, dim = q.shape
-    if dim != cache.head_dim or hq == 0 or hq % cache.heads or q.device != cache.device:
+    q, hq = _rows(q, "q", cache.dtype)
+    tokens, heads, dim = q.shape
+    if dim != cache.head_dim or heads == 0 or heads % cache.heads or q.device != cache.device:
         raise ValueError(f"q must be [tokens, a multiple of {cache.heads}, {cache.head_dim}] on the cache's device")
-    out = _out(out, q, "out")
+    out, ho = _out(out, q, "out")
     kb = _batch(cache, block_table, kv_len, cu_q, max_q, tokens)
     if tokens == 0:
         return out
     L = lib()
-    cache_p, kb_p, st = ctypes.byref(cache._c), ctypes.byref(kb), _stream(q)
+    cache_p, kb_p, st = _ref(cache._c), _ref(kb), _stream(q)
     max_kv = 0 if max_kv is None else max(int(max_kv), 1)
-    n = L.qmv_attention_4bit_workspace(cache_p, kb_p, tokens, hq, max_kv, window)
+    n = L.qmv_attention_4bit_workspace(cache_p, kb_p, tokens, heads, max_kv, window)
     ws = _workspace(n, q.device, st)
-    _check(L.qmv_attention_4bit(ctypes.byref(_heads(q)), cache_p, kb_p, tokens, max_kv,
-                                dim ** -0.5 if scale is None else scale, int(causal), window,
-                                ctypes.byref(_heads(out)), ws.data_ptr() if ws is not None else None,
-                                ws.numel() if ws is not None else 0, st), "attention_4bit")
+    _check(L.qmv_attention_4bit(_ref(hq), cache_p, kb_p, tokens, max_kv, dim ** -0.5 if scale is None else scale,
+                                int(causal), window, _ref(ho), None if ws is None else ws.data_ptr(), n, st),
+           "attention_4bit")
     return out
