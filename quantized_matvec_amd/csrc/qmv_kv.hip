@@ -42,8 +42,7 @@ __device__ __forceinline__ uint32_t nearest_code(float x, const float (&thr)[15]
 }
 
 template <int DT>
-__device__ __forceinline__ void load8(const uint16_t *p, float (&x)[8]) {
-  const uint4 w = *reinterpret_cast<const uint4 *>(p);
+__device__ __forceinline__ void unpack8(const uint4 &w, float (&x)[8]) {
   const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -52,55 +51,101 @@ __device__ __forceinline__ void load8(const uint16_t *p, float (&x)[8]) {
   }
 }
 
-// Elements e0 .. e0 + 7 of a row turned by the table row cs (half pairs), or
-// zeros where there is no table row.
+// The rotation of elements e0 .. e0 + 7 of a token's rows: the angles are
+// fetched once.  An element e of the rotated part becomes
+// x_e c + sign x_partner s, sign -1 for the first of a pair (rounded as
+// x c - partner s, since negation is exact).
 template <int DT>
-__device__ __forceinline__ void turn8(const uint16_t *row, int e0, const Rope &rope, int64_t pos,
-                                      float (&x)[8]) {
-  if (pos < 0 || pos >= rope.max_pos) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = 0.f;
-    return;
-  }
-  const float2 *cs = rope.table + pos * rope.half;
-  const int half = rope.half;
-  if (rope.interleaved) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int p = (e0 >> 1) + i;
-      if (p < half) {
-        const float2 v = cs[p];
-        const float a = x[2 * i], b = x[2 * i + 1];
-        x[2 * i] = a * v.x - b * v.y;
-        x[2 * i + 1] = b * v.x + a * v.y;
-      }
-    }
-  } else if (e0 < 2 * half) {
-    float y[8];
-    const bool whole = half % 8 == 0;  // the run's partners are one aligned run
-    if (whole) load8<DT>(row + (e0 < half ? e0 + half : e0 - half), y);
+struct Turn {
+  float c[8], s[8];  // cos, and sin with the sign
+  uint32_t turned;   // bit i: element e0 + i is of the rotated part
+  int off;           // partner run's distance (halves), 0: pairs inside the run or no whole run
+  int first;         // halves without a whole run: e0, else -1
+  int half;
+  bool zero;         // no such position in the table: zeros
+  bool inter, any;
+
+  __device__ __forceinline__ void load(const Rope &rope, int e0, int64_t pos) {
+    half = rope.half;
+    inter = rope.interleaved;
+    any = rope.table != nullptr && e0 < 2 * half;
+    zero = rope.table != nullptr && (pos < 0 || pos >= rope.max_pos);
+    off = 0;
+    first = -1;
+    turned = 0;
+    if (!any || zero) return;
+    const float2 *cs = rope.table + pos * half;
+    const bool whole = half % 8 == 0;  // a run's partners are one aligned run
+    if (!inter && whole) off = e0 < half ? half : -half;
+    if (!inter && !whole) first = e0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int e = e0 + i;
-      if (e >= 2 * half) continue;
-      const bool first = e < half;
-      const float o = whole ? y[i] : bits16_to_f32<DT>(row[first ? e + half : e - half]);
-      const float2 v = cs[first ? e : e - half];
-      x[i] = first ? x[i] * v.x - o * v.y : x[i] * v.x + o * v.y;
+      const bool in = e < 2 * half;
+      const bool lead = inter ? (e & 1) == 0 : e < half;
+      const int p = inter ? e >> 1 : (lead ? e : e - half);
+      const float2 v = cs[in ? p : 0];
+      c[i] = v.x;
+      s[i] = lead ? -v.y : v.y;
+      turned |= in ? 1u << i : 0u;
     }
   }
-}
+  // The run that holds the partners (p: this run); itself where there is none.
+  __device__ __forceinline__ uint4 partner(const uint16_t *p) const {
+    return *reinterpret_cast<const uint4 *>(p + off);
+  }
+  __device__ __forceinline__ void apply(const uint16_t *p, const uint4 &other, float (&x)[8]) const {
+    if (zero) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = 0.f;
+      return;
+    }
+    if (!any) return;
+    float y[8];
+    if (inter) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] = x[i ^ 1];
+    } else if (first < 0) {
+      unpack8<DT>(other, y);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int e = first + i;
+        y[i] = e < 2 * half ? bits16_to_f32<DT>(p[i + (e < half ? half : -half)]) : 0.f;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float r = x[i] * c[i] + y[i] * s[i];
+      x[i] = turned >> i & 1u ? r : x[i];
+    }
+  }
+};
 
-// Token of the sequence (and row h of it) that this thread's LPR lanes take:
-// rows are numbered through over the tokens, in 64 bits.
-template <int LPR>
-__device__ __forceinline__ int unit_token(int rows, int &h) {
-  const int64_t first = (int64_t)blockIdx.x * (256 / LPR);
-  const int64_t i0 = first / rows;
-  const uint32_t u = (uint32_t)(first - i0 * rows) + threadIdx.x / LPR;
-  h = (int)(u % (uint32_t)rows);
-  return (int)(i0 + u / (uint32_t)rows);
-}
+// What a thread works on.  A row takes LPR lanes of a wave, 8 elements each; a
+// workgroup has 256 / LPR rows at a time: TG tokens side by side for each of
+// HS rows h, and goes through `iters` such sets of rows, so that positions,
+// pages and angles are fetched once and the next row's elements while this
+// one is worked on.  With TG = 1 (few tokens) the rows of one token fill the
+// workgroup; otherwise TG places of one group of 16 cache positions do, and
+// one workgroup writes all bytes of a value group and of a group's scales.
+template <int LPR, int TG>
+struct Place {
+  static constexpr int RPW = 256 / LPR, HS = RPW / TG;
+  int i;   // token of the sequence, or negative: none
+  int h;   // the first row h; further ones HS apart
+  int end; // rows of this workgroup end before
+  __device__ __forceinline__ Place(int rows, int iters, const SeqRange &s, int most) {
+    const int blocks = (rows + HS * iters - 1) / (HS * iters);  // along the rows of a token
+    const int group = (int)(blockIdx.x / (unsigned)blocks), block = (int)(blockIdx.x - (unsigned)group * blocks);
+    const int slot = threadIdx.x / LPR;
+    h = block * HS * iters + slot / TG;
+    end = (block + 1) * HS * iters < rows ? (block + 1) * HS * iters : rows;
+    const int64_t place = (int64_t)group * TG + slot % TG;
+    const int64_t t = place - (s.pos0 & (TG - 1));
+    i = t >= 0 && t < s.n && t < most ? (int)t : -1;
+  }
+};
 
 struct AppendArgs {
   KVCache c;
@@ -110,92 +155,135 @@ struct AppendArgs {
   Mids32 mids;
 };
 
-// A row takes LPR lanes of a wave, 8 elements each (the first head_dim / 8
-// lanes hold some); rows of a token: its queries, its keys, its values.
-template <int DT, int QT, int LPR>
-__global__ __launch_bounds__(256) void kv_append_kernel(AppendArgs a) {
+// blockIdx.z: what a workgroup takes, so that its loop over rows is one code
+// for all its waves.
+enum : int { kQueries = 0, kKeys = 1, kValues = 2 };
+
+template <int DT, int QT, int LPR, int TG, int WHAT>
+__device__ __forceinline__ void append_rows(const AppendArgs &a, int iters) {
+  using P = Place<LPR, TG>;
   const int b = blockIdx.y;
   const SeqRange s = seq_range(a.kb, b);
-  const int rows = a.q.heads + 2 * a.c.heads;
-  int h;
-  const int i = unit_token<LPR>(rows, h);
-  if (i >= s.n || i >= a.kb.max_q) return;
-  const int l = threadIdx.x % LPR;
-  const int e0 = 8 * l;
-  const int pos = s.pos0 + i;
-  const int64_t t = s.row0 + i;
-  const bool isq = h < a.q.heads;
-  if (!isq) h -= a.q.heads;
-  const bool isv = !isq && h >= a.c.heads;
-  if (isv) h -= a.c.heads;
-  const Heads &src = isq ? a.q : (isv ? a.v : a.k);
-  const uint16_t *row = static_cast<const uint16_t *>(src.p) + t * src.ts + h * src.hs;
+  const Heads &src = WHAT == kQueries ? a.q : (WHAT == kKeys ? a.k : a.v);
+  const P pl(src.heads, iters, s, a.kb.max_q);
+  const int e0 = 8 * (int)(threadIdx.x % LPR);
+  if (pl.i < 0 || pl.h >= pl.end) return;
+  const int pos = s.pos0 + pl.i;
+  const int64_t t = s.row0 + pl.i;
   const bool mine = e0 < a.c.dim;
-
-  float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  if (mine) {
-    load8<DT>(row + e0, x);
-    if (!isv && a.rope.table) turn8<DT>(row, e0, a.rope, pos, x);
+  int64_t page = 0;
+  if constexpr (WHAT != kQueries) {
+    page = page_of(a.kb, a.c, b, pos);
+    if (page < 0) return;  // the same for the whole row
   }
-  uint32_t w[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) w[j] = cvt_pair<DT>(x[2 * j], x[2 * j + 1]);
-  if (isq) {
-    if (mine)
-      *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.qo.p) + t * a.qo.ts + h * a.qo.hs + e0) =
-          make_uint4(w[0], w[1], w[2], w[3]);
-    return;
-  }
-  const int64_t page = page_of(a.kb, a.c, b, pos);
-  if (page < 0) return;  // the same for the whole row
-  float m = 0.f;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {  // what is quantized: the row as the cache's type holds it
-    x[2 * j] = bits16_to_f32<DT>(w[j] & 0xffffu);
-    x[2 * j + 1] = bits16_to_f32<DT>(w[j] >> 16);
-    m = fmaxf(m, fmaxf(fabsf(x[2 * j]), fabsf(x[2 * j + 1])));
-  }
-  m = group_max(m, a.c.bs >> 3);
-  const float up = m < 0x1p-100f ? 0x1p100f : 1.f;
-  float thr[15];
-#pragma unroll
-  for (int j = 0; j < 15; ++j) thr[j] = (m * up) * a.mids.m[j];
-  uint32_t word = 0;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const uint32_t code = nearest_code<QT>(x[j] * up, thr);
-    word |= code << (8 * (j >> 1) + (j & 1 ? 0 : 4));  // even element: high nibble
-  }
-  if (!mine) return;
   const int at = pos & ((1 << a.c.log2page) - 1);
-  const int64_t cb = code_base(a.c, page, h);
-  if (isv) {
-    uint8_t *dst = a.c.vc + cb + (int64_t)(at >> 4) * a.c.dim * 8 + (e0 >> 1) * 16 + (at & 15);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) dst[16 * j] = (uint8_t)(word >> (8 * j));
+  const uint16_t *in = static_cast<const uint16_t *>(src.p) + t * src.ts + pl.h * src.hs + (mine ? e0 : 0);
+  Turn<DT> turn;
+  if constexpr (WHAT != kValues) turn.load(a.rope, e0, pos);
+  uint16_t *out = nullptr;  // queries
+  uint8_t *codes = nullptr;
+  uint16_t *scales = nullptr;
+  const int64_t head_bytes = (int64_t)(a.c.dim >> 1) << a.c.log2page, head_scales = (int64_t)(a.c.dim / a.c.bs) << a.c.log2page;
+  if constexpr (WHAT == kQueries) {
+    out = static_cast<uint16_t *>(a.qo.p) + t * a.qo.ts + pl.h * a.qo.hs + e0;
   } else {
-    *reinterpret_cast<uint32_t *>(a.c.kc + cb + (int64_t)at * (a.c.dim >> 1) + (e0 >> 1)) = word;
+    const int64_t first = page * a.c.heads + pl.h;
+    codes = (WHAT == kValues ? a.c.vc + (int64_t)(at >> 4) * a.c.dim * 8 + (e0 >> 1) * 16 + (at & 15)
+                             : a.c.kc + (int64_t)at * (a.c.dim >> 1) + (e0 >> 1)) + first * head_bytes;
+    scales = (WHAT == kValues ? a.c.vs : a.c.ks) + first * head_scales + ((int64_t)(e0 / a.c.bs) << a.c.log2page) + at;
   }
-  if ((e0 & (a.c.bs - 1)) == 0) {
-    uint16_t *sc = isv ? a.c.vs : a.c.ks;
-    sc[scale_base(a.c, page, h) + ((int64_t)(e0 / a.c.bs) << a.c.log2page) + at] =
-        (uint16_t)f32_to_bits16<DT>(m);
+#pragma unroll WHAT == kQueries ? 4 : 2
+  for (int h = pl.h; h < pl.end; h += P::HS) {
+    const uint4 raw = *reinterpret_cast<const uint4 *>(in);
+    float x[8];
+    unpack8<DT>(raw, x);
+    if constexpr (WHAT != kValues) turn.apply(in, turn.partner(in), x);
+    in += P::HS * src.hs;
+    uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+    if constexpr (WHAT != kValues) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w[j] = cvt_pair<DT>(x[2 * j], x[2 * j + 1]);
+    }
+    if constexpr (WHAT == kQueries) {
+      if (mine) *reinterpret_cast<uint4 *>(out) = make_uint4(w[0], w[1], w[2], w[3]);
+      out += P::HS * a.qo.hs;
+    } else {
+      float m = 0.f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {  // what is quantized: the row as the cache's type holds it
+        x[2 * j] = bits16_to_f32<DT>(w[j] & 0xffffu);
+        x[2 * j + 1] = bits16_to_f32<DT>(w[j] >> 16);
+        m = fmaxf(m, fmaxf(fabsf(x[2 * j]), fabsf(x[2 * j + 1])));
+      }
+      m = group_max(m, a.c.bs >> 3);  // (lanes past the row's end repeat its first run, in blocks of their own)
+      const float up = m < 0x1p-100f ? 0x1p100f : 1.f;
+      float thr[15];
+#pragma unroll
+      for (int j = 0; j < 15; ++j) thr[j] = (m * up) * a.mids.m[j];
+      uint32_t word = 0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const uint32_t code = nearest_code<QT>(x[j] * up, thr);
+        word |= code << (8 * (j >> 1) + (j & 1 ? 0 : 4));  // even element: high nibble
+      }
+      if (mine) {
+        if constexpr (WHAT == kValues) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) codes[16 * j] = (uint8_t)(word >> (8 * j));
+        } else {
+          *reinterpret_cast<uint32_t *>(codes) = word;
+        }
+        if ((e0 & (a.c.bs - 1)) == 0) *scales = (uint16_t)f32_to_bits16<DT>(m);
+      }
+      codes += P::HS * head_bytes;
+      scales += P::HS * head_scales;
+    }
   }
+}
+
+template <int DT, int QT, int LPR, int TG>
+__global__ __launch_bounds__(256) void kv_append_kernel(AppendArgs a, int q_iters, int kv_iters) {
+  if (blockIdx.z == kKeys) append_rows<DT, QT, LPR, TG, kKeys>(a, kv_iters);
+  else if (blockIdx.z == kValues) append_rows<DT, QT, LPR, TG, kValues>(a, kv_iters);
+  else if (a.q.heads) append_rows<DT, QT, LPR, TG, kQueries>(a, q_iters);
 }
 
 // Lanes of a row: head_dim / 8 rounded up to a power of two.
 static int row_lanes(int dim) { return dim <= 32 ? 4 : dim <= 64 ? 8 : dim <= 128 ? 16 : 32; }
 
+// Calls with fewer new tokens of a sequence take them one by one.
+constexpr int kGroupFrom = 8;
+
+// Grid and sets of rows of a workgroup: as many sets (up to 16) as leave 8
+// workgroups for each compute unit.
+template <int LPR, int TG>
+static unsigned append_grid(const KVBatch &kb, int rows, int *iters) {
+  constexpr int HS = 256 / LPR / TG;
+  const int64_t groups = ((int64_t)kb.max_q + 2 * (TG - 1)) / TG;  // a group may begin TG - 1 places early
+  const int64_t sets = (rows + HS - 1) / HS;
+  *iters = (int)std::min<int64_t>(std::max<int64_t>(groups * kb.batch * sets * 3 / (8 * device_cu_count()), 1),
+                                  std::min<int64_t>(sets, 16));
+  return (unsigned)(groups * ((rows + HS * *iters - 1) / (HS * *iters)));
+}
+
+template <int DT, int QT, int LPR, int TG>
+static void launch_append_g(const AppendArgs &a, hipStream_t st) {
+  int q_iters = 1, kv_iters;
+  unsigned x = append_grid<LPR, TG>(a.kb, a.c.heads, &kv_iters);
+  if (a.q.heads) x = std::max(x, append_grid<LPR, TG>(a.kb, a.q.heads, &q_iters));
+  // workgroups past a part's own grid find no token
+  const dim3 grid(x, (unsigned)a.kb.batch, 3);
+  hipLaunchKernelGGL((kv_append_kernel<DT, QT, LPR, TG>), grid, dim3(256), 0, st, a, q_iters, kv_iters);
+}
+
 template <int DT, int QT>
 static void launch_append_t(const AppendArgs &a, hipStream_t st) {
-  const int lpr = row_lanes(a.c.dim);
-  const int64_t units = (int64_t)a.kb.max_q * (a.q.heads + 2 * a.c.heads);
-  const dim3 grid((unsigned)((units * lpr + 255) / 256), (unsigned)a.kb.batch);
-  switch (lpr) {
-    case 4: hipLaunchKernelGGL((kv_append_kernel<DT, QT, 4>), grid, dim3(256), 0, st, a); break;
-    case 8: hipLaunchKernelGGL((kv_append_kernel<DT, QT, 8>), grid, dim3(256), 0, st, a); break;
-    case 16: hipLaunchKernelGGL((kv_append_kernel<DT, QT, 16>), grid, dim3(256), 0, st, a); break;
-    default: hipLaunchKernelGGL((kv_append_kernel<DT, QT, 32>), grid, dim3(256), 0, st, a);
+  const bool few = a.kb.max_q < kGroupFrom;
+  switch (row_lanes(a.c.dim)) {
+    case 4: few ? launch_append_g<DT, QT, 4, 1>(a, st) : launch_append_g<DT, QT, 4, 16>(a, st); break;
+    case 8: few ? launch_append_g<DT, QT, 8, 1>(a, st) : launch_append_g<DT, QT, 8, 16>(a, st); break;
+    case 16: few ? launch_append_g<DT, QT, 16, 1>(a, st) : launch_append_g<DT, QT, 16, 16>(a, st); break;
+    default: few ? launch_append_g<DT, QT, 32, 1>(a, st) : launch_append_g<DT, QT, 32, 8>(a, st);
   }
 }
 
@@ -223,8 +311,9 @@ struct ReadArgs {
   Heads k, v;
 };
 
-template <int DT, int LPR>
-__global__ __launch_bounds__(256) void kv_dequantize_kernel(ReadArgs a, int qt) {
+template <int DT, int LPR, int TG>
+__global__ __launch_bounds__(256) void kv_dequantize_kernel(ReadArgs a, int qt, int iters) {
+  using P = Place<LPR, TG>;
   __shared__ float2 lut[256];  // packed byte -> (T[byte >> 4], T[byte & 15])
   {
     const uint32_t *tb = table_bits(qt);
@@ -234,51 +323,56 @@ __global__ __launch_bounds__(256) void kv_dequantize_kernel(ReadArgs a, int qt) 
   __syncthreads();
   const int b = blockIdx.y;
   const SeqRange s = seq_range(a.kb, b);
-  const int rows = 2 * a.c.heads;
-  int h;
-  const int i = unit_token<LPR>(rows, h);
-  const int e0 = 8 * (threadIdx.x % LPR);
-  if (i >= s.n || i >= a.kb.max_q || e0 >= a.c.dim) return;
-  const bool isv = h >= a.c.heads;
-  if (isv) h -= a.c.heads;
-  const int pos = s.pos0 + i;
+  const bool isv = blockIdx.z != 0;
+  const P pl(a.c.heads, iters, s, a.kb.max_q);
+  const int e0 = 8 * (int)(threadIdx.x % LPR);
+  if (pl.i < 0 || e0 >= a.c.dim || pl.h >= pl.end) return;
+  const int pos = s.pos0 + pl.i;
+  const int64_t t = s.row0 + pl.i;
   const int64_t page = page_of(a.kb, a.c, b, pos);
-  uint32_t out[4] = {0, 0, 0, 0};
-  if (page >= 0) {
-    const int at = pos & ((1 << a.c.log2page) - 1);
-    const int64_t cb = code_base(a.c, page, h);
-    uint32_t word = 0;
-    if (isv) {
-      const uint8_t *src = a.c.vc + cb + (int64_t)(at >> 4) * a.c.dim * 8 + (e0 >> 1) * 16 + (at & 15);
+  const int at = pos & ((1 << a.c.log2page) - 1);
+  const int64_t head_bytes = (int64_t)(a.c.dim >> 1) << a.c.log2page, head_scales = (int64_t)(a.c.dim / a.c.bs) << a.c.log2page;
+  const int64_t first = page < 0 ? 0 : page * a.c.heads + pl.h;
+  const uint8_t *src = (isv ? a.c.vc + (int64_t)(at >> 4) * a.c.dim * 8 + (e0 >> 1) * 16 + (at & 15)
+                            : a.c.kc + (int64_t)at * (a.c.dim >> 1) + (e0 >> 1)) + first * head_bytes;
+  const uint16_t *sc = (isv ? a.c.vs : a.c.ks) + first * head_scales + ((int64_t)(e0 / a.c.bs) << a.c.log2page) + at;
+  const Heads &dst = isv ? a.v : a.k;
+  uint16_t *out = static_cast<uint16_t *>(dst.p) + t * dst.ts + pl.h * dst.hs + e0;
+  const int step = isv ? 16 : 1;  // bytes from one pair of elements to the next
+#pragma unroll 4
+  for (int h = pl.h; h < pl.end; h += P::HS) {
+    uint32_t w[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) word |= (uint32_t)src[16 * j] << (8 * j);
-    } else {
-      word = *reinterpret_cast<const uint32_t *>(a.c.kc + cb + (int64_t)at * (a.c.dim >> 1) + (e0 >> 1));
-    }
-    const uint16_t *sc = isv ? a.c.vs : a.c.ks;
-    const float m = bits16_to_f32<DT>(
-        sc[scale_base(a.c, page, h) + ((int64_t)(e0 / a.c.bs) << a.c.log2page) + at]);
+    for (int j = 0; j < 4; ++j) w[j] = src[j * step];
+    const float m = bits16_to_f32<DT>(sc[0]);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const float2 v = lut[(word >> (8 * j)) & 0xffu];
-      out[j] = cvt_pair<DT>(v.x * m, v.y * m);
+      const float2 v = lut[w[j]];
+      w[j] = page >= 0 ? cvt_pair<DT>(v.x * m, v.y * m) : 0u;
     }
+    *reinterpret_cast<uint4 *>(out) = make_uint4(w[0], w[1], w[2], w[3]);
+    src += P::HS * head_bytes;
+    sc += P::HS * head_scales;
+    out += P::HS * dst.hs;
   }
-  const Heads &dst = isv ? a.v : a.k;
-  *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(dst.p) + (s.row0 + i) * dst.ts + h * dst.hs + e0) =
-      make_uint4(out[0], out[1], out[2], out[3]);
+}
+
+template <int DT, int LPR, int TG>
+static void launch_read_g(const ReadArgs &a, int qt, hipStream_t st) {
+  int iters;
+  const unsigned x = append_grid<LPR, TG>(a.kb, a.c.heads, &iters);
+  const dim3 grid(x, (unsigned)a.kb.batch, 2);  // keys, values
+  hipLaunchKernelGGL((kv_dequantize_kernel<DT, LPR, TG>), grid, dim3(256), 0, st, a, qt, iters);
 }
 
 template <int DT>
 static void launch_read_t(const ReadArgs &a, int qt, hipStream_t st) {
-  const int lpr = row_lanes(a.c.dim);
-  const int64_t units = (int64_t)a.kb.max_q * 2 * a.c.heads;
-  const dim3 grid((unsigned)((units * lpr + 255) / 256), (unsigned)a.kb.batch);
-  switch (lpr) {
-    case 4: hipLaunchKernelGGL((kv_dequantize_kernel<DT, 4>), grid, dim3(256), 0, st, a, qt); break;
-    case 8: hipLaunchKernelGGL((kv_dequantize_kernel<DT, 8>), grid, dim3(256), 0, st, a, qt); break;
-    case 16: hipLaunchKernelGGL((kv_dequantize_kernel<DT, 16>), grid, dim3(256), 0, st, a, qt); break;
-    default: hipLaunchKernelGGL((kv_dequantize_kernel<DT, 32>), grid, dim3(256), 0, st, a, qt);
+  const bool few = a.kb.max_q < kGroupFrom;
+  switch (row_lanes(a.c.dim)) {
+    case 4: few ? launch_read_g<DT, 4, 1>(a, qt, st) : launch_read_g<DT, 4, 16>(a, qt, st); break;
+    case 8: few ? launch_read_g<DT, 8, 1>(a, qt, st) : launch_read_g<DT, 8, 16>(a, qt, st); break;
+    case 16: few ? launch_read_g<DT, 16, 1>(a, qt, st) : launch_read_g<DT, 16, 16>(a, qt, st); break;
+    default: few ? launch_read_g<DT, 32, 1>(a, qt, st) : launch_read_g<DT, 32, 8>(a, qt, st);
   }
 }
 

@@ -114,11 +114,15 @@ struct RotaryArgs {
   const int64_t *positions;
   int64_t tokens;
   int dim;
-  int per_head;  // units of a head
-  int per_token; // units of a token: heads * per_head
+  int per_head;   // units of a head
+  int head_sets;  // threads along the heads of a token
+  int per_token;  // threads of a token: head_sets * per_head
 };
 
-template <int DT, int V, bool INTER>
+// A thread takes the same unit of HP heads of a token (head_sets apart): the
+// position and the angles are fetched once, and HP heads' elements are in
+// flight together.
+template <int DT, int V, bool INTER, int HP>
 __global__ __launch_bounds__(256) void rotary_kernel(RotaryArgs a, float sign) {
   const int64_t base = (int64_t)blockIdx.x * 256;
   const int64_t t0 = base / a.per_token;
@@ -126,13 +130,8 @@ __global__ __launch_bounds__(256) void rotary_kernel(RotaryArgs a, float sign) {
   const int64_t t = t0 + u / (uint32_t)a.per_token;
   if (t >= a.tokens) return;
   const uint32_t w = u % (uint32_t)a.per_token;
-  int h = (int)(w / (uint32_t)a.per_head);
+  const int h0 = (int)(w / (uint32_t)a.per_head);
   const int i = (int)(w % (uint32_t)a.per_head);
-  const bool isk = h >= a.q.heads;
-  if (isk) h -= a.q.heads;
-  const Heads &x = isk ? a.k : a.q;
-  const Heads &y = isk ? a.ko : a.qo;
-  const int64_t xo = t * x.ts + h * x.hs, yo = t * y.ts + h * y.hs;
   const int half = a.rope.half;
   const int64_t pos = a.positions[t];
   const bool there = pos >= 0 && pos < a.rope.max_pos;
@@ -140,53 +139,77 @@ __global__ __launch_bounds__(256) void rotary_kernel(RotaryArgs a, float sign) {
 
   constexpr int NP = INTER ? V / 2 : V;  // pairs of a unit
   const int turned = half / NP;          // units that turn
-  if (i < turned) {
-    float c[NP], s[NP];
+  const bool turns = i < turned;
+  const int at = turns ? i * V : 2 * half + (i - turned) * V;
+  const int at2 = !INTER && turns ? half + i * V : at;  // the run of the pairs' second elements
+  const void *xp[HP];
+  void *yp[HP];
+  int64_t xo[HP], yo[HP];
+  bool real[HP];
 #pragma unroll
-    for (int j = 0; j < NP; ++j) {
-      const float2 v = cs[i * NP + j];
-      c[j] = v.x;
-      s[j] = sign * v.y;
-    }
-    if constexpr (INTER) {
-      float e[V], r[V];
-      load_run<DT, V>(x.p, xo + i * V, e);
+  for (int n = 0; n < HP; ++n) {
+    int h = h0 + n * a.head_sets;
+    real[n] = h < a.q.heads + a.k.heads;
+    h = real[n] ? h : h0;  // one that is there
+    const bool isk = h >= a.q.heads;
+    if (isk) h -= a.q.heads;
+    const Heads &x = isk ? a.k : a.q;
+    const Heads &y = isk ? a.ko : a.qo;
+    xp[n] = x.p, yp[n] = y.p;
+    xo[n] = t * x.ts + h * x.hs;
+    yo[n] = t * y.ts + h * y.hs;
+  }
+  float e[HP][V], f[HP][V];
 #pragma unroll
-      for (int j = 0; j < NP; ++j) {
-        r[2 * j] = there ? e[2 * j] * c[j] - e[2 * j + 1] * s[j] : 0.f;
-        r[2 * j + 1] = there ? e[2 * j + 1] * c[j] + e[2 * j] * s[j] : 0.f;
+  for (int n = 0; n < HP; ++n) {
+    load_run<DT, V>(xp[n], xo[n] + at, e[n]);
+    if constexpr (!INTER) load_run<DT, V>(xp[n], xo[n] + at2, f[n]);
+  }
+  float c[NP], s[NP];
+#pragma unroll
+  for (int j = 0; j < NP; ++j) {
+    const float2 v = cs[turns ? i * NP + j : 0];
+    c[j] = v.x;
+    s[j] = sign * v.y;
+  }
+#pragma unroll
+  for (int n = 0; n < HP; ++n) {
+    if (!real[n]) continue;
+    float r[V], g[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      if constexpr (INTER) {
+        const float o = e[n][j ^ 1];
+        r[j] = j & 1 ? e[n][j] * c[j / 2] + o * s[j / 2] : e[n][j] * c[j / 2] - o * s[j / 2];
+      } else {
+        r[j] = e[n][j] * c[j] - f[n][j] * s[j];
+        g[j] = f[n][j] * c[j] + e[n][j] * s[j];
       }
-      store_run<DT, V>(y.p, yo + i * V, r);
-    } else {
-      float e[V], f[V], r[V], g[V];
-      load_run<DT, V>(x.p, xo + i * V, e);
-      load_run<DT, V>(x.p, xo + half + i * V, f);
-#pragma unroll
-      for (int j = 0; j < V; ++j) {
-        r[j] = there ? e[j] * c[j] - f[j] * s[j] : 0.f;
-        g[j] = there ? f[j] * c[j] + e[j] * s[j] : 0.f;
-      }
-      store_run<DT, V>(y.p, yo + i * V, r);
-      store_run<DT, V>(y.p, yo + half + i * V, g);
     }
-  } else {
-    const int at = 2 * half + (i - turned) * V;
-    float e[V];
-    load_run<DT, V>(x.p, xo + at, e);
 #pragma unroll
-    for (int j = 0; j < V; ++j) e[j] = there ? e[j] : 0.f;
-    store_run<DT, V>(y.p, yo + at, e);
+    for (int j = 0; j < V; ++j) {
+      r[j] = there ? (turns ? r[j] : e[n][j]) : 0.f;
+      if constexpr (!INTER) g[j] = there ? g[j] : 0.f;
+    }
+    store_run<DT, V>(yp[n], yo[n] + at, r);
+    if constexpr (!INTER) {
+      if (turns) store_run<DT, V>(yp[n], yo[n] + at2, g);
+    }
   }
 }
 
 template <int DT, int V, bool INTER>
 static void launch_rotary_t(RotaryArgs &a, float sign, hipStream_t st) {
-  const int half = a.rope.half;
+  constexpr int HP = 4;
+  const int half = a.rope.half, heads = a.q.heads + a.k.heads;
   a.per_head = half / (INTER ? V / 2 : V) + (a.dim - 2 * half) / V;
-  a.per_token = a.per_head * (a.q.heads + a.k.heads);
-  const int64_t units = a.tokens * a.per_token;
-  hipLaunchKernelGGL((rotary_kernel<DT, V, INTER>), dim3((unsigned)((units + 255) / 256)), dim3(256),
-                     0, st, a, sign);
+  // four heads a thread where that leaves 8 workgroups for each compute unit
+  const bool many = a.tokens * a.per_head * heads >= (int64_t)HP * 256 * 8 * device_cu_count() && heads >= HP;
+  a.head_sets = many ? (heads + HP - 1) / HP : heads;
+  a.per_token = a.per_head * a.head_sets;
+  const dim3 grid((unsigned)((a.tokens * a.per_token + 255) / 256));
+  if (many) hipLaunchKernelGGL((rotary_kernel<DT, V, INTER, HP>), grid, dim3(256), 0, st, a, sign);
+  else hipLaunchKernelGGL((rotary_kernel<DT, V, INTER, 1>), grid, dim3(256), 0, st, a, sign);
 }
 
 template <int DT>
@@ -205,7 +228,7 @@ static void launch_rotary_d(RotaryArgs &a, float sign, hipStream_t st) {
 hipError_t launch_rotary(const Heads &q, const Heads &qo, const Heads &k, const Heads &ko, int dt,
                          int64_t tokens, int dim, const int64_t *positions, const Rope &rope,
                          bool inverse, hipStream_t st) {
-  RotaryArgs a{q, qo, k, ko, rope, positions, tokens, dim, 0, 0};
+  RotaryArgs a{q, qo, k, ko, rope, positions, tokens, dim, 0, 0, 0};
   const float sign = inverse ? -1.f : 1.f;
   if (dt == kF32) launch_rotary_d<kF32>(a, sign, st);
   else if (dt == kF16) launch_rotary_d<kF16>(a, sign, st);
