@@ -248,6 +248,9 @@ int qmv_attention_4bit(const qmv_heads *q, const qmv_kv_cache *cache, const qmv_
   const int64_t most = reach(c, kb, max_kv);
   // steps of 64 tokens over all sequences and heads are counted in 31 bits
   if ((most / 64 + 2) * c.heads >= kMost / kb.batch) return QMV_ERR_TOO_LARGE;
+  // workgroups of 256 query rows (and a row's parts, at most one for each
+  // compute unit, only where there are fewer workgroups than units)
+  if (((int64_t)kb.max_q * (hq.heads / c.heads) / 256 + 1) * c.heads >= kMost / kb.batch) return QMV_ERR_TOO_LARGE;
   const size_t need = attention_workspace_bytes(c, kb, hq.heads, most, window);
   if (need && (!workspace || workspace_bytes < need)) return QMV_ERR_WORKSPACE;
   if (need && !aligned(workspace, 16)) return QMV_ERR_ALIGNMENT;

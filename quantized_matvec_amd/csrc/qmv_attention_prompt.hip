@@ -24,7 +24,7 @@
 //    planes, since the result would show it.
 // Neighbouring workgroups take neighbouring cache heads, which puts a head's
 // workgroups on one of the eight dies and its keys in that die's L2 cache; the
-// longest rows go first.  Where there are few workgroups the keys are divided
+// rows that see most keys go first, over all sequences.  Where there are few workgroups the keys are divided
 // among several (splits), joined by prompt_join_kernel.
 #include <algorithm>
 
@@ -60,15 +60,17 @@ __global__ __launch_bounds__(kPThreads, 2) void attention_prompt_kernel(PromptAr
   __shared__ __align__(16) uint8_t kbuf[2][PL][KT * KS];
   __shared__ __align__(16) uint8_t vbuf[2][PL][D * VS];
   __shared__ __align__(16) float2 lut[256 * COPIES];  // packed byte -> (T[byte >> 4], T[byte & 15])
-  __shared__ uint32_t kmax[2][kPWaves], vmax[2][kPWaves];
-  __shared__ uint8_t there[3][KT / 16];  // whether 16 tokens have a page: written two tiles ahead
+  __shared__ __align__(16) uint32_t kmax[2][4], vmax[2][4];  // by wave of the role
+  __shared__ __align__(4) uint8_t there[3][4];  // whether 16 tokens have a page: written two tiles ahead
   const AttnArgs &a = pa.a;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int b = blockIdx.y, heads = a.c.heads;
-  const int h = blockIdx.x % heads;
-  const int rest = blockIdx.x / heads;
-  const int split = rest / pa.mtiles, mt = pa.mtiles - 1 - (rest - split * pa.mtiles);
+  const int heads = a.c.heads;
+  const int h = (int)(blockIdx.x % (unsigned)heads);
+  const unsigned rest = blockIdx.x / (unsigned)heads;
+  const int b = (int)(rest % (unsigned)a.kb.batch);
+  const int rest2 = (int)(rest / (unsigned)a.kb.batch);  // tiles of rows from the last on, then splits
+  const int split = rest2 % pa.splits, mt = pa.mtiles - 1 - rest2 / pa.splits;
   const SeqRange s = seq_range(a.kb, b);
   const int n = s.n < a.kb.max_q ? s.n : a.kb.max_q;
   const int64_t rows = (int64_t)n * a.group;
@@ -79,6 +81,12 @@ __global__ __launch_bounds__(kPThreads, 2) void attention_prompt_kernel(PromptAr
     for (int i = tid; i < 256 * COPIES; i += kPThreads)
       lut[i] = make_float2(__uint_as_float(tb[i / COPIES >> 4]), __uint_as_float(tb[i / COPIES & 15]));
   }
+
+  if (tid < 8) {  // roles of fewer than four waves
+    kmax[tid >> 2][tid & 3] = 0u;
+    vmax[tid >> 2][tid & 3] = 0u;
+  }
+  __syncthreads();
 
   // keys [lo, hi) of the workgroup's rows; tiles [t, t_to) of them
   int lo, hi, unused;
@@ -193,15 +201,12 @@ __global__ __launch_bounds__(kPThreads, 2) void attention_prompt_kernel(PromptAr
       s1 = make_uint4(w[4], w[5], w[6], w[7]);
     }
     big = (uint32_t)wave_max_i32((int)big);
-    if (lane == 0) {
-      kmax[buf][wave] = isk ? big : 0u;
-      vmax[buf][wave] = isk ? 0u : big;
-    }
+    if (lane == 0 && isk) kmax[buf][wave] = big;
+    if (lane == 0 && isv) vmax[buf][wave - NU / 64] = big;
   };
-  auto exponent16 = [&](const uint32_t (&x)[kPWaves]) {
-    uint32_t big = 0;
-#pragma unroll
-    for (int w = 0; w < kPWaves; ++w) big = max(big, x[w]);
+  auto exponent16 = [&](const uint32_t (&x)[4]) {
+    const uint4 w = *reinterpret_cast<const uint4 *>(x);
+    const uint32_t big = max(max(w.x, w.y), max(w.z, w.w));
     int e = __builtin_amdgcn_readfirstlane(exponent_of(bits16_to_f32<DT>(big)));
     return e < -100 ? -100 : (e > 100 ? 100 : e);
   };
@@ -209,6 +214,10 @@ __global__ __launch_bounds__(kPThreads, 2) void attention_prompt_kernel(PromptAr
   const float2 *my_lut = lut + (lane & (COPIES - 1));
   auto dequantize = [&](int buf, int ek, int ev) {
     const uint32_t c[4] = {raw.x, raw.y, raw.z, raw.w};
+    float2 tv[16];  // all table reads in flight before the first is used
+#pragma unroll
+    for (int j = 0; j < 16; ++j) tv[j] = my_lut[((c[j >> 2] >> (8 * (j & 3))) & 0xffu) * COPIES];
+    __builtin_amdgcn_sched_barrier(0);
     if (isk) {
       const float f = ldexpf(bits16_to_f32<DT>(s0.x), -ek);
 #pragma unroll
@@ -216,7 +225,7 @@ __global__ __launch_bounds__(kPThreads, 2) void attention_prompt_kernel(PromptAr
         uint32_t w[4], y[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const float2 v = my_lut[((c[x] >> (8 * j)) & 0xffu) * COPIES];
+          const float2 v = tv[4 * x + j];
           const float p0 = v.x * f, p1 = v.y * f;
           w[j] = f16_pair(p0, p1);
           if constexpr (TWO) {
@@ -236,8 +245,7 @@ __global__ __launch_bounds__(kPThreads, 2) void attention_prompt_kernel(PromptAr
       for (int j = 0; j < 8; ++j) {  // tokens 2 j, 2 j + 1
         const float f0 = ldexpf(bits16_to_f32<DT>(sw[j] & 0xffffu), 14 - ev);
         const float f1 = ldexpf(bits16_to_f32<DT>(sw[j] >> 16), 14 - ev);
-        const float2 v0 = my_lut[((c[j >> 1] >> (16 * (j & 1))) & 0xffu) * COPIES];
-        const float2 v1 = my_lut[((c[j >> 1] >> (16 * (j & 1) + 8)) & 0xffu) * COPIES];
+        const float2 v0 = tv[2 * j], v1 = tv[2 * j + 1];
         const float e0 = v0.x * f0, e1 = v1.x * f1, o0 = v0.y * f0, o1 = v1.y * f1;
         w[0][j] = f16_pair(e0, e1);
         w[1][j] = f16_pair(o0, o1);
@@ -310,16 +318,22 @@ __global__ __launch_bounds__(kPThreads, 2) void attention_prompt_kernel(PromptAr
               sc[x] = __builtin_amdgcn_mfma_f32_32x32x16_f16(*reinterpret_cast<const f16x8_t *>(kr + KT * KS + 32 * c), qf[c], sc[x], 0, 0, 0);
           }
         }
-        bool all_there = true;
+        // fragments are read six ahead of the products that take them
+        __builtin_amdgcn_sched_group_barrier(0x100, 6, 0);
 #pragma unroll
-        for (int x = 0; x < KT / 16; ++x) all_there &= there[slot][x] != 0;
-        if (!(t0 >= all_lo && t0 + KT <= all_hi && __all(all_there))) {
+        for (int x = 0; x < TT * QS * PL - 6; ++x) {
+          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+          __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        }
+        __builtin_amdgcn_sched_group_barrier(0x008, 6, 0);
+        const uint32_t pages = *reinterpret_cast<const uint32_t *>(there[slot]) & (KT == 64 ? 0x01010101u : 0x0101u);
+        if (!(t0 >= all_lo && t0 + KT <= all_hi && __all(pages == (KT == 64 ? 0x01010101u : 0x0101u)))) {
 #pragma unroll
           for (int x = 0; x < TT; ++x)
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
               const int at = 32 * x + 8 * (j >> 2) + 4 * half + (j & 3);
-              const bool seen = t0 + at >= row_lo && t0 + at < row_hi && there[slot][2 * x + (j >> 3)];
+              const bool seen = (t0 + at >= row_lo) & (t0 + at < row_hi) & (pages >> (8 * (2 * x + (j >> 3))) & 1u);
               sc[x][j] = seen ? sc[x][j] : -INFINITY;
             }
         }
@@ -483,7 +497,7 @@ size_t prompt_workspace_bytes(const KVCache &c, const KVBatch &kb, int q_heads, 
 template <int DT>
 static void launch_prompt_t(const PromptArgs &pa, hipStream_t st) {
   const AttnArgs &a = pa.a;
-  const dim3 grid((unsigned)(a.c.heads * pa.mtiles * pa.splits), (unsigned)a.kb.batch);
+  const dim3 grid((unsigned)((int64_t)a.c.heads * pa.mtiles * pa.splits * a.kb.batch));
   constexpr bool two = DT == kF16;
 #define QMV_P(D) hipLaunchKernelGGL((attention_prompt_kernel<D, DT, two>), grid, dim3(kPThreads), 0, st, pa)
   switch (a.c.dim) {
