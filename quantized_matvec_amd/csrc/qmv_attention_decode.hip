@@ -621,20 +621,22 @@ __global__ __launch_bounds__(64 * decode_waves(D), decode_waves(D) / 4) void att
   }
 }
 
-// The partial sums of a row joined: grid (rows, cache heads, sequences), one
-// workgroup a row.  Rows that a wave or workgroup held whole are written.
+// The partial sums of a head joined: grid (cache heads, sequences, sets of
+// `set` query rows).  Heads that a wave or workgroup held whole are written.  A
+// thread sums four elements of a row over every `lists`-th part.
 template <int DT>
-__global__ __launch_bounds__(64 * kJoinWaves) void attention_join_kernel(DecodeArgs da, int dim, int qr) {
+__global__ __launch_bounds__(64 * kJoinWaves) void attention_join_kernel(DecodeArgs da, int dim, int qr, int set) {
   constexpr int kThreads = 64 * kJoinWaves;
-  __shared__ int tmp[2][kJoinWaves];
+  __shared__ int tmp[3][kJoinWaves];
   __shared__ __align__(16) float4 acc[kThreads];
   __shared__ float acc_l[kThreads];
-  __shared__ float2 ml[kMaxRuns + 32];
   __shared__ int where[kMaxRuns + 32];
+  __shared__ float row_max[16];
   const AttnArgs &a = da.a;
-  const int row = blockIdx.x, h = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
+  const int h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x;
   const SeqSteps q = seq_steps(a, b);
-  if (row >= q.n * a.group) return;
+  const int row0 = blockIdx.z * set;
+  const int rows = q.n * a.group - row0 < set ? q.n * a.group - row0 : set;
   int mine = 0, prior = 0, unused;
   for (int x = tid; x < a.kb.batch; x += kThreads) {
     const int st = seq_steps(a, x).steps;
@@ -644,66 +646,79 @@ __global__ __launch_bounds__(64 * kJoinWaves) void attention_join_kernel(DecodeA
   const int W = decode_waves(dim);
   const Runs runs(scan<kJoinWaves>(mine, tmp[0], unused) * a.c.heads, da.runs);
   const int start = scan<kJoinWaves>(prior, tmp[1], unused) * a.c.heads + h * q.steps, stop = start + q.steps;
+  if (rows <= 0) return;
   const int k0 = start / runs.per, k1 = (stop - 1) / runs.per;
   // the parts: up to W waves of the first and of the last workgroup (or one,
   // where its run lies in this head), one of each between
-  const int count = 2 * W + (k1 - k0 > 1 ? k1 - k0 - 1 : 0);
+  const int places = 2 * W + (k1 - k0 > 1 ? k1 - k0 - 1 : 0);
   auto part = [&](int x) {
     const int k = x < W ? k0 : (x < 2 * W ? k1 : k0 + 1 + x - 2 * W);
     const int w = x < W ? x : (x < 2 * W ? x - W : 0);
-    if (x >= W && x < 2 * W && k0 == k1) return -1;
+    if (x >= places || (x >= W && x < 2 * W && k0 == k1)) return -1;
     if (runs.from(k) >= start && runs.from(k + 1) <= stop) return w == 0 ? 2 * W * k : -1;
     const int from = runs.from(k), n = runs.from(k + 1) - from;
     const int at = from + (int)((uint32_t)n * (uint32_t)w / W), to = from + (int)((uint32_t)n * (uint32_t)(w + 1) / W);
     if (at >= to || to <= start || at >= stop) return -1;
     return 2 * (W * k + w) + (at >= start ? 0 : 1);
   };
-  int found = 0;
-  float mx = kNoScore;
-  for (int x = tid; x < count; x += kThreads) {
-    const int p = part(x);
-    where[x] = p;
-    ml[x] = p >= 0 ? da.part.ml[(int64_t)p * qr + row] : make_float2(kNoScore, 0.f);
-    mx = fmaxf(mx, ml[x].x);
-    found += p >= 0;
+  // at most 2 W + kMaxRuns places: one or two for a thread
+  int count = 0;
+  for (int x0 = 0; x0 < places; x0 += kThreads) {
+    const int p = part(x0 + tid);
+    int before;
+    if (x0 > 0) __syncthreads();
+    const int found = scan<kJoinWaves>(p >= 0, tmp[2], before);
+    if (p >= 0) where[count + before] = p;
+    count += found;
+  }
+  if (count <= 1) return;  // written whole
+  __syncthreads();
+  const int quads = dim / 4, items = rows * quads;
+  const int lists = items >= kThreads ? 1 : kThreads / items;
+  // rows' maxima: a wave for each row
+  for (int row = tid >> 6; row < rows; row += kJoinWaves) {
+    float mx = kNoScore;
+    for (int k = tid & 63; k < count; k += 64) mx = fmaxf(mx, da.part.ml[(int64_t)where[k] * qr + row0 + row].x);
+    mx = rows_max(row16_max(mx));
+    if ((tid & 63) == 0) row_max[row] = mx;
   }
   __syncthreads();
-  if (scan<kJoinWaves>(found, tmp[0], unused) <= 1) return;  // written whole
-  mx = rows_max(row16_max(mx));
-  if ((tid & 63) == 0) acc_l[tid >> 6] = mx;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kJoinWaves; ++w) mx = fmaxf(mx, acc_l[w]);
-  for (int x = tid; x < count; x += kThreads) ml[x].x = __builtin_amdgcn_exp2f(ml[x].x - mx);
-  __syncthreads();
-  const int quads = dim / 4, lists = kThreads / quads;  // dim <= 256: 4 lists or more
-  const int x4 = tid % quads, list = tid / quads;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  float l = 0.f;
-  if (list < lists) {
+  for (int i0 = 0; i0 < items; i0 += kThreads) {
+    const int item = i0 + tid % (lists > 1 ? items : kThreads), list = lists > 1 ? tid / items : 0;
+    const bool busy = item < items && list < lists;
+    const int row = busy ? item / quads : 0, x4 = busy ? item - row * quads : 0;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    float l = 0.f;
+    if (busy) {
+      const float mx = row_max[row];
 #pragma unroll 8
-    for (int x = list; x < count; x += lists) {
-      const int p = where[x];
-      const float4 y = p >= 0 ? *reinterpret_cast<const float4 *>(da.part.o + ((int64_t)p * qr + row) * dim + 4 * x4)
-                              : make_float4(0.f, 0.f, 0.f, 0.f);
-      const float f = ml[x].x;
-      l = fmaf(f, ml[x].y, l);
-      o.x = fmaf(f, y.x, o.x), o.y = fmaf(f, y.y, o.y), o.z = fmaf(f, y.z, o.z), o.w = fmaf(f, y.w, o.w);
+      for (int k = list; k < count; k += lists) {
+        const int64_t at = (int64_t)where[k] * qr + row0 + row;
+        const float2 ml = da.part.ml[at];
+        const float4 y = *reinterpret_cast<const float4 *>(da.part.o + at * dim + 4 * x4);
+        const float f = __builtin_amdgcn_exp2f(ml.x - mx);
+        l = fmaf(f, ml.y, l);
+        o.x = fmaf(f, y.x, o.x), o.y = fmaf(f, y.y, o.y), o.z = fmaf(f, y.z, o.z), o.w = fmaf(f, y.w, o.w);
+      }
     }
-  }
-  acc[tid] = o;
-  acc_l[tid] = l;
-  __syncthreads();
-  if (tid < quads) {
-    for (int k = 1; k < lists; ++k) {
-      const float4 y = acc[k * quads + tid];
-      o.x += y.x, o.y += y.y, o.z += y.z, o.w += y.w;
-      l += acc_l[k * quads + tid];
+    if (lists > 1) {  // one round: items < kThreads
+      acc[tid] = o;
+      acc_l[tid] = l;
+      __syncthreads();
+      if (busy && list == 0) {
+        for (int k = 1; k < lists; ++k) {
+          const float4 y = acc[k * items + item];
+          o.x += y.x, o.y += y.y, o.z += y.z, o.w += y.w;
+          l += acc_l[k * items + item];
+        }
+      }
     }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-    uint16_t *dst = static_cast<uint16_t *>(a.out.p) + (q.s.row0 + row / a.group) * a.out.ts +
-                    (h * a.group + row % a.group) * a.out.hs + 4 * x4;
-    *reinterpret_cast<uint2 *>(dst) = make_uint2(cvt_pair<DT>(o.x * inv, o.y * inv), cvt_pair<DT>(o.z * inv, o.w * inv));
+    if (busy && list == 0) {
+      const float inv = l > 0.f ? 1.f / l : 0.f;
+      uint16_t *dst = static_cast<uint16_t *>(a.out.p) + (q.s.row0 + (row0 + row) / a.group) * a.out.ts +
+                      (h * a.group + (row0 + row) % a.group) * a.out.hs + 4 * x4;
+      *reinterpret_cast<uint2 *>(dst) = make_uint2(cvt_pair<DT>(o.x * inv, o.y * inv), cvt_pair<DT>(o.z * inv, o.w * inv));
+    }
   }
 }
 
@@ -771,9 +786,13 @@ hipError_t launch_attention_decode(const AttnArgs &a, int dt, void *ws, hipStrea
   da.part.ml = reinterpret_cast<float2 *>(da.part.o + (size_t)da.runs * 2 * decode_waves(a.c.dim) * qr * a.c.dim);
   const hipError_t e = dt == kBF16 ? launch_decode_d<kBF16>(da, st) : launch_decode_d<kF16>(da, st);
   if (e != hipSuccess) return e;
-  const dim3 grid((unsigned)(a.kb.max_q * a.group), (unsigned)a.c.heads, (unsigned)a.kb.batch);
-  if (dt == kBF16) hipLaunchKernelGGL((attention_join_kernel<kBF16>), grid, dim3(64 * kJoinWaves), 0, st, da, a.c.dim, qr);
-  else hipLaunchKernelGGL((attention_join_kernel<kF16>), grid, dim3(64 * kJoinWaves), 0, st, da, a.c.dim, qr);
+  // all rows of a head together, or, where there are few heads and so many
+  // parts of each, one by one (196611 tokens, 8 heads of 8 rows: 7 us against 12)
+  const int rows = a.kb.max_q * a.group;
+  const int set = (int64_t)a.c.heads * a.kb.batch >= device_cu_count() ? rows : 1;
+  const dim3 grid((unsigned)a.c.heads, (unsigned)a.kb.batch, (unsigned)((rows + set - 1) / set));
+  if (dt == kBF16) hipLaunchKernelGGL((attention_join_kernel<kBF16>), grid, dim3(64 * kJoinWaves), 0, st, da, a.c.dim, qr, set);
+  else hipLaunchKernelGGL((attention_join_kernel<kF16>), grid, dim3(64 * kJoinWaves), 0, st, da, a.c.dim, qr, set);
   return hipGetLastError();
 }
 
