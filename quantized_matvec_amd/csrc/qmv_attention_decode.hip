@@ -169,7 +169,7 @@ struct StepPages {
 
 // Waves of a workgroup, which has a compute unit to itself: three waves of a
 // SIMD share its registers, or two where rows are long.
-__host__ __device__ constexpr int decode_waves(int D) { return D <= 96 ? 12 : 8; }
+__host__ __device__ constexpr int decode_waves(int D) { return D <= 96 ? 12 : D <= 128 ? 8 : 4; }
 
 template <int D, int CB, int RJ, int DT, bool LO>
 __global__ __launch_bounds__(64 * decode_waves(D), decode_waves(D) / 4) void attention_decode_kernel(DecodeArgs da) {
