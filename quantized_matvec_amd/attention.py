@@ -331,7 +331,7 @@ def kv_dequantize_4bit(cache: KVCache4bit, block_table: torch.Tensor, kv_len: to
     kb = _batch(cache, block_table, kv_len, cu_q, max_q, tokens)
     shape = (tokens, cache.heads, cache.head_dim)
     if k_out is None:
-        k_out = torch.empty(shape, dtype=cache.dtype, device=cache.device)
+        k_out = cache.k_scales.new_empty(shape)
     elif k_out.shape != shape or k_out.dtype != cache.dtype or k_out.device != cache.device:
         raise ValueError("k_out must be [tokens, heads, head_dim] of the cache's type and device")
     k_out, hk = _out(k_out, k_out, "k_out")

@@ -156,7 +156,7 @@ __device__ __forceinline__ void transpose_rows(uint4 &w) {
   swap16(w.z, w.w);
 }
 
-// Maximum and sum over the four rows of 16 lanes (lanes of equal l % 16).
+// Maximum over the four rows of 16 lanes (lanes of equal l % 16).
 __device__ __forceinline__ float rows_max(float v) {
   uint32_t a = __float_as_uint(v), b = a;
   swap32(a, b);
@@ -165,15 +165,6 @@ __device__ __forceinline__ float rows_max(float v) {
   swap16(a, b);
   return fmaxf(__uint_as_float(a), __uint_as_float(b));
 }
-__device__ __forceinline__ float rows_sum(float v) {
-  uint32_t a = __float_as_uint(v), b = a;
-  swap32(a, b);
-  v = __uint_as_float(a) + __uint_as_float(b);
-  a = b = __float_as_uint(v);
-  swap16(a, b);
-  return __uint_as_float(a) + __uint_as_float(b);
-}
-
 __device__ __forceinline__ uint32_t f16_pair(float lo, float hi) {
   const f32x2_t v = {lo, hi};
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, f16x2v_t));

@@ -320,3 +320,41 @@ def test_refusals():
         with pytest.raises(qmv.QmvError):
             attention_4bit(**{**ok, **bad})
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("dim,bs", [(64, 64), (128, 64), (256, 128)])
+def test_many_sequences(dim, bs):
+    """More sequences than a workgroup has threads, many of them empty or without tokens."""
+    rng = np.random.default_rng(dim)
+    lens = rng.integers(0, 40, 900)
+    lens[rng.integers(0, 900, 200)] = 0
+    check(lens.tolist(), [1] * 900, 2, 1, dim, bs, 16, seed=dim)
+    new = rng.integers(0, 3, 900)
+    new[:300] = 0
+    new[899] = 2
+    check((lens + new).tolist(), new.tolist(), 2, 1, dim, bs, 16, "fp16", seed=dim + 1)
+
+
+def test_uneven_batch_over_every_division():
+    """Sequences whose steps fall on all sides of the division among waves and workgroups."""
+    lens = [9000, 1, 64, 700, 12000, 65, 3, 4097, 0, 511]
+    check(lens, [1] * 10, 8, 2, 128, 64, 64, seed=31)
+    check(lens, [1] * 10, 32, 4, 64, 32, 16, "fp16", "fp4", seed=32)
+    check(lens, [1] * 10, 2, 1, 256, 64, 32, seed=33)
+
+
+def test_long_sums_do_not_drift():
+    """Uniform weights over 60000 values of one block scale: the values cancel,
+    their rounding must not add up.  The sum of N values of variance s^2 is of
+    size s sqrt(N), so a bias of 6e-5 of a value (the fp16 rounding of the NF4
+    values) would be 1.5 % of it; the result's own rounding is 2^-9."""
+    for dt, tol in (("bf16", 2.5e-3), ("fp16", 3.5e-4)):
+        for new in ([1], [24]):
+            cache, table, K, V = make([60000], 1, 128, 64, 64, dt, "nf4", 41, spread=0.0)
+            q = torch.zeros(new[0], 4, 128, dtype=TDT[dt], device="cuda")
+            kl = torch.tensor([60000], dtype=torch.int32, device="cuda")
+            cu = torch.tensor([0, new[0]], dtype=torch.int32, device="cuda")
+            got = attention_4bit(q, cache, table, kl, cu_q=cu, max_q=new[0], causal=False).double().cpu().numpy()
+            want = V[0][:, 0].mean(0)
+            err = np.linalg.norm(got - want) / np.linalg.norm(np.broadcast_to(want, got.shape))
+            assert err <= tol, (dt, new, err)

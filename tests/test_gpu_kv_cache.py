@@ -353,3 +353,60 @@ def test_refusals():
     with pytest.raises(ValueError):
         rotary(q, k, rope, torch.zeros(1, dtype=torch.int64, device="cuda"), q_out=q.float())
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("interleaved,rot", [(False, 128), (True, 64), (False, 24)])
+def test_rotary_of_many_tokens_is_that_of_its_parts(interleaved, rot):
+    """A call large enough for several heads a thread, bit for bit against small calls."""
+    T = 50000 if rot == 128 else 20000
+    table = rope_table(rope_frequencies(rot), 4096)
+    q, k = rows(T, [7, 2], 128, "bf16", 3, strided=True)
+    pos = torch.arange(T, device="cuda") % 4100
+    yq, yk = rotary(q, k, table, pos, interleaved=interleaved)
+    for a in (0, 777, T // 2, T - 100):
+        pq, pk = rotary(q[a:a + 100], k[a:a + 100], table, pos[a:a + 100].contiguous(), interleaved=interleaved)
+        torch.cuda.synchronize()
+        assert torch.equal(yq[a:a + 100], pq) and torch.equal(yk[a:a + 100], pk), a
+
+
+@pytest.mark.parametrize("dim,bs,hk", [(128, 64, 8), (64, 32, 3), (256, 64, 2), (96, 32, 5)])
+def test_append_of_many_tokens_is_that_of_its_parts(dim, bs, hk):
+    """Long calls (several rows a thread, groups of 16 positions) against the
+    same tokens appended a few at a time: the cache's bytes are the same."""
+    T, past, hq = 4000, 5, 2 * hk
+    pages = -(-(T + past) // 64)
+    bt = torch.randperm(pages, device="cuda").to(torch.int32)[None]
+    q, k, v = rows(T, [hq, hk, hk], dim, "bf16", dim, strided=True)
+    rope = rope_table(rope_frequencies(dim), T + past)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    one, many = KVCache4bit(pages, hk, 64, dim, bs), KVCache4bit(pages, hk, 64, dim, bs)
+    got = kv_append_4bit(one, k, v, bt, i32([past + T]), cu_q=i32([0, T]), q=q, table=rope)
+    back = kv_dequantize_4bit(one, bt, i32([past + T]), T, cu_q=i32([0, T]))
+    at, parts, reads = 0, [], []
+    sizes = [1, 6, 7, 8, 9, 100, 333]
+    while at < T:
+        n = min(sizes[len(parts) % len(sizes)], T - at)
+        lens, cu = i32([past + at + n]), i32([0, n])
+        parts.append(kv_append_4bit(many, k[at:at + n], v[at:at + n], bt, lens, cu_q=cu, q=q[at:at + n], table=rope))
+        reads.append(kv_dequantize_4bit(many, bt, lens, n, cu_q=cu))
+        at += n
+    torch.cuda.synchronize()
+    for name in ("k_codes", "k_scales", "v_codes", "v_scales"):
+        assert torch.equal(getattr(one, name), getattr(many, name)), name
+    assert torch.equal(got, torch.cat(parts))
+    for x in (0, 1):
+        assert torch.equal(back[x], torch.cat([r[x] for r in reads]))
+
+
+def test_dequantize_into_given_strided_outputs():
+    cache = KVCache4bit(4, 2, 16, 64, 32)
+    bt = torch.arange(4, dtype=torch.int32, device="cuda")[None]
+    q, k, v = rows(40, [4, 2, 2], 64, "bf16", 12, True)
+    kl, cu = torch.tensor([40], dtype=torch.int32, device="cuda"), torch.tensor([0, 40], dtype=torch.int32, device="cuda")
+    kv_append_4bit(cache, k, v, bt, kl, cu_q=cu)
+    want = kv_dequantize_4bit(cache, bt, kl, 40, cu_q=cu)
+    whole = torch.full((40, 7, 64), 9.0, dtype=torch.bfloat16, device="cuda")
+    kv_dequantize_4bit(cache, bt, kl, 40, cu_q=cu, k_out=whole[:, 1:3], v_out=whole[:, 4:6])
+    torch.cuda.synchronize()
+    assert torch.equal(whole[:, 1:3], want[0]) and torch.equal(whole[:, 4:6], want[1])
+    assert (whole[:, [0, 3, 6]] == 9).all()
