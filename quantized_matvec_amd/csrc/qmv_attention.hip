@@ -127,7 +127,7 @@ hipError_t launch_attention_rows(const AttnArgs &a, int dt, hipStream_t st) {
 size_t attention_workspace_bytes(const KVCache &c, const KVBatch &kb, int q_heads, int64_t max_kv,
                                  int64_t window) {
   const int64_t rows = (int64_t)kb.max_q * (q_heads / c.heads);
-  if (rows <= 16 && decode_eligible(c, (int)rows))
+  if (decode_eligible(c, rows))
     return decode_workspace_bytes(c, kb, (int)rows, max_kv, window);
   return prompt_eligible(c) ? prompt_workspace_bytes(c, kb, q_heads, max_kv, window) : 0;
 }
@@ -138,7 +138,7 @@ hipError_t launch_attention(const KVCache &c, int dt, int qt, const KVBatch &kb,
   const AttnArgs a{c, kb, q, out, q.heads / c.heads, scale, (int)max_kv,
                    (int)std::min<int64_t>(window, INT32_MAX), causal, qt};
   const int64_t rows = (int64_t)kb.max_q * a.group;
-  if (rows <= 16 && decode_eligible(c, (int)rows)) return launch_attention_decode(a, dt, ws, st);
+  if (decode_eligible(c, rows)) return launch_attention_decode(a, dt, ws, st);
   return prompt_eligible(c) ? launch_attention_prompt(a, dt, ws, st) : launch_attention_rows(a, dt, st);
 }
 

@@ -246,8 +246,9 @@ int qmv_attention_4bit(const qmv_heads *q, const qmv_kv_cache *cache, const qmv_
     return QMV_ERR_INVALID_ARG;
   if (kb.max_q > (kMost - 1) / hq.heads) return QMV_ERR_TOO_LARGE;
   const int64_t most = reach(c, kb, max_kv);
-  // steps of 64 tokens over all sequences and heads are counted in 31 bits
-  if ((most / 64 + 2) * c.heads >= kMost / kb.batch) return QMV_ERR_TOO_LARGE;
+  // steps of 64 tokens over all sequences, heads and (up to three) row tiles
+  // are counted in 31 bits
+  if ((most / 64 + 2) * 3 * c.heads >= kMost / kb.batch) return QMV_ERR_TOO_LARGE;
   // workgroups of 256 query rows (and a row's parts, at most one for each
   // compute unit, only where there are fewer workgroups than units)
   if (((int64_t)kb.max_q * (hq.heads / c.heads) / 256 + 1) * c.heads >= kMost / kb.batch) return QMV_ERR_TOO_LARGE;

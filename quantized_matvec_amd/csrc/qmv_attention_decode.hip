@@ -1,6 +1,6 @@
-// Attention of a few query rows (up to 16: new tokens times query heads of a
-// cache head) over the 4-bit cache: the serving step, bound by reading the
-// cache once.
+// Attention of a few query rows (up to 48, in tiles of 16: new tokens times
+// query heads of a cache head) over the 4-bit cache: the serving step, bound by
+// reading the cache once.
 //
 // A wave takes 64 tokens a step.  Scores are S = Q K^T with
 // v_mfma_f32_16x16x32_f16 (16 query rows by 16 tokens), outputs O^T = V^T P^T
@@ -51,7 +51,8 @@ constexpr int kMaxRuns = 1024;  // workgroups of a call
 struct DecodeArgs {
   AttnArgs a;
   Partials part;
-  int runs;  // workgroups
+  int runs;   // workgroups
+  int tiles;  // of 16 query rows; the division of work takes a head's tiles for heads
 };
 
 // Steps of sequence b for each cache head: at least one, which writes the
@@ -200,7 +201,7 @@ __global__ __launch_bounds__(64 * decode_waves(D), decode_waves(D) / 4) void att
   // this wave's steps [cur, end) of the order (sequence, head, step): the
   // lengths are summed up, and the thread whose sequence holds a wave's first
   // step tells it
-  const int heads = a.c.heads;
+  const int heads = a.c.heads, units = heads * da.tiles;
   SeqSteps q = {};
   if (tid < a.kb.batch) q = seq_steps(a, tid);
   fill_lut<LO, kThreads>(lut, a.qt, tid);
@@ -210,7 +211,7 @@ __global__ __launch_bounds__(64 * decode_waves(D), decode_waves(D) / 4) void att
     __syncthreads();
     total += scan<kWaves>(b0 + tid < a.kb.batch ? seq_steps(a, b0 + tid).steps : 0, tmp[0], unused);
   }
-  const Runs runs(uniform(total) * heads, da.runs);
+  const Runs runs(uniform(total) * units, da.runs);
   const int run_from = runs.from(blockIdx.x), run_to = runs.from(blockIdx.x + 1);
   if (run_from >= run_to) return;
   for (int b0 = 0, base = 0; b0 < a.kb.batch; b0 += kThreads) {
@@ -221,7 +222,7 @@ __global__ __launch_bounds__(64 * decode_waves(D), decode_waves(D) / 4) void att
       __syncthreads();
       sum = scan<kWaves>(q.steps, tmp[1], before);
     }
-    const int first = (base + before) * heads, last = first + q.steps * heads;
+    const int first = (base + before) * units, last = first + q.steps * units;
     if (first < run_to && last > run_from) {
       for (int w = 0; w < kWaves; ++w) {
         const int at = runs.wave_from<kWaves>(blockIdx.x, w);
@@ -236,8 +237,8 @@ __global__ __launch_bounds__(64 * decode_waves(D), decode_waves(D) / 4) void att
   int cur = wave_run;
   // whether the run lies in one head, and which
   const int run_steps = uniform(starts[0].q.steps), run_first = uniform(starts[0].first);
-  const int run_h = (run_from - run_first) / run_steps;
-  const int run_head0 = run_first + run_h * run_steps;
+  const int run_unit = (run_from - run_first) / run_steps;
+  const int run_head0 = run_first + run_unit * run_steps;
   const bool joined = run_to <= run_head0 + run_steps;
   // (a wave of a joined run takes part in it also without a step of its own)
   if (!joined && cur >= end) return;
@@ -267,11 +268,13 @@ __global__ __launch_bounds__(64 * decode_waves(D), decode_waves(D) / 4) void att
       const int i = (4 * L + g) / KU, c = 4 * L + g - i * KU;
       koff[L] = (4 * (r & 3) + i) * row_bytes + 16 * c;
     }
-    const int h = joined ? run_h : (cur - first) / q.steps;
-    const int head0 = first + h * q.steps;
+    const int unit = joined ? run_unit : (cur - first) / q.steps;
+    const int h = unit / da.tiles, base_row = (unit - h * da.tiles) * 16;
+    const int head0 = first + unit * q.steps;
     const int t_from = cur - head0;
     const int t_to = end - head0 < q.steps ? end - head0 : q.steps;
-    const int rows = q.n * a.group;
+    const int all_rows = q.n * a.group - base_row;  // none in a tile past this sequence's rows
+    const int rows = all_rows < 0 ? 0 : (all_rows < 16 ? all_rows : 16);
 
     // ---- loads of a step ----
     // entries of the block table, loaded unconditionally (a branch around a
@@ -327,7 +330,7 @@ __global__ __launch_bounds__(64 * decode_waves(D), decode_waves(D) / 4) void att
     };
     const int mine = (r >> 2) * RJ + (r & 3);
     const bool real = (r & 3) < RJ && mine < rows;
-    const uint16_t *qrow = query(real ? mine : 0);
+    const uint16_t *qrow = query(real ? base_row + mine : 0);
     uint4 raw[KU];
 #pragma unroll
     for (int c = 0; c < KU; ++c) raw[c] = *reinterpret_cast<const uint4 *>(qrow + 32 * c + 8 * g);
@@ -364,7 +367,7 @@ __global__ __launch_bounds__(64 * decode_waves(D), decode_waves(D) / 4) void att
     for (int j = 0; j < RJ; ++j) {
       qscale[j] = __shfl(big, 4 * g + j);
       const int row = g * RJ + j;
-      key_range(a, q.s, row < rows ? row / a.group : 0, lo[j], hi[j]);
+      key_range(a, q.s, row < rows ? (base_row + row) / a.group : 0, lo[j], hi[j]);
       if (row >= rows) lo[j] = hi[j] = 0;
     }
     int all_lo, all_hi, unused;
@@ -541,8 +544,9 @@ __global__ __launch_bounds__(64 * decode_waves(D), decode_waves(D) / 4) void att
         jl[wave][g * RJ + j] = l[j];
       }
     }
-    const float unit = ldexpf(1.f / half_factor(a.qt), -ev);
-    auto out_row = [&](int row) {
+    const float factor = ldexpf(1.f / half_factor(a.qt), -ev);
+    auto out_row = [&](int r) {
+      const int row = base_row + r;
       return static_cast<uint16_t *>(a.out.p) + (q.s.row0 + row / a.group) * a.out.ts +
              (h * a.group + row % a.group) * a.out.hs;
     };
@@ -554,7 +558,7 @@ __global__ __launch_bounds__(64 * decode_waves(D), decode_waves(D) / 4) void att
       float top = kNoScore;
 #pragma unroll
       for (int w = 0; w < kWaves; ++w) top = fmaxf(top, jm[w][r % QR]);
-      const float f = unit * __builtin_amdgcn_exp2f(jm[wave][r % QR] - top);
+      const float f = factor * __builtin_amdgcn_exp2f(jm[wave][r % QR] - top);
       const int64_t part = (int64_t)(2 * kWaves) * blockIdx.x * QR;
 #pragma unroll
       for (int c = 0; c < KU; ++c) {
@@ -592,7 +596,7 @@ __global__ __launch_bounds__(64 * decode_waves(D), decode_waves(D) / 4) void att
     // ---- the wave writes them itself ----
     const bool whole = t_from == 0 && t_to == q.steps;
     const float sum = jl[wave][r % QR];
-    const float f = unit * (whole ? (sum > 0.f ? 1.f / sum : 0.f) : 1.f);
+    const float f = factor * (whole ? (sum > 0.f ? 1.f / sum : 0.f) : 1.f);
     const int part = 2 * (kWaves * blockIdx.x + wave) + (cur == wave_run ? 0 : 1);
     if (r < rows) {
 #pragma unroll
@@ -613,7 +617,7 @@ __global__ __launch_bounds__(64 * decode_waves(D), decode_waves(D) / 4) void att
     }
     cur = head0 + t_to;
     if (cur >= end) return;
-    if (cur == first + q.steps * heads) {
+    if (cur == first + q.steps * units) {
       first = cur;
       if (++b >= a.kb.batch) return;
       q = uniform(seq_steps(a, b));
@@ -621,9 +625,9 @@ __global__ __launch_bounds__(64 * decode_waves(D), decode_waves(D) / 4) void att
   }
 }
 
-// The partial sums of a head joined: grid (cache heads, sequences, sets of
-// `set` query rows).  Heads that a wave or workgroup held whole are written.  A
-// thread sums four elements of a row over every `lists`-th part.
+// The partial sums of a tile of rows joined: grid (cache heads times tiles,
+// sequences, sets of `set` query rows).  What a wave or workgroup held whole is
+// written.  A thread sums four elements of a row over every `lists`-th part.
 template <int DT>
 __global__ __launch_bounds__(64 * kJoinWaves) void attention_join_kernel(DecodeArgs da, int dim, int qr, int set) {
   constexpr int kThreads = 64 * kJoinWaves;
@@ -633,10 +637,12 @@ __global__ __launch_bounds__(64 * kJoinWaves) void attention_join_kernel(DecodeA
   __shared__ int where[kMaxRuns + 32];
   __shared__ float row_max[16];
   const AttnArgs &a = da.a;
-  const int h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x;
+  const int unit = blockIdx.x, b = blockIdx.y, tid = threadIdx.x;
+  const int h = unit / da.tiles, base_row = (unit - h * da.tiles) * 16, units = a.c.heads * da.tiles;
   const SeqSteps q = seq_steps(a, b);
   const int row0 = blockIdx.z * set;
-  const int rows = q.n * a.group - row0 < set ? q.n * a.group - row0 : set;
+  const int all_rows = q.n * a.group - base_row < 16 ? q.n * a.group - base_row : 16;
+  const int rows = all_rows - row0 < set ? all_rows - row0 : set;
   int mine = 0, prior = 0, unused;
   for (int x = tid; x < a.kb.batch; x += kThreads) {
     const int st = seq_steps(a, x).steps;
@@ -644,8 +650,8 @@ __global__ __launch_bounds__(64 * kJoinWaves) void attention_join_kernel(DecodeA
     if (x < b) prior += st;
   }
   const int W = decode_waves(dim);
-  const Runs runs(scan<kJoinWaves>(mine, tmp[0], unused) * a.c.heads, da.runs);
-  const int start = scan<kJoinWaves>(prior, tmp[1], unused) * a.c.heads + h * q.steps, stop = start + q.steps;
+  const Runs runs(scan<kJoinWaves>(mine, tmp[0], unused) * units, da.runs);
+  const int start = scan<kJoinWaves>(prior, tmp[1], unused) * units + unit * q.steps, stop = start + q.steps;
   if (rows <= 0) return;
   const int k0 = start / runs.per, k1 = (stop - 1) / runs.per;
   // the parts: up to W waves of the first and of the last workgroup (or one,
@@ -715,31 +721,41 @@ __global__ __launch_bounds__(64 * kJoinWaves) void attention_join_kernel(DecodeA
     }
     if (busy && list == 0) {
       const float inv = l > 0.f ? 1.f / l : 0.f;
-      uint16_t *dst = static_cast<uint16_t *>(a.out.p) + (q.s.row0 + (row0 + row) / a.group) * a.out.ts +
-                      (h * a.group + (row0 + row) % a.group) * a.out.hs + 4 * x4;
+      const int m = base_row + row0 + row;
+      uint16_t *dst = static_cast<uint16_t *>(a.out.p) + (q.s.row0 + m / a.group) * a.out.ts +
+                      (h * a.group + m % a.group) * a.out.hs + 4 * x4;
       *reinterpret_cast<uint2 *>(dst) = make_uint2(cvt_pair<DT>(o.x * inv, o.y * inv), cvt_pair<DT>(o.z * inv, o.w * inv));
     }
   }
 }
 
-bool decode_eligible(const KVCache &c, int rows) {
-  return rows <= 16 && (c.dim == 64 || c.dim == 96 || c.dim == 128 || c.dim == 192 || c.dim == 256);
+// Up to 48 query rows are three tiles, each of which goes over the keys by
+// itself (mostly out of the caches); the prompt kernel's time is about the same
+// for any number of rows up to 256.  Kernels and join, here against there, 16
+// sequences of about 4600 tokens, 64 heads over 4 of 128: 16 rows 32 us / 68,
+// 32 rows 49 / 70, 48 rows 66 / 73, so that a fourth tile would be slower; 24
+// sequences of 40 rows, 8 heads of 128: 122 / 264, 32 heads of 64 with fp16 and
+// a window of 4096: 216 / 395.
+bool decode_eligible(const KVCache &c, int64_t rows) {
+  return rows <= 48 && (c.dim == 64 || c.dim == 96 || c.dim == 128 || c.dim == 192 || c.dim == 256);
 }
 
 // Query rows that a call's kernel has room for.
 static int decode_rows(int rows) { return rows <= 4 ? 4 : rows <= 8 ? 8 : 16; }
 
+static int decode_tiles(int rows) { return (rows + 15) / 16; }
+
 // Workgroups of a call: one for each compute unit, fewer where there cannot be
 // that many steps.
-static int decode_runs(const KVCache &c, const KVBatch &kb, int64_t max_kv, int64_t window) {
+static int decode_runs(const KVCache &c, const KVBatch &kb, int rows, int64_t max_kv, int64_t window) {
   int64_t keys = max_kv;
   if (window > 0) keys = std::min<int64_t>(keys, window + kb.max_q + 15);
-  const int64_t steps = (int64_t)kb.batch * c.heads * ((keys + kStep - 1) / kStep + 1);
+  const int64_t steps = (int64_t)kb.batch * c.heads * decode_tiles(rows) * ((keys + kStep - 1) / kStep + 1);
   return (int)std::max<int64_t>(1, std::min<int64_t>(std::min(device_cu_count(), kMaxRuns), steps));
 }
 
 size_t decode_workspace_bytes(const KVCache &c, const KVBatch &kb, int rows, int64_t max_kv, int64_t window) {
-  const size_t parts = (size_t)decode_runs(c, kb, max_kv, window) * 2 * decode_waves(c.dim);
+  const size_t parts = (size_t)decode_runs(c, kb, rows, max_kv, window) * 2 * decode_waves(c.dim);
   return parts * decode_rows(rows) * (c.dim + 2) * 4;
 }
 
@@ -780,17 +796,18 @@ static hipError_t launch_decode_d(const DecodeArgs &da, hipStream_t st) {
 }
 
 hipError_t launch_attention_decode(const AttnArgs &a, int dt, void *ws, hipStream_t st) {
-  DecodeArgs da{a, {}, decode_runs(a.c, a.kb, a.max_kv, a.window)};
+  const int rows = a.kb.max_q * a.group;
+  DecodeArgs da{a, {}, decode_runs(a.c, a.kb, rows, a.max_kv, a.window), decode_tiles(rows)};
   da.part.o = static_cast<float *>(ws);
-  const int qr = decode_rows(a.kb.max_q * a.group);
+  const int qr = decode_rows(rows);
   da.part.ml = reinterpret_cast<float2 *>(da.part.o + (size_t)da.runs * 2 * decode_waves(a.c.dim) * qr * a.c.dim);
   const hipError_t e = dt == kBF16 ? launch_decode_d<kBF16>(da, st) : launch_decode_d<kF16>(da, st);
   if (e != hipSuccess) return e;
   // all rows of a head together, or, where there are few heads and so many
   // parts of each, one by one (196611 tokens, 8 heads of 8 rows: 7 us against 12)
-  const int rows = a.kb.max_q * a.group;
-  const int set = (int64_t)a.c.heads * a.kb.batch >= device_cu_count() ? rows : 1;
-  const dim3 grid((unsigned)a.c.heads, (unsigned)a.kb.batch, (unsigned)((rows + set - 1) / set));
+  const int units = a.c.heads * da.tiles, most = std::min(rows, 16);
+  const int set = (int64_t)units * a.kb.batch >= device_cu_count() ? most : 1;
+  const dim3 grid((unsigned)units, (unsigned)a.kb.batch, (unsigned)((most + set - 1) / set));
   if (dt == kBF16) hipLaunchKernelGGL((attention_join_kernel<kBF16>), grid, dim3(64 * kJoinWaves), 0, st, da, a.c.dim, qr, set);
   else hipLaunchKernelGGL((attention_join_kernel<kF16>), grid, dim3(64 * kJoinWaves), 0, st, da, a.c.dim, qr, set);
   return hipGetLastError();

@@ -202,8 +202,8 @@ struct Partials {
 
 // The generic kernel: head sizes without a matrix-core kernel.
 hipError_t launch_attention_rows(const AttnArgs &a, int dt, hipStream_t st);
-// Up to 16 query rows (tokens times group) of a cache head.
-bool decode_eligible(const KVCache &c, int rows);
+// Up to 48 query rows (tokens times group) of a cache head.
+bool decode_eligible(const KVCache &c, int64_t rows);
 size_t decode_workspace_bytes(const KVCache &c, const KVBatch &kb, int rows, int64_t max_kv, int64_t window);
 hipError_t launch_attention_decode(const AttnArgs &a, int dt, void *ws, hipStream_t st);
 // Any number of query rows.

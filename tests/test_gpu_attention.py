@@ -335,6 +335,17 @@ def test_many_sequences(dim, bs):
     check((lens + new).tolist(), new.tolist(), 2, 1, dim, bs, 16, "fp16", seed=dim + 1)
 
 
+@pytest.mark.parametrize("hq,hk,new", [(8, 8, [17, 33, 48]), (64, 4, [2, 1, 3]), (34, 2, [2, 0, 1]), (6, 2, [1, 16, 15]),
+                                       (24, 1, [1, 1, 1]), (40, 1, [1, 1, 1]), (2, 2, [47, 1, 32])])
+@pytest.mark.parametrize("dim,dt", [(64, "fp16"), (96, "bf16"), (128, "bf16"), (256, "fp16")])
+def test_row_tiles(hq, hk, new, dim, dt):
+    """17 to 48 rows of a cache head: tiles that end inside a token, that a
+    sequence fills in part or not at all, over short and divided sequences."""
+    check([70, 900, 3000], new, hq, hk, dim, 32, 16, dt, seed=hq + dim)
+    check([5000, 49, 0], new, hq, hk, dim, 32, 64, dt, "fp4", seed=hq + dim + 1, window=100)
+    check([48, 47, 260], new, hq, hk, dim, 32, 16, dt, seed=hq + dim + 2, causal=False, missing=[(2, 1)], strided=True)
+
+
 def test_uneven_batch_over_every_division():
     """Sequences whose steps fall on all sides of the division among waves and workgroups."""
     lens = [9000, 1, 64, 700, 12000, 65, 3, 4097, 0, 511]
