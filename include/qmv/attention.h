@@ -6,7 +6,8 @@
  * The conventions of qmv.h hold here too: every array is the caller's, device
  * arrays are 16-byte aligned, work is enqueued on ``stream`` and nothing
  * synchronizes the host, and every argument the host can see is checked
- * before anything is launched.  What only the device sees (positions, lengths,
+ * before anything is launched (QMV_ERR_TOO_LARGE where a call's sizes pass the
+ * limits named at each structure and call).  What only the device sees (positions, lengths,
  * offsets and page numbers) is checked by the kernels: a value out of range
  * never reaches memory, and what it means is stated at each call.
  */
@@ -77,7 +78,7 @@ int qmv_rope_table(const double *freqs, int32_t rot_dim, int64_t max_pos, double
  *   q, q_out   heads of any of the three types; q_out may be q itself (same
  *              pointer and strides), but must not overlap it otherwise
  *   k, k_out   both NULL, or as q with a head count of their own
- *   head_dim   a multiple of 8
+ *   head_dim   a multiple of 8, at most 4096, else QMV_ERR_UNSUPPORTED; heads at most 65535
  *   positions  [tokens] device int64, 8-byte aligned
  *   inverse    1: the rotation by minus the angle.  It is the backward pass:
  *              with dY the gradient of the outputs, the gradient of the inputs
@@ -104,6 +105,9 @@ int qmv_rotary(const qmv_heads *q, const qmv_heads *q_out, const qmv_heads *k,
  *   blocksize  power of two, at least 32, dividing head_dim
  *   dtype      QMV_F16 or QMV_BF16: the type of keys, values and queries
  * else QMV_ERR_UNSUPPORTED.
+ *   heads      1 .. 65535, num_pages 1 .. 2^31 - 1 (QMV_ERR_INVALID_ARG)
+ * heads * page_size * head_dim, a page's elements, is below 2^31, else
+ * QMV_ERR_TOO_LARGE; offsets of pages are 64-bit.
  */
 typedef struct {
   uint8_t *k_codes;
@@ -131,7 +135,10 @@ typedef struct {
  *                one token for each sequence (tokens = batch)
  *   max_q        at least the most tokens of one sequence in this call; the
  *                tokens of a sequence beyond it are not worked on
- *   batch        1 .. 65535
+ *   batch        1 .. 65535, else QMV_ERR_UNSUPPORTED
+ * max_q times the heads of a token, and the 64-token steps of the longest
+ * sequence times batch and heads, have to fit in 31 bits (attention counts
+ * three row tiles for each head), else QMV_ERR_TOO_LARGE.
  * Token i of a sequence's n tokens has position kv_len - n + i.
  */
 typedef struct {

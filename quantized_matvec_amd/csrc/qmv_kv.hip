@@ -128,7 +128,9 @@ struct Turn {
 // pages and angles are fetched once and the next row's elements while this
 // one is worked on.  With TG = 1 (few tokens) the rows of one token fill the
 // workgroup; otherwise TG places of one group of 16 cache positions do, and
-// one workgroup writes all bytes of a value group and of a group's scales.
+// one workgroup writes all bytes of a value group and of a group's scales
+// (2532 tokens of three chunks, 32 + 32 + 32 heads of 64: 28.3 us one by one,
+// 23.6 us in groups, one set of rows a thread both times).
 template <int LPR, int TG>
 struct Place {
   static constexpr int RPW = 256 / LPR, HS = RPW / TG;
@@ -241,6 +243,13 @@ __device__ __forceinline__ void append_rows(const AppendArgs &a, int iters) {
   }
 }
 
+// Bound by memory in large calls, where a value byte is a store of its own, and
+// by the fifteen comparisons of an element.  7375 tokens of 5 prompts, 64 + 8 +
+// 8 heads of 128, bf16: 84 us for 280 MB, 3.3 TB/s, of which the queries are
+// 242 MB; 2532 tokens, 32 + 32 + 32 heads of 64, fp16: 18.5 us; 32 single
+// tokens: 5.4 us, mostly the chain length -> page -> write.  Queries, keys and
+// values are in workgroups of their own, since one loop with all three kept the
+// registers of each (144 and 28 us, with one set of rows a thread).
 template <int DT, int QT, int LPR, int TG>
 __global__ __launch_bounds__(256) void kv_append_kernel(AppendArgs a, int q_iters, int kv_iters) {
   if (blockIdx.z == kKeys) append_rows<DT, QT, LPR, TG, kKeys>(a, kv_iters);
@@ -253,11 +262,12 @@ static int row_lanes(int dim) { return dim <= 32 ? 4 : dim <= 64 ? 8 : dim <= 12
 
 // Calls with fewer new tokens of a sequence take them one by one (64 sequences,
 // 32 + 8 + 8 rows of 128: 4 tokens 9.7 us one by one, 12.0 in groups; 8 tokens
-// 14.0 and 14.9; 2500 tokens of 5 sequences see Place).
+// 14.0 and 14.9; chunks of 1000 tokens at Place).
 constexpr int kGroupFrom = 16;
 
 // Grid and sets of rows of a workgroup: as many sets (up to 16) as leave 8
-// workgroups for each compute unit.
+// workgroups for each compute unit (the two large calls above with 4, 8 and 16:
+// 85.6 and 18.7, 85.4 and 18.1, 82.4 and 20.9 us).
 template <int LPR, int TG>
 static unsigned append_grid(const KVBatch &kb, int rows, int *iters) {
   constexpr int HS = 256 / LPR / TG;
@@ -305,7 +315,12 @@ hipError_t launch_kv_append(const KVCache &c, int dt, int qt, const Midpoints4 &
 }
 
 // ---------------------------------------------------------------------------
-// Reading back: fp32(T[code] * a) rounded to the cache's type.
+// Reading back: fp32(T[code] * a) rounded to the cache's type.  A byte becomes
+// both values by one table read.  Rows go through it as through the append, with
+// the same places and sets.  Bound by the 16-bit writes and, for values, by
+// loads of single bytes 16 apart: the 7375 tokens (8 + 8 heads of 128) 20.1 us
+// for 38 MB, the 2532 tokens (32 + 32 heads of 64) 11.2 us for 27 MB, 32 single
+// tokens 3.8 us.
 // ---------------------------------------------------------------------------
 struct ReadArgs {
   KVCache c;
