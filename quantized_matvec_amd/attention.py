@@ -350,9 +350,12 @@ _WS: dict = {}
 
 def _workspace(nbytes: int, device: torch.device, stream: int) -> Optional[torch.Tensor]:
     """The workspace of one stream (its calls run in order and share it; a
-    larger request replaces it)."""
+    larger request replaces it).  A call that is being captured gets one of its
+    own from the graph's memory, which lives as long as the graph does."""
     if nbytes == 0:
         return None
+    if torch.cuda.is_current_stream_capturing():
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
     key = (device.index, stream)
     ws = _WS.get(key)
     if ws is None or ws.numel() < nbytes:

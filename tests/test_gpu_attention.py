@@ -304,6 +304,35 @@ def test_graph_replays():
         assert torch.equal(out, want), r
 
 
+def test_graphs_keep_their_own_workspace():
+    """A captured call writes into memory of its graph: not into the workspace
+    of the calls outside, and not into that of a graph that is gone."""
+    from quantized_matvec_amd import attention
+    cache, table, K, V = make([3000, 700], 2, 128, 64, 16, "bf16", "nf4", 27)
+    kl = torch.tensor([3000, 700], dtype=torch.int32, device="cuda")
+    q = torch.randn(2, 8, 128, device="cuda").to(torch.bfloat16)
+    want = attention_4bit(q, cache, table, kl, max_kv=3000)
+    long = attention_4bit(q[:1], cache, table[:1], kl[:1], max_kv=3000)
+    torch.cuda.synchronize()
+    before = {k: w.data_ptr() for k, w in attention._WS.items()}
+    graphs, outs = [], []
+    for n in (1, 2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(attention_4bit(q[:n], cache, table[:n], kl[:n], max_kv=3000))
+        graphs.append(g)
+    assert {k: w.data_ptr() for k, w in attention._WS.items()} == before
+    for r in range(3):
+        for g, o, w in zip(graphs, outs, (long, want)):
+            o.zero_()
+            torch.cuda.synchronize()
+            g.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(o, w), r
+        assert torch.equal(attention_4bit(q, cache, table, kl, max_kv=3000), want)
+        torch.cuda.synchronize()
+
+
 def test_refusals():
     cache, table, K, V = make([64], 2, 64, 64, 16, "bf16", "nf4", 23)
     kl = torch.tensor([64], dtype=torch.int32, device="cuda")
