@@ -197,7 +197,7 @@ int qmv_kv_append_4bit(const qmv_kv_cache *cache, const qmv_kv_batch *batch, int
   if (rc == QMV_OK && q) rc = check_heads(q_out, tokens, 2, &hqo);
   if (rc != QMV_OK) return rc;
   if (hk.heads != c.heads || hv.heads != c.heads || hq.heads != hqo.heads) return QMV_ERR_INVALID_ARG;
-  if (kb.max_q > kMost * 7 / (hq.heads + 2 * (int64_t)c.heads)) return QMV_ERR_TOO_LARGE;
+  if (kb.max_q > kMost * 5 / (hq.heads + 2 * (int64_t)c.heads)) return QMV_ERR_TOO_LARGE;
   return launch_status(launch_kv_append(c, cache->dtype, cache->quant_type,
                                         code_midpoints(cache->quant_type), kb, hk, hv, r, hq, hqo,
                                         (hipStream_t)stream));

@@ -137,9 +137,9 @@ struct Place {
   int i;   // token of the sequence, or negative: none
   int h;   // the first row h; further ones HS apart
   int end; // rows of this workgroup end before
-  __device__ __forceinline__ Place(int rows, int iters, const SeqRange &s, int most) {
+  __device__ __forceinline__ Place(unsigned x, int rows, int iters, const SeqRange &s, int most) {
     const int blocks = (rows + HS * iters - 1) / (HS * iters);  // along the rows of a token
-    const int group = (int)(blockIdx.x / (unsigned)blocks), block = (int)(blockIdx.x - (unsigned)group * blocks);
+    const int group = (int)(x / (unsigned)blocks), block = (int)(x - (unsigned)group * blocks);
     const int slot = threadIdx.x / LPR;
     h = block * HS * iters + slot / TG;
     end = (block + 1) * HS * iters < rows ? (block + 1) * HS * iters : rows;
@@ -157,17 +157,22 @@ struct AppendArgs {
   Mids32 mids;
 };
 
-// blockIdx.z: what a workgroup takes, so that its loop over rows is one code
-// for all its waves.
-enum : int { kQueries = 0, kKeys = 1, kValues = 2 };
+// What a workgroup takes, so that its loop over rows is one code for all its
+// waves.
+enum : int { kQueries, kKeys, kValues };
+
+// Tokens side by side for queries, which need no whole groups: four make longer
+// runs of a token's heads (16 for queries too 78.7 us at 7375 tokens of 64
+// query heads, 19.3 at 2532 of 32; 4: 73.9 and 19.8; 1: 82.7 and 22.5).
+constexpr int query_tokens(int tg) { return tg < 4 ? tg : 4; }
 
 template <int DT, int QT, int LPR, int TG, int WHAT>
-__device__ __forceinline__ void append_rows(const AppendArgs &a, int iters) {
+__device__ __forceinline__ void append_rows(const AppendArgs &a, unsigned place, int iters) {
   using P = Place<LPR, TG>;
   const int b = blockIdx.y;
   const SeqRange s = seq_range(a.kb, b);
   const Heads &src = WHAT == kQueries ? a.q : (WHAT == kKeys ? a.k : a.v);
-  const P pl(src.heads, iters, s, a.kb.max_q);
+  const P pl(place, src.heads, iters, s, a.kb.max_q);
   const int e0 = 8 * (int)(threadIdx.x % LPR);
   if (pl.i < 0 || pl.h >= pl.end) return;
   const int pos = s.pos0 + pl.i;
@@ -245,16 +250,19 @@ __device__ __forceinline__ void append_rows(const AppendArgs &a, int iters) {
 
 // Bound by memory in large calls, where a value byte is a store of its own, and
 // by the fifteen comparisons of an element.  7375 tokens of 5 prompts, 64 + 8 +
-// 8 heads of 128, bf16: 84 us for 280 MB, 3.3 TB/s, of which the queries are
-// 242 MB; 2532 tokens, 32 + 32 + 32 heads of 64, fp16: 18.5 us; 32 single
-// tokens: 5.4 us, mostly the chain length -> page -> write.  Queries, keys and
+// 8 heads of 128, bf16: 74 us for 280 MB, 3.8 TB/s, of which the queries are
+// 242 MB; 2532 tokens, 32 + 32 + 32 heads of 64, fp16: 19.5 us; 32 single
+// tokens: 5.1 us, mostly the chain length -> page -> write.  Queries, keys and
 // values are in workgroups of their own, since one loop with all three kept the
-// registers of each (144 and 28 us, with one set of rows a thread).
+// registers of each (144 and 28 us, with one set of rows a thread).  Values,
+// which take longest, come first, and no part's grid is padded to another's
+// (queries first and padded: 84.5 us instead of 79).
 template <int DT, int QT, int LPR, int TG>
-__global__ __launch_bounds__(256) void kv_append_kernel(AppendArgs a, int q_iters, int kv_iters) {
-  if (blockIdx.z == kKeys) append_rows<DT, QT, LPR, TG, kKeys>(a, kv_iters);
-  else if (blockIdx.z == kValues) append_rows<DT, QT, LPR, TG, kValues>(a, kv_iters);
-  else if (a.q.heads) append_rows<DT, QT, LPR, TG, kQueries>(a, q_iters);
+__global__ __launch_bounds__(256) void kv_append_kernel(AppendArgs a, int q_iters, int kv_iters, unsigned kv_grid) {
+  const unsigned x = blockIdx.x;
+  if (x < kv_grid) append_rows<DT, QT, LPR, TG, kValues>(a, x, kv_iters);
+  else if (x < 2 * kv_grid) append_rows<DT, QT, LPR, TG, kKeys>(a, x - kv_grid, kv_iters);
+  else append_rows<DT, QT, LPR, query_tokens(TG), kQueries>(a, x - 2 * kv_grid, q_iters);
 }
 
 // Lanes of a row: head_dim / 8 rounded up to a power of two.
@@ -266,8 +274,9 @@ static int row_lanes(int dim) { return dim <= 32 ? 4 : dim <= 64 ? 8 : dim <= 12
 constexpr int kGroupFrom = 16;
 
 // Grid and sets of rows of a workgroup: as many sets (up to 16) as leave 8
-// workgroups for each compute unit (the two large calls above with 4, 8 and 16:
-// 85.6 and 18.7, 85.4 and 18.1, 82.4 and 20.9 us).
+// workgroups for each compute unit (the two large calls above, all parts in
+// groups of 16, with 4, 8 and 16: 85.6 and 18.7, 85.4 and 18.1, 82.4 and 20.9
+// us; at most 32 sets: 87.2 and 19.5 against 79.1 and 19.1).
 template <int LPR, int TG>
 static unsigned append_grid(const KVBatch &kb, int rows, int *iters) {
   constexpr int HS = 256 / LPR / TG;
@@ -281,11 +290,10 @@ static unsigned append_grid(const KVBatch &kb, int rows, int *iters) {
 template <int DT, int QT, int LPR, int TG>
 static void launch_append_g(const AppendArgs &a, hipStream_t st) {
   int q_iters = 1, kv_iters;
-  unsigned x = append_grid<LPR, TG>(a.kb, a.c.heads, &kv_iters);
-  if (a.q.heads) x = std::max(x, append_grid<LPR, TG>(a.kb, a.q.heads, &q_iters));
-  // workgroups past a part's own grid find no token
-  const dim3 grid(x, (unsigned)a.kb.batch, 3);
-  hipLaunchKernelGGL((kv_append_kernel<DT, QT, LPR, TG>), grid, dim3(256), 0, st, a, q_iters, kv_iters);
+  const unsigned kv_grid = append_grid<LPR, TG>(a.kb, a.c.heads, &kv_iters);
+  const unsigned q_grid = a.q.heads ? append_grid<LPR, query_tokens(TG)>(a.kb, a.q.heads, &q_iters) : 0;
+  const dim3 grid(2 * kv_grid + q_grid, (unsigned)a.kb.batch);
+  hipLaunchKernelGGL((kv_append_kernel<DT, QT, LPR, TG>), grid, dim3(256), 0, st, a, q_iters, kv_iters, kv_grid);
 }
 
 template <int DT, int QT>
@@ -341,7 +349,7 @@ __global__ __launch_bounds__(256) void kv_dequantize_kernel(ReadArgs a, int qt, 
   const int b = blockIdx.y;
   const SeqRange s = seq_range(a.kb, b);
   const bool isv = blockIdx.z != 0;
-  const P pl(a.c.heads, iters, s, a.kb.max_q);
+  const P pl(blockIdx.x, a.c.heads, iters, s, a.kb.max_q);
   const int e0 = 8 * (int)(threadIdx.x % LPR);
   if (pl.i < 0 || e0 >= a.c.dim || pl.h >= pl.end) return;
   const int pos = s.pos0 + pl.i;
