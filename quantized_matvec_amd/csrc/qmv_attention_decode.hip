@@ -752,7 +752,10 @@ __global__ __launch_bounds__(64 * kJoinWaves) void attention_join_kernel(DecodeA
 // sequences of about 4600 tokens, 64 heads over 4 of 128: 16 rows 32 us / 68,
 // 32 rows 49 / 70, 48 rows 66 / 73, so that a fourth tile would be slower; 24
 // sequences of 40 rows, 8 heads of 128: 122 / 264, 32 heads of 64 with fp16 and
-// a window of 4096: 216 / 395.
+// a window of 4096: 216 / 395; heads of 256 in the first call, 32 rows in fp16
+// 98 / 309, 48 rows in bf16 120 / 200.  Where there are hardly any keys the join
+// costs more than it saves (32 prompts of 44 tokens: 15 / 10), the price of one
+// rule for all lengths, which the host knows only a bound of.
 bool decode_eligible(const KVCache &c, int64_t rows) {
   return rows <= 48 && (c.dim == 64 || c.dim == 96 || c.dim == 128 || c.dim == 192 || c.dim == 256);
 }
