@@ -18,10 +18,15 @@
 //    a power of two of their own into fp16's range (their largest scale
 //    becomes 1 .. 2), the values by a running one, weights by 2^14: what falls
 //    below fp16 is 2^-39 of the largest.
-//  * bf16: an fp16 product T a is off by 2^-12 at most, differently for every
-//    scale, so also long sums stay well below the result's rounding.  fp16
-//    (TWO): keys, values and weights keep what fp16 leaves of them in second
-//    planes, since the result would show it.
+//  * bf16: one fp16 term each.  For the values T a that must not mean nearest
+//    rounding: there are few distinct scales and 16 codes, so its errors have a
+//    mean, which adds up over the keys while the values themselves cancel (normal
+//    rows under equal weights: 7e-4 of the result at 2500 keys, 3e-3 at 34000,
+//    5.5e-3 at 131072, where bf16 rounds by 1.7e-3).  They are rounded up or down
+//    by a threshold that goes through the 16 sixteenths of a last place with the
+//    token (dithered_pair): no mean, 2.7e-4 at each of these lengths.  fp16 (TWO):
+//    keys, values and weights keep what fp16 leaves of them in second planes,
+//    since the result would show it.
 // Neighbouring workgroups take neighbouring cache heads, which puts a head's
 // workgroups on one of the eight dies and its keys in that die's L2 cache; the
 // rows that see most keys go first, over all sequences (three prompts 302 us
@@ -55,6 +60,19 @@ struct PromptArgs {
 __host__ __device__ constexpr int prompt_tile(int D, bool two) { return D <= (two ? 96 : 128) ? 64 : 32; }
 // Copies of the code table (float pairs).
 __host__ __device__ constexpr int prompt_copies(int D, bool two) { return two && D > 128 ? 4 : 16; }
+
+// lo and hi of tokens 2 j and 2 j + 1 of a group of 16 as an fp16 pair, a
+// magnitude rounded up where what lies below its last fp16 place is at least 1
+// minus the token's threshold of that place.  Thresholds (2 k + 1) / 32 with k
+// the token's bits reversed: every sixteenth once, neighbours far apart.
+constexpr uint32_t dither(int token) {
+  const int k = (token & 1) << 3 | (token & 2) << 1 | (token & 4) >> 1 | (token & 8) >> 3;
+  return (uint32_t)(2 * k + 1) << 8;  // fp16 drops 13 of fp32's bits
+}
+__device__ __forceinline__ uint32_t dithered_pair(float lo, float hi, int j) {
+  return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(__uint_as_float(__float_as_uint(lo) + dither(2 * j)),
+                                                                __uint_as_float(__float_as_uint(hi) + dither(2 * j + 1))));
+}
 
 template <int D, int DT, bool TWO>
 __global__ __launch_bounds__(kPThreads, 2) void attention_prompt_kernel(PromptArgs pa) {
@@ -256,8 +274,8 @@ __global__ __launch_bounds__(kPThreads, 2) void attention_prompt_kernel(PromptAr
         const float f1 = ldexpf(bits16_to_f32<DT>(sw[j] >> 16), 14 - ev);
         const float2 v0 = tv[2 * j], v1 = tv[2 * j + 1];
         const float e0 = v0.x * f0, e1 = v1.x * f1, o0 = v0.y * f0, o1 = v1.y * f1;
-        w[0][j] = f16_pair(e0, e1);
-        w[1][j] = f16_pair(o0, o1);
+        w[0][j] = TWO ? f16_pair(e0, e1) : dithered_pair(e0, e1, j);
+        w[1][j] = TWO ? f16_pair(o0, o1) : dithered_pair(o0, o1, j);
         if constexpr (TWO) {
           const f16x2v_t he = __builtin_bit_cast(f16x2v_t, w[0][j]), ho = __builtin_bit_cast(f16x2v_t, w[1][j]);
           y[0][j] = f16_pair(e0 - (float)he[0], e1 - (float)he[1]);

@@ -1,0 +1,66 @@
+"""attention_4bit on inputs that its reduced formats could get wrong: sums over
+many keys that cancel.
+
+Relative norms here are over all outputs of a call.  With u the measured error
+of rounding the exact result to the output's type, a kernel whose own error has
+the relative norm e is at sqrt(u^2 + e^2): the two are independent."""
+import numpy as np
+import pytest
+import torch
+
+import kv_reference as R
+from quantized_matvec_amd import KVCache4bit, attention_4bit, kv_append_4bit
+from test_gpu_attention import TDT
+
+pytestmark = pytest.mark.gpu
+i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def filled(L, hk, dim, bs, dt, qt, seed, k_gain=1.0, v_gain=1.0, page=64):
+    """One sequence of L normal rows, appended, and its cached rows in float64 [L, hk, D]."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    rows = lambda gain: (torch.randn(L, hk, dim, generator=g, device="cuda") * gain).to(TDT[dt])
+    pages = -(-L // page)
+    cache = KVCache4bit(pages, hk, page, dim, bs, qt, TDT[dt])
+    table = torch.randperm(pages, generator=g, device="cuda").to(torch.int32)[None]
+    kv_append_4bit(cache, rows(k_gain), rows(v_gain), table, i32([L]), cu_q=i32([0, L]))
+    return cache, table, *cached(cache, table, L)
+
+
+def cached(cache, table, L):
+    pages = table[0].cpu().numpy()
+    kc = cache.k_codes.cpu().numpy()[pages].transpose(0, 2, 1, 3)
+    vc = cache.v_codes.cpu().numpy()[pages].transpose(0, 2, 4, 1, 3)
+    out = []
+    for codes, scales in ((kc, cache.k_scales), (vc, cache.v_scales)):
+        codes = codes.reshape(-1, cache.heads, cache.head_dim // 2)[:L]
+        s = scales.double().cpu().numpy()[pages].transpose(0, 3, 1, 2).reshape(-1, cache.heads, scales.shape[2])[:L]
+        out.append(R.decode_rows(np.ascontiguousarray(codes), np.ascontiguousarray(s), cache.quant_type))
+    return out
+
+
+def norms(got, want, dt):
+    """Relative norms of got's error and of rounding want to the type."""
+    rounded = torch.from_numpy(want).to(TDT[dt]).double().numpy()
+    size = np.linalg.norm(want)
+    return np.linalg.norm(got.double().cpu().numpy() - want) / size, np.linalg.norm(rounded - want) / size
+
+
+# --------------------------------------------------------------------------
+@pytest.mark.parametrize("new", [1, 16, 64])
+@pytest.mark.parametrize("dt,qt,bs", [("bf16", "nf4", 64), ("bf16", "nf4", 128), ("bf16", "fp4", 64), ("fp16", "nf4", 64)])
+def test_cancelling_sums_do_not_drift(new, dt, qt, bs):
+    """Uniform weights over 65536 normal rows, whose sum is 1/256 of their
+    size: an error of the values with a mean would be 256 times as large in it.
+    The kernel's own error: one fp16 rounding of a value by at most a unit of
+    the last place (2^-10 / sqrt 6 of the value at most, 3e-4 on average) for
+    bf16, second terms for fp16; fp32 sums of 65536 terms 2^-24 sqrt(65536) =
+    1.5e-5 of the running sum."""
+    L, dim = 65536, 128
+    cache, table, _, V = filled(L, 1, dim, bs, dt, qt, new + bs)
+    want = np.broadcast_to(V.mean(0), (new, 1, dim))
+    assert np.linalg.norm(want) < 0.01 * np.sqrt(new * dim)
+    q = torch.zeros(new, 1, dim, dtype=TDT[dt], device="cuda")
+    got = attention_4bit(q, cache, table, i32([L]), cu_q=i32([0, new]), max_q=new, causal=False)
+    err, u = norms(got, want, dt)
+    assert err <= np.hypot(u, 5e-4 if dt == "bf16" else 5e-5), (err, u)
