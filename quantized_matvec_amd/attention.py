@@ -21,6 +21,7 @@ most tokens of one sequence.
 from __future__ import annotations
 
 import ctypes
+import threading
 from typing import Optional
 
 import torch
@@ -345,23 +346,33 @@ def kv_dequantize_4bit(cache: KVCache4bit, block_table: torch.Tensor, kv_len: to
 # --------------------------------------------------------------------------
 # attention
 # --------------------------------------------------------------------------
-_WS: dict = {}
+_WS: dict = {}        # (device, stream) -> workspace
+_WS_LOCKS: dict = {}
 
 
-def _workspace(nbytes: int, device: torch.device, stream: int) -> Optional[torch.Tensor]:
-    """The workspace of one stream (its calls run in order and share it; a
-    larger request replaces it).  A call that is being captured gets one of its
-    own from the graph's memory, which lives as long as the graph does."""
-    if nbytes == 0:
-        return None
-    if torch.cuda.is_current_stream_capturing():
-        return torch.empty(nbytes, dtype=torch.uint8, device=device)
-    key = (device.index, stream)
+def _workspace(nbytes: int, device: torch.device, key) -> torch.Tensor:
+    """The workspace of one stream; a larger request replaces it."""
     ws = _WS.get(key)
     if ws is None or ws.numel() < nbytes:
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
-        _WS[key] = ws
+        ws = _WS[key] = torch.empty(nbytes, dtype=torch.uint8, device=device)
     return ws
+
+
+def _with_workspace(nbytes: int, device: torch.device, stream: int, enqueue) -> int:
+    """enqueue(pointer of a workspace, or None).  Calls on a stream share its
+    workspace and run in order there; a call is several kernels, so from the
+    look at the workspace until they are all enqueued no other thread's call
+    may enqueue any on this stream.  A call that is being captured gets a
+    workspace of its own from the graph's memory, which lives as long as the
+    graph does."""
+    if nbytes == 0:
+        return enqueue(None)
+    if torch.cuda.is_current_stream_capturing():
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        return enqueue(ws.data_ptr())
+    key = (device.index, stream)
+    with _WS_LOCKS.get(key) or _WS_LOCKS.setdefault(key, threading.RLock()):
+        return enqueue(_workspace(nbytes, device, key).data_ptr())
 
 
 def attention_4bit(q: torch.Tensor, cache: KVCache4bit, block_table: torch.Tensor, kv_len: torch.Tensor,
@@ -385,8 +396,7 @@ def attention_4bit(q: torch.Tensor, cache: KVCache4bit, block_table: torch.Tenso
     cache_p, kb_p, st = _ref(cache._c), _ref(kb), _stream(q)
     max_kv = 0 if max_kv is None else max(int(max_kv), 1)
     n = L.qmv_attention_4bit_workspace(cache_p, kb_p, tokens, heads, max_kv, window)
-    ws = _workspace(n, q.device, st)
-    _check(L.qmv_attention_4bit(_ref(hq), cache_p, kb_p, tokens, max_kv, dim ** -0.5 if scale is None else scale,
-                                int(causal), window, _ref(ho), None if ws is None else ws.data_ptr(), n, st),
-           "attention_4bit")
+    scale = dim ** -0.5 if scale is None else scale
+    _check(_with_workspace(n, q.device, st, lambda ws: L.qmv_attention_4bit(
+        _ref(hq), cache_p, kb_p, tokens, max_kv, scale, int(causal), window, _ref(ho), ws, n, st)), "attention_4bit")
     return out
