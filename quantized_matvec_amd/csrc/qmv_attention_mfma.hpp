@@ -23,13 +23,15 @@ struct AttnArgs {
   int qt;
 };
 
-// Keys [lo, hi) that token i of the sequence sees.
+// Keys [lo, hi) that token i of the sequence sees.  Both are within max_kv (below
+// 2^31 - 1024, so positions a step past them do not overflow), whatever kv_len says.
 __device__ __forceinline__ void key_range(const AttnArgs &a, const SeqRange &s, int i, int &lo,
                                           int &hi) {
   const int pos = s.pos0 + i;
   const int len = s.len < a.max_kv ? s.len : a.max_kv;
   hi = a.causal ? (pos + 1 < len ? pos + 1 : len) : len;
   lo = a.window > 0 && pos >= a.window ? pos - a.window + 1 : 0;
+  lo = lo < len ? lo : len;
 }
 
 // The code values in fp16, times a factor: with 11 significant bits the NF4
