@@ -57,7 +57,9 @@ typedef enum {
                            is stretched by factor, the fastest not at all */
   QMV_ROPE_BANDS = 3    /* pairs that turn more than beta_fast times in original_len positions keep
                            their frequency, those that turn fewer than beta_slow times are divided by
-                           factor, in between the two are mixed linearly in the pair's index */
+                           factor, in between the two are mixed linearly in the pair's index (from the
+                           last index of the first kind to the first of the second, also where these
+                           lie outside the pairs) */
 } qmv_rope_scaling;
 
 /* Host-side: freqs [rot_dim / 2] float64 out.  factor >= 1 (ignored for

@@ -128,8 +128,9 @@ int qmv_rope_frequencies(int32_t rot_dim, double theta, qmv_rope_scaling scaling
     auto index = [&](double beta) {
       return 0.5 * rot_dim * log((double)original_len / (two_pi * beta)) / log(theta);
     };
-    first = fmax(floor(index(beta_fast)), 0.0);
-    last = fmin(ceil(index(beta_slow)), rot_dim / 2 - 1.0);
+    // not clipped to the pairs there are: that would turn the line between
+    first = floor(index(beta_fast));
+    last = ceil(index(beta_slow));
     if (last <= first) last = first + 1e-3;
   }
   for (int i = 0; i < rot_dim / 2; ++i) {
