@@ -15,9 +15,11 @@
 //    running maxima, sums and rescaling are of the lane's own row.
 //  * Key and value scales are multiplied into the tiles, so no score needs
 //    more than the exponential's own multiply-add.  A tile's keys are taken by
-//    a power of two of their own into fp16's range (their largest scale
-//    becomes 1 .. 2), the values by a running one, weights by 2^14: what falls
-//    below fp16 is 2^-39 of the largest.
+//    a power of two of their own to the top of fp16's range (their largest
+//    scale becomes 2^14 .. 2^15), the values by a running one, weights by 2^14.
+//    That power is shared by all tokens of the tile (of the tiles so far), seen
+//    or not, so keys and values down to 2^-28 of the largest keep all of fp16's
+//    bits, smaller ones lose them, and below 2^-39 nothing is left.
 //  * bf16: one fp16 term each.  For the values T a that must not mean nearest
 //    rounding: there are few distinct scales and 16 codes, so its errors have a
 //    mean, which adds up over the keys while the values themselves cancel (normal
@@ -246,7 +248,7 @@ __global__ __launch_bounds__(kPThreads, 2) void attention_prompt_kernel(PromptAr
     for (int j = 0; j < 16; ++j) tv[j] = my_lut[((c[j >> 2] >> (8 * (j & 3))) & 0xffu) * COPIES];
     __builtin_amdgcn_sched_barrier(0);
     if (isk) {
-      const float f = ldexpf(bits16_to_f32<DT>(s0.x), -ek);
+      const float f = ldexpf(bits16_to_f32<DT>(s0.x), 14 - ek);
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
         uint32_t w[4], y[4];
@@ -375,7 +377,7 @@ __global__ __launch_bounds__(kPThreads, 2) void attention_prompt_kernel(PromptAr
           swap32(p, q);
           top = fmaxf(__uint_as_float(p), __uint_as_float(q));
         }
-        const float f = fmaxf(ldexpf(qscale, ek), 0x1p-100f);  // never 0: a masked score stays -inf
+        const float f = fmaxf(ldexpf(qscale, ek - 14), 0x1p-100f);  // never 0: a masked score stays -inf
         top *= f;
         if (__any(top > mx)) {
           const float mn = fmaxf(mx, top);

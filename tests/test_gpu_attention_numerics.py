@@ -1,5 +1,5 @@
 """attention_4bit on inputs that its reduced formats could get wrong: sums over
-many keys that cancel.
+many keys that cancel, keys and values of very different size side by side.
 
 Relative norms here are over all outputs of a call.  With u the measured error
 of rounding the exact result to the output's type, a kernel whose own error has
@@ -10,7 +10,7 @@ import torch
 
 import kv_reference as R
 from quantized_matvec_amd import KVCache4bit, attention_4bit, kv_append_4bit
-from test_gpu_attention import TDT
+from test_gpu_attention import TDT, check
 
 pytestmark = pytest.mark.gpu
 i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
@@ -64,3 +64,35 @@ def test_cancelling_sums_do_not_drift(new, dt, qt, bs):
     got = attention_4bit(q, cache, table, i32([L]), cu_q=i32([0, new]), max_q=new, causal=False)
     err, u = norms(got, want, dt)
     assert err <= np.hypot(u, 5e-4 if dt == "bf16" else 5e-5), (err, u)
+
+
+# --------------------------------------------------------------------------
+@pytest.mark.parametrize("new", [[300], [12]])
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+@pytest.mark.parametrize("dim,bs", [(64, 32), (128, 128), (256, 64)])
+def test_a_large_key_leaves_rows_before_it_alone(new, dt, dim, bs):
+    """Keys 2^20 times as large as their neighbours: hidden from the rows
+    before them, whose scores are those of the small keys."""
+    at = [300 - new[0] + 9, 299] if new[0] < 300 else [20, 100, 230, 299]
+
+    def gain(n, isv):
+        a = np.ones(n)
+        if not isv:
+            a *= 2.0 ** -10
+            a[at] = 2.0 ** 10
+        return a
+    check([300], new, 4, 2, dim, bs, 16, dt, seed=dim, scale_gain=gain, scale=dim ** -0.5 * 2.0 ** 10)
+
+
+@pytest.mark.parametrize("new", [[300], [12]])
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+def test_a_large_value_leaves_rows_before_it_alone(new, dt):
+    at = [300 - new[0] + 9, 299] if new[0] < 300 else [20, 100, 230, 299]
+
+    def gain(n, isv):
+        a = np.ones(n)
+        if isv:
+            a *= 2.0 ** -10
+            a[at] = 2.0 ** 10
+        return a
+    check([300], new, 4, 2, 64, 64, 16, dt, seed=64, scale_gain=gain)
