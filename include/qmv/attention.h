@@ -192,7 +192,14 @@ int qmv_kv_dequantize_4bit(const qmv_kv_cache *cache, const qmv_kv_batch *batch,
  *   window    0, or with causal: only keys j > p - window
  * A row that sees no key (an empty sequence, a negative position, pages that
  * are not there) is zeros.  Codes and scales of tokens past kv_len may hold
- * anything.
+ * anything.  A key or value that is not finite concerns the rows that see it,
+ * with one exception: where a sequence has more than 48 query rows of a cache
+ * head (max_q times q_heads / heads), a value's block of elements may be NaN in
+ * rows that do not see it too.
+ * Keys and values are taken to fp16 by a power of two that is shared by 64
+ * tokens or more, seen or not: those below 2^-28 of the largest lose bits,
+ * those below 2^-38 count as zeros.  (Keys up to 48 query rows are exempt.)
+ * 2^100 and more is outside the range of values.
  *   workspace  device scratch of at least qmv_attention_4bit_workspace(...)
  *              bytes for the same arguments, 16-byte aligned, any contents
  *              (NULL when that is 0): partial results where the keys of a

@@ -195,6 +195,7 @@ __global__ __launch_bounds__(64 * decode_waves(D), decode_waves(D) / 4) void att
   constexpr int QR = 4 * RJ;       // query rows
   constexpr int JW = 32 + 4;       // row stride of the join buffer (floats)
   constexpr int PB = DT == kF16 ? 2 : 1;  // fp16 terms of a weight
+  constexpr uint32_t kInf16 = DT == kF16 ? 0x7c00u : 0x7f80u;
   constexpr int row_bytes = D / 2;
   __shared__ __align__(256) uint32_t lut[kLutBytes / 4];
   union Scratch {
@@ -457,7 +458,8 @@ __global__ __launch_bounds__(64 * decode_waves(D), decode_waves(D) / 4) void att
           vm = __builtin_elementwise_max(vm, __builtin_bit_cast(u16x2_t, (uint32_t)vs[n].y));
         }
         const float vmax = bits16_to_f32<DT>(vm[0] > vm[1] ? vm[0] : vm[1]);
-        const bool high = ldexpf(vmax, ev) >= 0x1p15f;
+        const bool high = !(ldexpf(vmax, ev) < 0x1p15f);
+        bool odd = false;  // the step has a value scale that is not finite: 0 times it is 0
         float top[RJ];
         bool grows = high;
 #pragma unroll
@@ -468,8 +470,22 @@ __global__ __launch_bounds__(64 * decode_waves(D), decode_waves(D) / 4) void att
         }
         if (__any(grows)) {
           int en = ev;
-          if (__any(high)) {  // a power of two with the largest scale in [2^14, 2^15)
-            en = 14 - exponent_of(rows_max(group_max(vmax, 16)));
+          if (__any(high)) {
+            // a power of two with the largest scale in [2^14, 2^15).  One that is
+            // not finite counts for nothing: it is the business of the rows that
+            // see it, and its exponent would leave zeros of all else
+            odd = __any(vm[0] >= kInf16 || vm[1] >= kInf16);
+            uint32_t most = 0;
+#pragma unroll
+            for (int n = 0; n < NB; ++n) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const uint32_t x = (i & 2 ? vs[n].y : vs[n].x) >> (i & 1 ? 16 : 0) & 0xffffu;
+                most = x < kInf16 && x > most ? x : most;
+              }
+            }
+            const float big = rows_max(group_max(bits16_to_f32<DT>(most), 16));
+            if (ldexpf(big, ev) >= 0x1p15f) en = 14 - exponent_of(big);
             en = en < -100 ? -100 : (en > 100 ? 100 : en);
           }
 #pragma unroll
@@ -505,6 +521,11 @@ __global__ __launch_bounds__(64 * decode_waves(D), decode_waves(D) / 4) void att
             float w[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) w[i] = s[j][i] * scale_at<DT>(vs[n], i);
+            if (odd) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) w[i] = s[j][i] == 0.f ? 0.f : w[i];
+              asm volatile("" : "+v"(w[0]));  // a branch that is hardly ever taken, not eight selects
+            }
             const uint32_t h0 = f16_pair(w[0], w[1]), h1 = f16_pair(w[2], w[3]);
             *reinterpret_cast<uint2 *>(&sh.p[wave][0][g * RJ + j][4 * r]) = make_uint2(h0, h1);
             if constexpr (DT == kF16) {

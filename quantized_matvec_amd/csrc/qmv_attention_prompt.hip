@@ -210,13 +210,16 @@ __global__ __launch_bounds__(kPThreads, 2) void attention_prompt_kernel(PromptAr
     }
   };
   // scales of tokens that no row sees (which may hold anything) become 0; the
-  // largest of the wave's is told to the others
+  // largest of the wave's is told to the others.  One that is not finite counts
+  // for nothing there: it is the business of the rows that see it, and taking
+  // the tile down by its exponent would leave zeros of all else.
+  constexpr uint32_t kInf16 = DT == kF16 ? 0x7c00u : 0x7f80u;
   auto publish = [&](int t, int buf, int slot) {
     const int tok = lo + t * KT + my_tok;
     uint32_t big = 0;
     if (isk) {
       s0.x = page_ok ? s0.x & 0xffffu : 0u;
-      big = s0.x;
+      big = s0.x < kInf16 ? s0.x : 0u;
       if (kch == 0 && (ktok & 15) == 0) there[slot][ktok >> 4] = page_ok;
     } else if (isv) {
       uint32_t w[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
@@ -230,6 +233,16 @@ __global__ __launch_bounds__(kPThreads, 2) void attention_prompt_kernel(PromptAr
       s1 = make_uint4(w[4], w[5], w[6], w[7]);
     }
     big = (uint32_t)wave_max_i32((int)big);
+    if (big >= kInf16) {  // values: not looked at one by one above
+      big = 0;
+      const uint32_t w[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const uint32_t a = w[j] & 0xffffu, b = w[j] >> 16;
+        big = max(big, max(a < kInf16 ? a : 0u, b < kInf16 ? b : 0u));
+      }
+      big = (uint32_t)wave_max_i32((int)big);
+    }
     if (lane == 0 && isk) kmax[buf][wave] = big;
     if (lane == 0 && isv) vmax[buf][wave - NU / 64] = big;
   };
@@ -237,7 +250,7 @@ __global__ __launch_bounds__(kPThreads, 2) void attention_prompt_kernel(PromptAr
     const uint4 w = *reinterpret_cast<const uint4 *>(x);
     const uint32_t big = max(max(w.x, w.y), max(w.z, w.w));
     int e = __builtin_amdgcn_readfirstlane(exponent_of(bits16_to_f32<DT>(big)));
-    return e < -100 ? -100 : (e > 100 ? 100 : e);
+    return e < -100 ? -100 : e;
   };
   // T[code] * scale of the unit into LDS
   const float2 *my_lut = lut + (lane & (COPIES - 1));

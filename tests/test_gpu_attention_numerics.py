@@ -1,5 +1,6 @@
 """attention_4bit on inputs that its reduced formats could get wrong: sums over
-many keys that cancel, keys and values of very different size side by side.
+many keys that cancel, keys and values of very different size side by side,
+infinities and NaN in keys and values that a row does not see.
 
 Relative norms here are over all outputs of a call.  With u the measured error
 of rounding the exact result to the output's type, a kernel whose own error has
@@ -10,7 +11,7 @@ import torch
 
 import kv_reference as R
 from quantized_matvec_amd import KVCache4bit, attention_4bit, kv_append_4bit
-from test_gpu_attention import TDT, check
+from test_gpu_attention import TDT, check, make
 
 pytestmark = pytest.mark.gpu
 i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
@@ -96,3 +97,32 @@ def test_a_large_value_leaves_rows_before_it_alone(new, dt):
             a[at] = 2.0 ** 10
         return a
     check([300], new, 4, 2, 64, 64, 16, dt, seed=64, scale_gain=gain)
+
+
+# --------------------------------------------------------------------------
+@pytest.mark.parametrize("what", ["k", "v"])
+@pytest.mark.parametrize("bits", ["inf", "nan"])
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+@pytest.mark.parametrize("new,bad", [([4], 299), ([4], 297), ([12], 291), ([40], 270), ([300], 100), ([300], 290)])
+def test_a_key_or_value_that_is_not_finite(new, bad, dt, bits, what):
+    """Rows before such a key are as without it, and so are rows before such a
+    value up to 48 rows of a cache head; elements outside the value's block are
+    as they would be in every row."""
+    lens, hq, hk, dim, bs = [300], 2, 2, 128, 64
+    cache, table, K, V = make(lens, hk, dim, bs, 16, dt, "nf4", 77)
+    page, at = int(table[0, bad // 16]), bad % 16
+    scales = cache.k_scales if what == "k" else cache.v_scales
+    scales[page, :, 0, at] = float(bits)           # of the first block of 64 elements
+    q = torch.randn(new[0], hq, dim, generator=torch.Generator().manual_seed(3)).to(TDT[dt]).cuda()
+    got = attention_4bit(q, cache, table, i32(lens), cu_q=i32([0] + new), max_q=new[0])
+    got = got.double().cpu().numpy()
+    pos = lens[0] - new[0] + np.arange(new[0])
+    for h in range(hk):
+        ref, bound = R.attend(q[:, h].double().cpu().numpy(), K[0][:, h], V[0][:, h], dim ** -0.5, np.zeros(new[0], int), pos + 1)
+        ok = np.abs(got[:, h] - ref) <= 1.01 * (bound + R.U_OUT[dt] * np.abs(ref) + R.SUBNORMAL[dt])
+        before = pos < bad
+        if what == "k" or new[0] <= 48:
+            assert ok[before].all()
+        if what == "v":
+            assert ok[:, 64:].all()
+            assert not np.isfinite(got[~before, h, :64]).any()
