@@ -399,7 +399,8 @@ __global__ __launch_bounds__(64 * decode_waves(D), decode_waves(D) / 4) void att
     float m[RJ], l[RJ];
 #pragma unroll
     for (int j = 0; j < RJ; ++j) m[j] = kNoScore, l[j] = 0.f;
-    int ev = 100;  // weights are scaled by 2^ev
+    int ev = 100;      // weights are scaled by 2^ev
+    bool far = false;  // a row's maximum is_far
     {
       for (; t < t_to; ++t) {
         const int t0 = q.lo + t * kStep;
@@ -497,6 +498,10 @@ __global__ __launch_bounds__(64 * decode_waves(D), decode_waves(D) / 4) void att
             if (r == 0) jm[wave][g * RJ + j] = keep;
           }
           ev = en;
+          far = false;
+#pragma unroll
+          for (int j = 0; j < RJ; ++j) far |= is_far(m[j]);
+          far = __any(far);
           const float keep = jm[wave][r % QR];  // of the output's column
 #pragma unroll
           for (int c = 0; c < KU; ++c) {
@@ -505,12 +510,18 @@ __global__ __launch_bounds__(64 * decode_waves(D), decode_waves(D) / 4) void att
           }
         }
         // ---- weights, and the products with the values ----
+        if (far) {
+#pragma unroll
+          for (int j = 0; j < RJ; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[j][i] = s[j][i] * qscale[j] - m[j];
+        }
 #pragma unroll
         for (int j = 0; j < RJ; ++j) {
-          const float shift = (float)ev - m[j];
+          const float f = far ? 1.f : qscale[j], shift = far ? (float)ev : (float)ev - m[j];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            s[j][i] = __builtin_amdgcn_exp2f(fmaf(s[j][i], qscale[j], shift));
+            s[j][i] = __builtin_amdgcn_exp2f(fmaf(s[j][i], f, shift));
             l[j] += s[j][i];
           }
         }

@@ -193,7 +193,14 @@ __device__ __forceinline__ int exponent_of(float x) {
   return (int)((__float_as_uint(x) >> 23) & 0xffu) - 127;
 }
 
-constexpr float kNoScore = -1e30f;  // running maximum of a row that has seen nothing
+constexpr float kNoScore = -3e38f;  // running maximum of a row that has seen nothing
+
+// A score's exponent s f - m is one multiply-add.  Its product is not rounded
+// and m, the largest product, is, so all weights of a row carry a factor of up to
+// 2^(|m| 2^-24): nothing below this |m|, past it more than fp16 has room for.
+// There products are rounded before m is taken from them.
+constexpr float kFarScore = 0x1p20f;
+__device__ __forceinline__ bool is_far(float m) { return fabsf(m) >= kFarScore && m > kNoScore; }
 
 // Results of a part of a row's keys: running maximum (in powers of two), sum of
 // weights, and the weighted sum of values (not divided).

@@ -316,6 +316,7 @@ __global__ __launch_bounds__(kPThreads, 2) void attention_prompt_kernel(PromptAr
   for (int d = 0; d < DTI; ++d) acc[d] = f32x16_t{};
   float mx = kNoScore, l = 0.f;
   int ev = -100;
+  bool far = false;  // a row's maximum is_far
 
   if (t_from < t_to) {
     const int t_last = t_to - 1;
@@ -396,18 +397,25 @@ __global__ __launch_bounds__(kPThreads, 2) void attention_prompt_kernel(PromptAr
           const float mn = fmaxf(mx, top);
           const float keep = __builtin_amdgcn_exp2f(mx - mn);
           mx = mn;
+          far = __any(is_far(mx));
           l *= keep;
 #pragma unroll
           for (int d = 0; d < DTI; ++d) acc[d] *= keep;
         }
         // ---- weights (times 2^14) and the products with the values ----
-        const float shift = 14.f - mx;
+        if (far) {
+#pragma unroll
+          for (int x = 0; x < TT; ++x)
+#pragma unroll
+            for (int j = 0; j < 16; ++j) sc[x][j] = sc[x][j] * f - mx;
+        }
+        const float fm = far ? 1.f : f, shift = far ? 14.f : 14.f - mx;
         float sum = 0.f;
 #pragma unroll
         for (int x = 0; x < TT; ++x)
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
-            sc[x][j] = __builtin_amdgcn_exp2f(fmaf(sc[x][j], f, shift));
+            sc[x][j] = __builtin_amdgcn_exp2f(fmaf(sc[x][j], fm, shift));
             sum += sc[x][j];
           }
         l += sum;

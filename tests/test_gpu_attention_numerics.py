@@ -1,6 +1,7 @@
 """attention_4bit on inputs that its reduced formats could get wrong: sums over
 many keys that cancel, keys and values of very different size side by side,
-infinities and NaN in keys and values that a row does not see.
+infinities and NaN in keys and values that a row does not see, very large
+scores.
 
 Relative norms here are over all outputs of a call.  With u the measured error
 of rounding the exact result to the output's type, a kernel whose own error has
@@ -126,3 +127,45 @@ def test_a_key_or_value_that_is_not_finite(new, bad, dt, bits, what):
         if what == "v":
             assert ok[:, 64:].all()
             assert not np.isfinite(got[~before, h, :64]).any()
+
+
+# --------------------------------------------------------------------------
+@pytest.mark.parametrize("lens,new,dim", [([300, 40], [1, 1], 128), ([300, 40], [9, 40], 128), ([300, 130], [90, 130], 64),
+                                          ([300, 130], [3, 130], 256), ([300, 40], [5, 40], 32), ([9000], [1], 64)])
+@pytest.mark.parametrize("dt,q_gain,k_gain", [("fp16", 2.0 ** 8, 2.0 ** 8), ("fp16", 2.0 ** 13, 2.0 ** 13), ("bf16", 2.0 ** 40, 2.0 ** 40),
+                                              ("bf16", 2.0 ** 52, 2.0 ** 53)])
+def test_large_scores_pick_one_key(lens, new, dim, dt, q_gain, k_gain):
+    """Scores so far apart (2^20 and more) that the weights are one 1 and
+    zeros: the result is the value of the best key, whatever its score's sign
+    and size.  Rows whose best two keys are closer than the keys' rounding
+    (6e-5 of the scores' size, taken tenfold) are left out."""
+    cu = np.concatenate([[0], np.cumsum(new)])
+    parts = [filled(n, 2, dim, 32, dt, "nf4", 7 + n, k_gain=k_gain, page=64) for n in lens]
+    pages = [p[1].shape[1] for p in parts]
+    cat = lambda name: torch.cat([getattr(p[0], name) for p in parts])
+    cache = KVCache4bit.from_tensors(cat("k_codes"), cat("k_scales"), cat("v_codes"), cat("v_scales"))
+    table = torch.full((len(lens), max(pages)), -1, dtype=torch.int32, device="cuda")
+    for b, p in enumerate(parts):
+        table[b, :pages[b]] = p[1][0] + sum(pages[:b])
+    q = (torch.randn(cu[-1], 4, dim, device="cuda", generator=torch.Generator(device="cuda").manual_seed(dim)) * q_gain).to(TDT[dt])
+    got = attention_4bit(q, cache, table, i32(lens), cu_q=i32(cu.tolist()), max_q=max(new)).double().cpu().numpy()
+    qd = q.double().cpu().numpy()
+    tested = negative = 0
+    for b, n in enumerate(new):
+        _, _, K, V = parts[b]
+        for i in range(n):
+            hi = lens[b] - n + i + 1
+            for h in range(4):
+                s = K[:hi, h // 2] @ qd[cu[b] + i, h]
+                order = np.argsort(s)
+                size = np.sqrt((K[:hi, h // 2] ** 2).sum(1).max() * (qd[cu[b] + i, h] ** 2).mean())
+                if hi > 1 and s[order[-1]] - s[order[-2]] < 6e-4 * size:
+                    continue
+                want = V[order[-1], h // 2]
+                have = got[cu[b] + i, h]
+                # one fp16 rounding of the value and one of the result
+                assert np.all(np.abs(have - want) <= (R.U_OUT[dt] + 2.0 ** -10) * np.abs(want) + R.SUBNORMAL[dt]), (b, i, h)
+                tested += 1
+                negative += s[order[-1]] < 0
+    assert tested > 0.9 * 4 * cu[-1]
+    assert negative > 0 or lens[-1] != new[-1]
