@@ -146,7 +146,9 @@ def _rope(table: torch.Tensor, interleaved: bool, device) -> _Rope:
 
 
 class KVCache4bit:
-    """A paged cache of 4-bit keys and values (layout: include/qmv/attention.h).
+    """A paged cache of 4-bit keys and values (layout and sizes:
+    include/qmv/attention.h).  ``blocksize`` divides ``head_dim``: heads of 96
+    or 160 have blocks of 32.
 
     ``k_codes`` / ``v_codes`` uint8 and ``k_scales`` / ``v_scales`` in
     ``dtype``, the 16-bit type of the keys, values and queries."""
@@ -154,6 +156,10 @@ class KVCache4bit:
     def __init__(self, num_pages: int, heads: int, page_size: int, head_dim: int,
                  blocksize: int = 64, quant_type: str = "nf4",
                  dtype: torch.dtype = torch.bfloat16, device="cuda"):
+        if head_dim <= 0 or head_dim % 2 or blocksize <= 0 or head_dim % blocksize:
+            raise ValueError(f"blocksize must divide head_dim, an even number: got {blocksize} and {head_dim}")
+        if page_size <= 0 or page_size % 16:
+            raise ValueError(f"page_size must be a multiple of 16, got {page_size}")
         shape = (num_pages, heads, page_size, head_dim // 2)
         sshape = (num_pages, heads, head_dim // blocksize, page_size)
         kc = torch.zeros(shape, dtype=torch.uint8, device=device)
