@@ -21,12 +21,13 @@ most tokens of one sequence.
 from __future__ import annotations
 
 import ctypes
+import operator
 import threading
 from typing import Optional
 
 import torch
 
-from .qmv import _DT, _QT, _check, _stream as _stream_of, lib as _lib
+from .qmv import _DT, _QT, QmvError, _check, _stream as _stream_of, lib as _lib
 
 __all__ = ["KVCache4bit", "attention_4bit", "kv_append_4bit", "kv_dequantize_4bit",
            "rope_frequencies", "rope_table", "rotary", "rotary_backward"]
@@ -204,6 +205,15 @@ class KVCache4bit:
                    for t in (self.k_codes, self.k_scales, self.v_codes, self.v_scales))
 
 
+def _size(value, name: str, least: int) -> int:
+    """A count from the caller, cut off where the library's 32 bits end (no
+    sequence is longer): ctypes would keep its low bits."""
+    value = operator.index(value)
+    if value < least:
+        raise QmvError(-1, f"{name} must be at least {least}, got {value}")
+    return min(value, 2 ** 31 - 1)
+
+
 def _batch(cache: KVCache4bit, block_table, kv_len, cu_q, max_q, tokens: int) -> _Batch:
     dev = cache.device
     shape = block_table.shape
@@ -224,7 +234,7 @@ def _batch(cache: KVCache4bit, block_table, kv_len, cu_q, max_q, tokens: int) ->
         if cu_q.shape != (n + 1,) or cu_q.dtype != torch.int32 or cu_q.device != dev or not cu_q.is_contiguous():
             raise ValueError(f"cu_q must be contiguous int32 [{n + 1}] on the cache's device")
         cu = cu_q.data_ptr()
-        max_q = tokens if max_q is None else max_q
+        max_q = tokens if max_q is None else _size(max_q, "max_q", 1)
     return _Batch(block_table.data_ptr(), stride, kv_len.data_ptr(), cu, n, pages, max_q)
 
 
@@ -400,7 +410,8 @@ def attention_4bit(q: torch.Tensor, cache: KVCache4bit, block_table: torch.Tenso
         return out
     L = lib()
     cache_p, kb_p, st = _ref(cache._c), _ref(kb), _stream(q)
-    max_kv = 0 if max_kv is None else max(int(max_kv), 1)
+    max_kv = 0 if max_kv is None else max(_size(int(max_kv), "max_kv", 0), 1)
+    window = _size(window, "window", 0)
     n = L.qmv_attention_4bit_workspace(cache_p, kb_p, tokens, heads, max_kv, window)
     scale = dim ** -0.5 if scale is None else scale
     _check(_with_workspace(n, q.device, st, lambda ws: L.qmv_attention_4bit(

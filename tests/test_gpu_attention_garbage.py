@@ -1,9 +1,10 @@
-"""attention_4bit with device-side lengths that no cache holds: nothing outside
-the operands is read, and what the other sequences get is right."""
+"""attention_4bit with device-side lengths that no cache holds (nothing outside
+the operands is read, and what the other sequences get is right) and with
+host-side sizes that no integer of the library holds."""
 import pytest
 import torch
 
-from quantized_matvec_amd import attention_4bit
+from quantized_matvec_amd import attention_4bit, qmv
 from test_gpu_attention import make
 
 pytestmark = pytest.mark.gpu
@@ -30,3 +31,21 @@ def test_lengths_past_the_table_with_a_window(new, dim, window):
             assert torch.allclose(out[new:].float(), want[new:].float(), rtol=2.0 ** -7, atol=4e-3)
             if length - new - window > 112:      # 7 pages of 16: the window is past them
                 assert (out[:new] == 0).all()
+
+
+def test_windows_and_bounds_past_the_integers_are_unlimited():
+    """A window or a bound of the lengths that passes 64 bits is a large one, not its low bits."""
+    cache, table, _, _ = make([500, 100], 2, 64, 32, 16, "bf16", "nf4", 62)
+    kl = torch.tensor([500, 100], dtype=torch.int32, device="cuda")
+    cu = torch.tensor([0, 3, 5], dtype=torch.int32, device="cuda")
+    q = torch.randn(5, 4, 64, device="cuda").to(torch.bfloat16)
+    call = lambda **kw: attention_4bit(q, cache, table, kl, **{"cu_q": cu, "max_q": 3, **kw})
+    want = call()
+    for big in (2 ** 31, 2 ** 32 + 1, 2 ** 63, 2 ** 64 + 1, 2 ** 64 + 16):
+        assert torch.allclose(call(window=big).float(), want.float(), rtol=2.0 ** -7, atol=4e-3)
+        assert torch.equal(call(max_kv=big), want)
+        assert torch.equal(call(max_q=big), want)
+    for bad in (dict(max_kv=-1), dict(max_kv=-2 ** 64 + 100), dict(window=-1), dict(window=-2 ** 64 + 100)):
+        with pytest.raises(qmv.QmvError):
+            call(**bad)
+    torch.cuda.synchronize()
