@@ -6,10 +6,14 @@
  * The conventions of qmv.h hold here too: every array is the caller's, device
  * arrays are 16-byte aligned, work is enqueued on ``stream`` and nothing
  * synchronizes the host, and every argument the host can see is checked
- * before anything is launched (QMV_ERR_TOO_LARGE where a call's sizes pass the
- * limits named at each structure and call).  What only the device sees (positions, lengths,
- * offsets and page numbers) is checked by the kernels: a value out of range
- * never reaches memory, and what it means is stated at each call.
+ * before anything is launched.  QMV_ERR_TOO_LARGE: a call's sizes pass the
+ * limits named at each structure and call, or need a grid of 2^32 threads along
+ * a dimension (at the earliest: rotary at 2^32 elements, an append or a read back
+ * at 2^34, attention at 2^23 tiles of 256 query rows, or with head sizes of 32,
+ * 160 and 224 at 2^26 query rows of a sequence).  What only the device sees
+ * (positions, lengths, offsets and page numbers) is checked by the kernels: a
+ * value out of range never reaches memory, and what it means is stated at each
+ * call.
  */
 #ifndef QMV_ATTENTION_H
 #define QMV_ATTENTION_H

@@ -121,6 +121,7 @@ __global__ __launch_bounds__(64) void attention_rows_kernel(AttnArgs a, float sc
 }
 
 hipError_t launch_attention_rows(const AttnArgs &a, int dt, hipStream_t st) {
+  if (!grid_fits((int64_t)a.kb.max_q * a.q.heads, 64)) return hipErrorInvalidConfiguration;
   const dim3 grid((unsigned)(a.kb.max_q * a.q.heads), (unsigned)a.kb.batch);
   const float sl = a.scale * 1.44269504088896340736f;
   if (dt == kBF16) hipLaunchKernelGGL((attention_rows_kernel<kBF16>), grid, dim3(64), 0, st, a, sl);

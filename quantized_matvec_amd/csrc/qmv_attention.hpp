@@ -85,6 +85,10 @@ __device__ __forceinline__ int64_t scale_base(const KVCache &c, int64_t page, in
   return ((page * c.heads + h) << c.log2page) * (c.dim / c.bs);
 }
 
+// HIP takes fewer than 2^32 threads along a dimension of a grid.  The launchers
+// return hipErrorInvalidConfiguration, and launch nothing, where a call needs more.
+inline bool grid_fits(int64_t workgroups, int threads) { return workgroups * threads < ((int64_t)1 << 32); }
+
 hipError_t launch_rope_table(const double *freqs, int half, int64_t max_pos, double gain,
                              float *table, hipStream_t st);
 hipError_t launch_rotary(const Heads &q, const Heads &qo, const Heads &k, const Heads &ko, int dt,

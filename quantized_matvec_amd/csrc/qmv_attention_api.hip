@@ -13,7 +13,9 @@ constexpr int64_t kMost = (int64_t)1 << 31;  // tokens, positions and heads stay
 
 bool aligned(const void *p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 bool is_pow2(int64_t v) { return v > 0 && (v & (v - 1)) == 0; }
-int launch_status(hipError_t e) { return e == hipSuccess ? QMV_OK : QMV_ERR_LAUNCH; }
+int launch_status(hipError_t e) {
+  return e == hipSuccess ? QMV_OK : (e == hipErrorInvalidConfiguration ? QMV_ERR_TOO_LARGE : QMV_ERR_LAUNCH);
+}
 
 // The strides of a dimension of one count for nothing.
 int check_heads(const qmv_heads *h, int64_t tokens, int size, Heads *out) {
@@ -175,7 +177,7 @@ int qmv_rotary(const qmv_heads *q, const qmv_heads *q_out, const qmv_heads *k,
   if (rc != QMV_OK) return rc;
   if (hq.heads != hqo.heads || hk.heads != hko.heads) return QMV_ERR_INVALID_ARG;
   if (!aligned(positions, 8)) return QMV_ERR_ALIGNMENT;
-  // workgroups of 256 pairs or more: the grid's limit
+  // workgroups of 256 pairs or more are counted in 31 bits
   if (tokens > kMost * 255 / ((int64_t)(hq.heads + hk.heads) * head_dim)) return QMV_ERR_TOO_LARGE;
   return launch_status(launch_rotary(hq, hqo, hk, hko, dtype, tokens, head_dim, positions, r,
                                      inverse != 0, (hipStream_t)stream));

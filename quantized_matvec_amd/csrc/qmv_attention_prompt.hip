@@ -548,9 +548,11 @@ size_t prompt_workspace_bytes(const KVCache &c, const KVBatch &kb, int q_heads, 
 }
 
 template <int DT>
-static void launch_prompt_t(const PromptArgs &pa, hipStream_t st) {
+static hipError_t launch_prompt_t(const PromptArgs &pa, hipStream_t st) {
   const AttnArgs &a = pa.a;
-  const dim3 grid((unsigned)((int64_t)a.c.heads * pa.mtiles * pa.splits * a.kb.batch));
+  const int64_t wgs = (int64_t)a.c.heads * pa.mtiles * pa.splits * a.kb.batch;
+  if (!grid_fits(wgs, kPThreads)) return hipErrorInvalidConfiguration;
+  const dim3 grid((unsigned)wgs);
   constexpr bool two = DT == kF16;
 #define QMV_P(D) hipLaunchKernelGGL((attention_prompt_kernel<D, DT, two>), grid, dim3(kPThreads), 0, st, pa)
   switch (a.c.dim) {
@@ -561,6 +563,7 @@ static void launch_prompt_t(const PromptArgs &pa, hipStream_t st) {
     default: QMV_P(256);
   }
 #undef QMV_P
+  return hipGetLastError();
 }
 
 hipError_t launch_attention_prompt(const AttnArgs &a, int dt, void *ws, hipStream_t st) {
@@ -568,9 +571,7 @@ hipError_t launch_attention_prompt(const AttnArgs &a, int dt, void *ws, hipStrea
   prompt_plan(a.c, a.kb, a.group, a.max_kv, a.window, &pa.mtiles, &pa.splits);
   pa.part.o = static_cast<float *>(ws);
   pa.part.ml = reinterpret_cast<float2 *>(pa.part.o + (size_t)a.kb.tokens * a.q.heads * pa.splits * a.c.dim);
-  if (dt == kBF16) launch_prompt_t<kBF16>(pa, st);
-  else launch_prompt_t<kF16>(pa, st);
-  hipError_t e = hipGetLastError();
+  const hipError_t e = dt == kBF16 ? launch_prompt_t<kBF16>(pa, st) : launch_prompt_t<kF16>(pa, st);
   if (e != hipSuccess || pa.splits == 1) return e;
   const int per = 256 / (a.c.dim / 4);
   const int64_t rows = (int64_t)a.kb.max_q * a.q.heads;

@@ -278,32 +278,34 @@ constexpr int kGroupFrom = 16;
 // groups of 16, with 4, 8 and 16: 85.6 and 18.7, 85.4 and 18.1, 82.4 and 20.9
 // us; at most 32 sets: 87.2 and 19.5 against 79.1 and 19.1).
 template <int LPR, int TG>
-static unsigned append_grid(const KVBatch &kb, int rows, int *iters) {
+static int64_t append_grid(const KVBatch &kb, int rows, int *iters) {
   constexpr int HS = 256 / LPR / TG;
   const int64_t groups = ((int64_t)kb.max_q + 2 * (TG - 1)) / TG;  // a group may begin TG - 1 places early
   const int64_t sets = (rows + HS - 1) / HS;
   *iters = (int)std::min<int64_t>(std::max<int64_t>(groups * kb.batch * sets * 3 / (8 * device_cu_count()), 1),
                                   std::min<int64_t>(sets, 16));
-  return (unsigned)(groups * ((rows + HS * *iters - 1) / (HS * *iters)));
+  return groups * ((rows + HS * *iters - 1) / (HS * *iters));
 }
 
 template <int DT, int QT, int LPR, int TG>
-static void launch_append_g(const AppendArgs &a, hipStream_t st) {
+static hipError_t launch_append_g(const AppendArgs &a, hipStream_t st) {
   int q_iters = 1, kv_iters;
-  const unsigned kv_grid = append_grid<LPR, TG>(a.kb, a.c.heads, &kv_iters);
-  const unsigned q_grid = a.q.heads ? append_grid<LPR, query_tokens(TG)>(a.kb, a.q.heads, &q_iters) : 0;
-  const dim3 grid(2 * kv_grid + q_grid, (unsigned)a.kb.batch);
-  hipLaunchKernelGGL((kv_append_kernel<DT, QT, LPR, TG>), grid, dim3(256), 0, st, a, q_iters, kv_iters, kv_grid);
+  const int64_t kv_grid = append_grid<LPR, TG>(a.kb, a.c.heads, &kv_iters);
+  const int64_t q_grid = a.q.heads ? append_grid<LPR, query_tokens(TG)>(a.kb, a.q.heads, &q_iters) : 0;
+  if (!grid_fits(2 * kv_grid + q_grid, 256)) return hipErrorInvalidConfiguration;
+  const dim3 grid((unsigned)(2 * kv_grid + q_grid), (unsigned)a.kb.batch);
+  hipLaunchKernelGGL((kv_append_kernel<DT, QT, LPR, TG>), grid, dim3(256), 0, st, a, q_iters, kv_iters, (unsigned)kv_grid);
+  return hipGetLastError();
 }
 
 template <int DT, int QT>
-static void launch_append_t(const AppendArgs &a, hipStream_t st) {
+static hipError_t launch_append_t(const AppendArgs &a, hipStream_t st) {
   const bool few = a.kb.max_q < kGroupFrom;
   switch (row_lanes(a.c.dim)) {
-    case 4: few ? launch_append_g<DT, QT, 4, 1>(a, st) : launch_append_g<DT, QT, 4, 16>(a, st); break;
-    case 8: few ? launch_append_g<DT, QT, 8, 1>(a, st) : launch_append_g<DT, QT, 8, 16>(a, st); break;
-    case 16: few ? launch_append_g<DT, QT, 16, 1>(a, st) : launch_append_g<DT, QT, 16, 16>(a, st); break;
-    default: few ? launch_append_g<DT, QT, 32, 1>(a, st) : launch_append_g<DT, QT, 32, 8>(a, st);
+    case 4: return few ? launch_append_g<DT, QT, 4, 1>(a, st) : launch_append_g<DT, QT, 4, 16>(a, st);
+    case 8: return few ? launch_append_g<DT, QT, 8, 1>(a, st) : launch_append_g<DT, QT, 8, 16>(a, st);
+    case 16: return few ? launch_append_g<DT, QT, 16, 1>(a, st) : launch_append_g<DT, QT, 16, 16>(a, st);
+    default: return few ? launch_append_g<DT, QT, 32, 1>(a, st) : launch_append_g<DT, QT, 32, 8>(a, st);
   }
 }
 
@@ -313,13 +315,9 @@ hipError_t launch_kv_append(const KVCache &c, int dt, int qt, const Midpoints4 &
   AppendArgs a{c, kb, k, v, q, qo, rope, {}};
   for (int j = 0; j < 15; ++j) a.mids.m[j] = (float)mids.mid[qt == kNF4 ? j : std::min(7 + j, 13)];
   if (dt == kBF16) {
-    if (qt == kNF4) launch_append_t<kBF16, kNF4>(a, st);
-    else launch_append_t<kBF16, kFP4>(a, st);
-  } else {
-    if (qt == kNF4) launch_append_t<kF16, kNF4>(a, st);
-    else launch_append_t<kF16, kFP4>(a, st);
+    return qt == kNF4 ? launch_append_t<kBF16, kNF4>(a, st) : launch_append_t<kBF16, kFP4>(a, st);
   }
-  return hipGetLastError();
+  return qt == kNF4 ? launch_append_t<kF16, kNF4>(a, st) : launch_append_t<kF16, kFP4>(a, st);
 }
 
 // ---------------------------------------------------------------------------
@@ -383,30 +381,30 @@ __global__ __launch_bounds__(256) void kv_dequantize_kernel(ReadArgs a, int qt, 
 }
 
 template <int DT, int LPR, int TG>
-static void launch_read_g(const ReadArgs &a, int qt, hipStream_t st) {
+static hipError_t launch_read_g(const ReadArgs &a, int qt, hipStream_t st) {
   int iters;
-  const unsigned x = append_grid<LPR, TG>(a.kb, a.c.heads, &iters);
-  const dim3 grid(x, (unsigned)a.kb.batch, 2);  // keys, values
+  const int64_t x = append_grid<LPR, TG>(a.kb, a.c.heads, &iters);
+  if (!grid_fits(x, 256)) return hipErrorInvalidConfiguration;
+  const dim3 grid((unsigned)x, (unsigned)a.kb.batch, 2);  // keys, values
   hipLaunchKernelGGL((kv_dequantize_kernel<DT, LPR, TG>), grid, dim3(256), 0, st, a, qt, iters);
+  return hipGetLastError();
 }
 
 template <int DT>
-static void launch_read_t(const ReadArgs &a, int qt, hipStream_t st) {
+static hipError_t launch_read_t(const ReadArgs &a, int qt, hipStream_t st) {
   const bool few = a.kb.max_q < kGroupFrom;
   switch (row_lanes(a.c.dim)) {
-    case 4: few ? launch_read_g<DT, 4, 1>(a, qt, st) : launch_read_g<DT, 4, 16>(a, qt, st); break;
-    case 8: few ? launch_read_g<DT, 8, 1>(a, qt, st) : launch_read_g<DT, 8, 16>(a, qt, st); break;
-    case 16: few ? launch_read_g<DT, 16, 1>(a, qt, st) : launch_read_g<DT, 16, 16>(a, qt, st); break;
-    default: few ? launch_read_g<DT, 32, 1>(a, qt, st) : launch_read_g<DT, 32, 8>(a, qt, st);
+    case 4: return few ? launch_read_g<DT, 4, 1>(a, qt, st) : launch_read_g<DT, 4, 16>(a, qt, st);
+    case 8: return few ? launch_read_g<DT, 8, 1>(a, qt, st) : launch_read_g<DT, 8, 16>(a, qt, st);
+    case 16: return few ? launch_read_g<DT, 16, 1>(a, qt, st) : launch_read_g<DT, 16, 16>(a, qt, st);
+    default: return few ? launch_read_g<DT, 32, 1>(a, qt, st) : launch_read_g<DT, 32, 8>(a, qt, st);
   }
 }
 
 hipError_t launch_kv_dequantize(const KVCache &c, int dt, int qt, const KVBatch &kb,
                                 const Heads &k, const Heads &v, hipStream_t st) {
   const ReadArgs a{c, kb, k, v};
-  if (dt == kBF16) launch_read_t<kBF16>(a, qt, st);
-  else launch_read_t<kF16>(a, qt, st);
-  return hipGetLastError();
+  return dt == kBF16 ? launch_read_t<kBF16>(a, qt, st) : launch_read_t<kF16>(a, qt, st);
 }
 
 }  // namespace qmv

@@ -203,7 +203,7 @@ __global__ __launch_bounds__(256) void rotary_kernel(RotaryArgs a, float sign) {
 }
 
 template <int DT, int V, bool INTER>
-static void launch_rotary_t(RotaryArgs &a, float sign, hipStream_t st) {
+static hipError_t launch_rotary_t(RotaryArgs &a, float sign, hipStream_t st) {
   constexpr int HP = 4;
   const int half = a.rope.half, heads = a.q.heads + a.k.heads;
   a.per_head = half / (INTER ? V / 2 : V) + (a.dim - 2 * half) / V;
@@ -213,22 +213,24 @@ static void launch_rotary_t(RotaryArgs &a, float sign, hipStream_t st) {
   const bool many = a.tokens * a.per_head * heads >= (int64_t)HP * 256 * 8 * device_cu_count() && heads >= HP;
   a.head_sets = many ? (heads + HP - 1) / HP : heads;
   a.per_token = a.per_head * a.head_sets;
-  const dim3 grid((unsigned)((a.tokens * a.per_token + 255) / 256));
+  const int64_t wgs = (a.tokens * a.per_token + 255) / 256;
+  if (!grid_fits(wgs, 256)) return hipErrorInvalidConfiguration;
+  const dim3 grid((unsigned)wgs);
   if (many) hipLaunchKernelGGL((rotary_kernel<DT, V, INTER, HP>), grid, dim3(256), 0, st, a, sign);
   else hipLaunchKernelGGL((rotary_kernel<DT, V, INTER, 1>), grid, dim3(256), 0, st, a, sign);
+  return hipGetLastError();
 }
 
 template <int DT>
-static void launch_rotary_d(RotaryArgs &a, float sign, hipStream_t st) {
+static hipError_t launch_rotary_d(RotaryArgs &a, float sign, hipStream_t st) {
   const int half = a.rope.half;
   if (a.rope.interleaved) {
-    if (half % 4 == 0) launch_rotary_t<DT, 8, true>(a, sign, st);
-    else launch_rotary_t<DT, 2, true>(a, sign, st);
-  } else {
-    if (half % 8 == 0) launch_rotary_t<DT, 8, false>(a, sign, st);
-    else if (half % 4 == 0) launch_rotary_t<DT, 4, false>(a, sign, st);
-    else launch_rotary_t<DT, 1, false>(a, sign, st);
+    if (half % 4 == 0) return launch_rotary_t<DT, 8, true>(a, sign, st);
+    return launch_rotary_t<DT, 2, true>(a, sign, st);
   }
+  if (half % 8 == 0) return launch_rotary_t<DT, 8, false>(a, sign, st);
+  if (half % 4 == 0) return launch_rotary_t<DT, 4, false>(a, sign, st);
+  return launch_rotary_t<DT, 1, false>(a, sign, st);
 }
 
 hipError_t launch_rotary(const Heads &q, const Heads &qo, const Heads &k, const Heads &ko, int dt,
@@ -236,10 +238,8 @@ hipError_t launch_rotary(const Heads &q, const Heads &qo, const Heads &k, const 
                          bool inverse, hipStream_t st) {
   RotaryArgs a{q, qo, k, ko, rope, positions, tokens, dim, 0, 0, 0};
   const float sign = inverse ? -1.f : 1.f;
-  if (dt == kF32) launch_rotary_d<kF32>(a, sign, st);
-  else if (dt == kF16) launch_rotary_d<kF16>(a, sign, st);
-  else launch_rotary_d<kBF16>(a, sign, st);
-  return hipGetLastError();
+  if (dt == kF32) return launch_rotary_d<kF32>(a, sign, st);
+  return dt == kF16 ? launch_rotary_d<kF16>(a, sign, st) : launch_rotary_d<kBF16>(a, sign, st);
 }
 
 }  // namespace qmv
