@@ -1,7 +1,7 @@
 """attention_4bit on inputs that its reduced formats could get wrong: sums over
-many keys that cancel, keys and values of very different size side by side,
-infinities and NaN in keys and values that a row does not see, very large
-scores.
+many keys that cancel, second terms of fp16 operands, keys and values of very
+different size side by side, infinities and NaN in keys and values that a row
+does not see, very large scores.
 
 Relative norms here are over all outputs of a call.  With u the measured error
 of rounding the exact result to the output's type, a kernel whose own error has
@@ -46,6 +46,28 @@ def norms(got, want, dt):
     rounded = torch.from_numpy(want).to(TDT[dt]).double().numpy()
     size = np.linalg.norm(want)
     return np.linalg.norm(got.double().cpu().numpy() - want) / size, np.linalg.norm(rounded - want) / size
+
+
+@pytest.mark.parametrize("new", [3, 12, 64])
+@pytest.mark.parametrize("qt", ["nf4", "fp4"])
+def test_fp16_keeps_second_terms(new, qt):
+    """Weights and scales of many different sizes, fp16: rounding weights or
+    values to one fp16 term would be an error of 2^-10 / sqrt 12 of a term at
+    most, 2.0e-4 on average, as large as the result's own rounding.  Allowed:
+    the keys' NF4 values as one fp16 term (6.2e-5 of the score's spread, which
+    is 1, so of the weights; none with FP4) and fp32 arithmetic."""
+    L, hq, hk, dim = 2000, 16, 4, 128
+    cache, table, K, V = filled(L, hk, dim, 32, "fp16", qt, 5 + new)
+    q = torch.randn(new, hq, dim, device="cuda", generator=torch.Generator(device="cuda").manual_seed(new)).to(torch.float16)
+    got = attention_4bit(q, cache, table, i32([L]), cu_q=i32([0, new]), max_q=new, causal=False)
+    qd = q.double().cpu().numpy()
+    want = np.empty(qd.shape)
+    for h in range(hq):
+        s = qd[:, h] @ K[:, h // 4].T * dim ** -0.5
+        p = np.exp(s - s.max(1, keepdims=True))
+        want[:, h] = (p / p.sum(1, keepdims=True)) @ V[:, h // 4]
+    err, u = norms(got, want, "fp16")
+    assert err <= np.hypot(u, 1.2e-4 if qt == "nf4" else 8e-5), (err, u)
 
 
 # --------------------------------------------------------------------------
