@@ -16,7 +16,11 @@ anything is launched.
 [batch] int32 the tokens of each sequence in the cache, the new ones included.
 With more than one new token for a sequence, ``cu_q`` [batch + 1] int32 holds
 the offsets of each sequence's tokens among all new tokens and ``max_q`` the
-most tokens of one sequence.
+most tokens of one sequence.  Rows of tokens that are past ``max_q``, or of no
+sequence, are not written: new outputs hold anything there.
+
+A batch that mixes prompts with single tokens is right in one call, but faster in
+two: one kernel is chosen for all sequences, by ``max_q``.
 """
 from __future__ import annotations
 

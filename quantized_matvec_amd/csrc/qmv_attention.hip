@@ -23,9 +23,10 @@ __device__ __forceinline__ float wave_sum(float v) {
 // One wave for each (token, query head), 64 keys a step: a lane scores one
 // key, then each lane sums over the keys for two pairs of elements.  Bound by
 // the vector unit (each query head dequantizes the cache for itself).  It
-// serves the head sizes that the matrix-core kernels are not built for; where
-// they are it takes 1224 us for the 64 sequences of attention_decode_kernel's
-// comment (71 there), 132 ms for the chunk of attention_prompt_kernel's (2.7).
+// serves the head sizes that the matrix-core kernels are not built for: 64
+// sequences as in attention_decode_kernel's comment take 470, 1315 and 1545 us
+// with heads of 32, 160 and 224.  With heads of 128 it took 1224 us for them (73
+// there), and 132 ms for the chunk of attention_prompt_kernel's (2.8).
 // ---------------------------------------------------------------------------
 template <int DT>
 __global__ __launch_bounds__(64) void attention_rows_kernel(AttnArgs a, float scale_log2) {

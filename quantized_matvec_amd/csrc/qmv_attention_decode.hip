@@ -29,8 +29,8 @@
 //    6e-5 of the score.
 // Queries are scaled by a power of two of their own (exact) into fp16's range
 // and the products p a by one common to the wave, which keeps the largest
-// block scale seen so far in [2^14, 2^15): a weight loses nothing above 2^-38
-// of the largest.
+// finite block scale that any of its rows has seen so far in [2^14, 2^15): a
+// weight loses nothing above 2^-38 of the largest.
 //
 // Work is divided by steps, whatever the lengths are (they are read here, on
 // the device): each workgroup takes an equal run of the order (sequence, head,
@@ -41,14 +41,14 @@
 //
 // Measured (32 query heads over 8 of 128, NF4 blocks of 64, bf16, one token,
 // unless said otherwise), kernel and join:
-//  * 196611 tokens, 64 query heads: 56 + 7 us for 214 MB.  In its steady state
-//    it reads 9 bytes a cycle and compute unit, 5.6 TB/s of the 6.4 that a
-//    reading loop reaches; the table, the first loads and the uneven ends are
-//    some 6000 cycles around it.
-//  * 64 sequences of up to 8170 tokens: 71 + 6 us for 316 MB.
+//  * 196611 tokens, 64 query heads: 57 + 7 us for 214 MB.  In its steady state
+//    it read 9 bytes a cycle and compute unit, 5.6 TB/s of the 6.4 that a
+//    reading loop reaches (when the whole took 55 us); the table, the first loads
+//    and the uneven ends are some 6000 cycles around it.
+//  * 64 sequences of up to 8170 tokens: 73 + 6 us for 316 MB.
 //  * 24 sequences of up to 8799, 4 tokens with a window of 4096, 32 heads over
-//    32 of 64, FP4 blocks of 32, fp16: 49 + 6 us for 195 MB.
-//  * one sequence of 1001: 10 + 5 us, launch, table and the chain of dependent
+//    32 of 64, FP4 blocks of 32, fp16: 51 + 6 us for 195 MB.
+//  * one sequence of 1001: 11 + 5 us, launch, table and the chain of dependent
 //    loads length -> page -> keys -> values.
 #include <algorithm>
 
@@ -182,9 +182,14 @@ struct StepPages {
 
 // Waves of a workgroup, which has a compute unit to itself: three waves of a
 // SIMD share its registers, two or one where rows are long and three or two
-// would spill.  Heads of 64: 49 us with 12, 53 with 8 (the 24 sequences above);
-// of 128: 55 and 70 us with 8, 62 and 80 with 12 (the long sequence, the 64);
-// of 256: 25 us with 4, 28 with 8, in blocks of 32 61 and 70.
+// would spill.  With the join: heads of 64: 57 us with 12, 59 with 8 (the 24
+// sequences above); of 128: 62 and 81 us with 8, 71 and 90 with 12 (the long
+// sequence, the 64); of 256: 69 us with 4, 75 with 8 (16 of the 64), in blocks of
+// 32 100 and 120.  Between these neither number is always the better one.  Of 96:
+// 70 us with 12, 68 with 8 (the 64), 104 and 106 (24 sequences of 4 tokens, 32
+// cache heads), 69 and 58 (the same with 8).  Of 192: 137 us with 4, 115 with 8 (the
+// 64), 91 and 82 (the 24 with 8 cache heads), but with blocks of 32 102 and 167,
+// spilled: taken is the number whose worst case is the smaller.
 __host__ __device__ constexpr int decode_waves(int D) { return D <= 96 ? 12 : D <= 128 ? 8 : 4; }
 
 template <int D, int CB, int RJ, int DT, bool LO>
@@ -781,13 +786,16 @@ __global__ __launch_bounds__(64 * kJoinWaves) void attention_join_kernel(DecodeA
 // Up to 48 query rows are three tiles, each of which goes over the keys by
 // itself (mostly out of the caches); the prompt kernel's time is about the same
 // for any number of rows up to 256.  Kernels and join, here against there, 16
-// sequences of about 4600 tokens, 64 heads over 4 of 128: 16 rows 32 us / 68,
-// 32 rows 49 / 70, 48 rows 66 / 73, so that a fourth tile would be slower; 24
-// sequences of 40 rows, 8 heads of 128: 122 / 264, 32 heads of 64 with fp16 and
-// a window of 4096: 216 / 395; heads of 256 in the first call, 32 rows in fp16
-// 98 / 309, 48 rows in bf16 120 / 200.  Where there are hardly any keys the join
-// costs more than it saves (32 prompts of 44 tokens: 15 / 10), the price of one
-// rule for all lengths, which the host knows only a bound of.
+// sequences of about 4600 tokens, 64 heads over 4 of 128: 16 rows 32 us / 65,
+// 32 rows 48 / 66, 48 rows 63 / 68, 64 rows 71 / 69, so no fourth tile; 24
+// sequences of 40 rows, 8 heads of 128: 119 / 260, 32 heads of 64 with fp16 and
+// a window of 4096: 185 / 384; heads of 256 in the first call, 32 rows in fp16
+// 94 / 311, 48 rows in bf16 118 / 194.  Where there are hardly any keys the join
+// costs more than it saves (32 prompts of 44 tokens: 14 / 10), the price of a
+// rule that does not look at max_kv.  The tiles are those of the largest sequence,
+// and one without rows of its own still goes over its keys: one sequence of 48
+// rows among 15 of 16 (4600 tokens, 32 heads over 8 of 128) takes 78 us, 16 of 48
+// rows 83, 16 of 16 rows 41.
 bool decode_eligible(const KVCache &c, int64_t rows) {
   return rows <= 48 && (c.dim == 64 || c.dim == 96 || c.dim == 128 || c.dim == 192 || c.dim == 256);
 }

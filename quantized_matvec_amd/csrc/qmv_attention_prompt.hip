@@ -36,12 +36,16 @@
 // divided among several (splits), joined by prompt_join_kernel.
 //
 // Measured (64 query heads over 8 of 128, NF4 blocks of 128, bf16): 2048 tokens
-// over 32768, 2.2e12 operations, 2.68 ms a call, 845 TFLOP/s of the 1194 that a
+// over 32768, 2.27e12 operations, 2.78 ms a call, 816 TFLOP/s of the 1194 that a
 // large bf16 product reaches here; the vector unit (exponentials, conversions,
-// dequantization) is active 57 % of the time and the matrix cores 35 %, and
+// dequantization) is active 56 % of the time and the matrix cores 34 %, and
 // what the two do not overlap is the distance.  Three prompts of up to 2555
-// tokens (7105 in all) with 32 query heads: 227 us a call, 610 TFLOP/s, less because the
-// triangle's short rows leave units idle at the end.
+// tokens (7105 in all) with 32 query heads: 233 us a call, 596 TFLOP/s, less because the
+// triangle's short rows leave units idle at the end.  The same in fp16, whose
+// second planes make five products of two: 5.75 ms and 413 us.
+// A sequence of few rows among prompts has its keys walked by one workgroup a
+// head, whose other waves wait: a prompt of 512 tokens with 63 single tokens over
+// 8000 each takes 493 us, the two in calls of their own 34 and 134 us.
 #include <algorithm>
 
 #include "qmv_attention_mfma.hpp"

@@ -251,7 +251,7 @@ __device__ __forceinline__ void append_rows(const AppendArgs &a, unsigned place,
 // Bound by memory in large calls, where a value byte is a store of its own, and
 // by the fifteen comparisons of an element.  7375 tokens of 5 prompts, 64 + 8 +
 // 8 heads of 128, bf16: 74 us for 280 MB, 3.8 TB/s, of which the queries are
-// 242 MB; 2532 tokens, 32 + 32 + 32 heads of 64, fp16: 19.5 us; 32 single
+// 242 MB; 2532 tokens, 32 + 32 + 32 heads of 64, fp16: 18.6 us; 32 single
 // tokens: 5.1 us, mostly the chain length -> page -> write.  Queries, keys and
 // values are in workgroups of their own, since one loop with all three kept the
 // registers of each (144 and 28 us, with one set of rows a thread).  Values,
@@ -268,9 +268,12 @@ __global__ __launch_bounds__(256) void kv_append_kernel(AppendArgs a, int q_iter
 // Lanes of a row: head_dim / 8 rounded up to a power of two.
 static int row_lanes(int dim) { return dim <= 32 ? 4 : dim <= 64 ? 8 : dim <= 128 ? 16 : 32; }
 
-// Calls with fewer new tokens of a sequence take them one by one (64 sequences,
-// 32 + 8 + 8 rows of 128: 4 tokens 9.7 us one by one, 12.0 in groups; 8 tokens
-// 14.0 and 14.9; chunks of 1000 tokens at Place).
+// Calls with fewer new tokens of a sequence take them one by one (append and
+// read back of 64 sequences, 32 + 8 + 8 rows of 128, one by one and in groups: 4
+// tokens 9.7 us and 14.1, 8 tokens 15.8 and 14.8, 12 tokens 17.5 and 17.9, 16 tokens
+// 19.8 and 20.0, 20 tokens 22.8 and 22.1, 24 tokens 25.4 and 22.8, 64 tokens 51 and
+// 39; of 16 sequences, 32 + 32 + 32 heads of 64, 15 tokens 11.5 and 11.8, 24 tokens
+// 14.8 and 13.7; chunks of 1000 tokens at Place).
 constexpr int kGroupFrom = 16;
 
 // Grid and sets of rows of a workgroup: as many sets (up to 16) as leave 8
@@ -324,9 +327,9 @@ hipError_t launch_kv_append(const KVCache &c, int dt, int qt, const Midpoints4 &
 // Reading back: fp32(T[code] * a) rounded to the cache's type.  A byte becomes
 // both values by one table read.  Rows go through it as through the append, with
 // the same places and sets.  Bound by the 16-bit writes and, for values, by
-// loads of single bytes 16 apart: the 7375 tokens (8 + 8 heads of 128) 20.1 us
-// for 38 MB, the 2532 tokens (32 + 32 heads of 64) 11.2 us for 27 MB, 32 single
-// tokens 3.8 us.
+// loads of single bytes 16 apart: the 7375 tokens (8 + 8 heads of 128) 20.6 us
+// for 38 MB, the 2532 tokens (32 + 32 heads of 64) 11.0 us for 27 MB, 32 single
+// tokens 3.6 us.
 // ---------------------------------------------------------------------------
 struct ReadArgs {
   KVCache c;

@@ -54,7 +54,7 @@ hipError_t launch_rope_table(const double *freqs, int half, int64_t max_pos, dou
 // the rotated part a multiple of 4), else single pairs.
 // 16384 tokens of 32 + 8 heads of 128 in bf16 (336 MB): 63.5 us, 5.3 TB/s, the
 // rate of a large copy; 8198 tokens of 64 + 8 heads, 64 of 128 elements turned
-// as neighbours, fp16: 60.1 us, 5.0 TB/s.  16 tokens: 3.4 us, a launch.
+// as neighbours, fp16: 60.3 us, 5.0 TB/s.  16 tokens: 3.3 us, a launch.
 // ---------------------------------------------------------------------------
 template <int DT, int V>
 __device__ __forceinline__ void load_run(const void *base, int64_t at, float (&x)[V]) {
@@ -208,8 +208,11 @@ static hipError_t launch_rotary_t(RotaryArgs &a, float sign, hipStream_t st) {
   const int half = a.rope.half, heads = a.q.heads + a.k.heads;
   a.per_head = half / (INTER ? V / 2 : V) + (a.dim - 2 * half) / V;
   // Four heads a thread where that leaves 8 workgroups for each compute unit:
-  // the two large calls above take 64 and 62 us so, 67 and 95 us with one head
-  // a thread.  With fewer workgroups there is nothing to hide latency behind.
+  // the two large calls above take 64 and 60 us so, 74 and 79 us with one head
+  // a thread.  With few workgroups there is nothing to hide latency behind: 64
+  // tokens of 40 heads of 128 4.4 us with four, 3.2 with one, 512 tokens 5.1 and
+  // 5.0.  The rule is on the safe side, the two being even from about 1500 tokens
+  // on (2048: 10.5 and 11.2, 6144, just below it: 22.7 and 26).
   const bool many = a.tokens * a.per_head * heads >= (int64_t)HP * 256 * 8 * device_cu_count() && heads >= HP;
   a.head_sets = many ? (heads + HP - 1) / HP : heads;
   a.per_token = a.per_head * a.head_sets;
