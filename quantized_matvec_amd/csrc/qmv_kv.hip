@@ -125,8 +125,7 @@ struct Turn {
 // What a thread works on.  A row takes LPR lanes of a wave, 8 elements each; a
 // workgroup has 256 / LPR rows at a time: TG tokens side by side for each of
 // HS rows h, and goes through `iters` such sets of rows, so that positions,
-// pages and angles are fetched once and the next row's elements while this
-// one is worked on.  With TG = 1 (few tokens) the rows of one token fill the
+// pages and angles are fetched once.  With TG = 1 (few tokens) the rows of one token fill the
 // workgroup; otherwise TG places of one group of 16 cache positions do, and
 // one workgroup writes all bytes of a value group and of a group's scales
 // (2532 tokens of three chunks, 32 + 32 + 32 heads of 64: 28.3 us one by one,
@@ -199,7 +198,6 @@ __device__ __forceinline__ void append_rows(const AppendArgs &a, unsigned place,
                              : a.c.kc + (int64_t)at * (a.c.dim >> 1) + (e0 >> 1)) + first * head_bytes;
     scales = (WHAT == kValues ? a.c.vs : a.c.ks) + first * head_scales + ((int64_t)(e0 / a.c.bs) << a.c.log2page) + at;
   }
-#pragma unroll WHAT == kQueries ? 4 : 2
   for (int h = pl.h; h < pl.end; h += P::HS) {
     const uint4 raw = *reinterpret_cast<const uint4 *>(in);
     float x[8];
@@ -365,7 +363,6 @@ __global__ __launch_bounds__(256) void kv_dequantize_kernel(ReadArgs a, int qt, 
   const Heads &dst = isv ? a.v : a.k;
   uint16_t *out = static_cast<uint16_t *>(dst.p) + t * dst.ts + pl.h * dst.hs + e0;
   const int step = isv ? 16 : 1;  // bytes from one pair of elements to the next
-#pragma unroll 4
   for (int h = pl.h; h < pl.end; h += P::HS) {
     uint32_t w[4];
 #pragma unroll
