@@ -11,3 +11,6 @@ from .attention import (  # noqa: F401
     KVCache4bit, attention_4bit, kv_append_4bit, kv_dequantize_4bit, rope_frequencies, rope_table,
     rotary, rotary_backward,
 )
+from .tuning import (  # noqa: F401
+    LoraAdapters, cross_entropy_4bit, distill_4bit, lora_4bit, lora_4bit_backward,
+)

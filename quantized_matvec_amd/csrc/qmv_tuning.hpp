@@ -1,0 +1,108 @@
+// Shared by the kernels of include/qmv/tuning.h: low-rank adapters beside a
+// 4-bit projection, and losses over a 4-bit vocabulary.
+#pragma once
+
+#include "qmv_launch.hpp"
+
+namespace qmv {
+
+struct Weight4 {
+  const uint8_t *packed;
+  Scales sc;
+  bool dq;
+  int64_t N, K;
+  int log2bs, qt;
+};
+
+// Rows [first, first + n).  first * K / blocksize has to be a multiple of the
+// second-level group: first a multiple of 4096, the largest group, always is.
+inline Weight4 rows_of(const Weight4 &w, int64_t first, int64_t n) {
+  Weight4 r = w;
+  const int64_t block = (first * w.K) >> w.log2bs;
+  r.packed += first * w.K / 2;
+  if (w.dq) {
+    r.sc.q += block;
+    r.sc.absmax2 += block >> w.sc.log2bs2;
+  } else {
+    r.sc.absmax += block;
+  }
+  r.N = n;
+  return r;
+}
+
+struct Lora {
+  const uint16_t *down, *up;
+  const float *scale;
+  int count, rank;
+};
+
+// fp32 values of the 16 codes, as a kernel argument.
+struct CodeValues {
+  float v[16];
+};
+inline CodeValues code_values(int qt) {
+  CodeValues t;
+  for (int c = 0; c < 16; ++c) t.v[c] = __builtin_bit_cast(float, table_bits(qt)[c]);
+  return t;
+}
+
+// A workspace is handed out from its start in pieces of 256 bytes.
+struct Carver {
+  size_t at = 0;
+  size_t take(size_t bytes) {
+    const size_t p = at;
+    at += (bytes + 255) & ~(size_t)255;
+    return p;
+  }
+};
+
+size_t lora_workspace(int64_t T, int64_t N, int64_t K, int log2bs, int count, int rank, bool backward);
+hipError_t launch_lora(const void *x, int dt, int64_t T, const Weight4 &w, const Lora &l, const int32_t *index,
+                       const void *bias, void *y, int y_dt, char *ws, hipStream_t st);
+hipError_t launch_lora_backward(const void *dy, const void *x, int dt, int64_t T, const Weight4 &w, const Lora &l,
+                                const int32_t *index, void *dx, void *d_down, void *d_up, int grad_dt, char *ws,
+                                hipStream_t st);
+
+// What a loss is taken against: one target a token (teacher NULL), or k ids
+// with a teacher's logits.
+struct Targets {
+  const int64_t *ids;
+  const void *teacher;
+  int teacher_dt, k;
+  float inv_tau;
+};
+
+size_t loss_workspace(int64_t T, int64_t V, int64_t K, int log2bs, int k, bool grad);
+hipError_t launch_loss(const void *x, int dt, int64_t T, const Weight4 &w, const Targets &tg, const float *dloss,
+                       void *loss, int loss_dt, void *dx, char *ws, hipStream_t st);
+
+// Sums and maxima over a wave, every lane's result the same: a fixed tree.
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
+  return v;
+}
+__device__ __forceinline__ float wave_max(float v) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor(v, o));
+  return v;
+}
+
+// The two 16-bit elements of a word.
+template <int DT>
+__device__ __forceinline__ float lo16(uint32_t w) {
+  if constexpr (DT == kBF16) return __uint_as_float(w << 16);
+  else return (float)__builtin_bit_cast(_Float16, (uint16_t)w);
+}
+template <int DT>
+__device__ __forceinline__ float hi16(uint32_t w) {
+  if constexpr (DT == kBF16) return __uint_as_float(w & 0xffff0000u);
+  else return (float)__builtin_bit_cast(_Float16, (uint16_t)(w >> 16));
+}
+template <int DT>
+__device__ __forceinline__ void unpack8(const uint4 &v, float (&f)[8]) {
+  f[0] = lo16<DT>(v.x), f[1] = hi16<DT>(v.x), f[2] = lo16<DT>(v.y), f[3] = hi16<DT>(v.y);
+  f[4] = lo16<DT>(v.z), f[5] = hi16<DT>(v.z), f[6] = lo16<DT>(v.w), f[7] = hi16<DT>(v.w);
+}
+
+}  // namespace qmv
