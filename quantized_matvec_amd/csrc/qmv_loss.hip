@@ -13,13 +13,15 @@
 // token whose target is all but certain keeps its precision (1 - q is
 // computed from s, not by subtracting), and a type with few exponent bits
 // does not flush the rest of the vocabulary against the target's logit.
-#include "qmv_tuning.hpp"
+#include "qmv_tile.hpp"
 
 namespace qmv {
 
 constexpr int kPieceV = 8192;    // columns of a piece: a multiple of 4096 (rows_of)
-constexpr int64_t kTokens = 4096;  // tokens taken at a time
+constexpr int64_t kTokens = 4096;  // most tokens taken at a time
 constexpr int kTail = 32;
+constexpr int kMostPiece = 32768;   // of the tile product's pieces
+constexpr int64_t kTiledFrom = 448;  // tokens from which it is used
 
 // What exp(l - m) is multiplied by before its rounding.  fp16 has no normal
 // numbers below 2^-14: with 2^14 (sums are fp32, and D is divided by it at the
@@ -32,6 +34,59 @@ struct RowState {
   float *lt;         // [T, k] logits of the target ids
   float *tail;       // [T, 32] logits of the last V % 32 columns (-inf: none, or a target)
 };
+
+// ---------------------------------------------------------------------------
+// Which tokens count (an id in [0, V) with a logit above -inf): one wave a token,
+// then the tokens that do, in order, followed by the others, and their number.
+// Many tokens: the others are left out of the products.
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ float teacher_logit(const void *teacher, int dt, int64_t i) {
+  return dt == kF32 ? static_cast<const float *>(teacher)[i]
+         : dt == kF16 ? bits16_to_f32<kF16>(static_cast<const uint16_t *>(teacher)[i])
+                      : bits16_to_f32<kBF16>(static_cast<const uint16_t *>(teacher)[i]);
+}
+
+__global__ __launch_bounds__(256) void loss_live_kernel(const int64_t *__restrict__ ids, const void *teacher,
+                                                        int teacher_dt, int k, int64_t V, int T, int32_t *__restrict__ live) {
+  const int t = blockIdx.x * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
+  if (t >= T) return;
+  bool any = false;
+  for (int j = lane; j < k; j += 64) {
+    const int64_t v = ids[(int64_t)t * k + j];
+    if (v >= 0 && v < V) any |= !teacher || !(teacher_logit(teacher, teacher_dt, (int64_t)t * k + j) == -INFINITY);
+  }
+  const bool on = __ballot(any) != 0;
+  if (lane == 0) live[t] = on;
+}
+
+__global__ __launch_bounds__(1024) void loss_order_kernel(const int32_t *__restrict__ live, int T,
+                                                          int32_t *__restrict__ list, int32_t *__restrict__ count) {
+  __shared__ int before[17];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int each = (T + 1023) / 1024, t0 = threadIdx.x * each, t1 = min(t0 + each, T);
+  int mine = 0;
+  for (int t = t0; t < t1; ++t) mine += live[t];
+  int upto = mine;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const int v = __shfl_up(upto, o);
+    if (lane >= o) upto += v;
+  }
+  if (lane == 63) before[wave + 1] = upto;
+  if (threadIdx.x == 0) before[0] = 0;
+  __syncthreads();
+  if (threadIdx.x == 0)
+    for (int w = 0; w < 16; ++w) before[w + 1] += before[w];
+  __syncthreads();
+  const int total = before[16];
+  int at = before[wave] + upto - mine;  // tokens before t0 that count
+  for (int t = t0; t < t1; ++t) {
+    const bool on = live[t];
+    list[on ? at : total + t - at] = t;
+    at += on;
+  }
+  if (threadIdx.x == 0) *count = total;
+}
 
 template <class F>
 __device__ __forceinline__ float block_reduce(float v, float *buf, F op) {  // 256 threads
@@ -105,14 +160,16 @@ __global__ __launch_bounds__(256) void loss_add_kernel(float *__restrict__ D, co
 template <int DT, int LDT, bool DQ>
 __global__ __launch_bounds__(256) void loss_finish_kernel(const int64_t *__restrict__ ids, const void *teacher,
                                                           int teacher_dt, int k, float inv_tau, int64_t V, RowState rs,
-                                                          int tail_n, const float *__restrict__ D, int64_t K,
+                                                          int tail_n, const float *__restrict__ D, int parts,
+                                                          int64_t part, int64_t K, const int32_t *list,
                                                           const uint8_t *__restrict__ packed, Scales sc, int log2bs,
                                                           CodeValues table, const float *__restrict__ dloss,
                                                           typename Storage<LDT>::type *__restrict__ loss,
                                                           uint16_t *__restrict__ dx) {
   __shared__ float z[128], p[128], lt[128], coef[128 + kTail], tab[16], buf[4];
   __shared__ int64_t id[128 + kTail];
-  const int64_t t = blockIdx.x;
+  const int64_t i = blockIdx.x;             // its place among the rows of D and rs
+  const int64_t t = list ? list[i] : i;
   const int tid = threadIdx.x;
   if (tid < 16) tab[tid] = table.v[tid];
   // the target distribution; an entry that repeats an earlier id lends that
@@ -122,27 +179,22 @@ __global__ __launch_bounds__(256) void loss_finish_kernel(const int64_t *__restr
     const int64_t v = ids[t * k + tid];
     there = v >= 0 && v < V;
     id[tid] = there ? v : -1;
-    lt[tid] = there ? rs.lt[t * k + tid] : -INFINITY;
-    z[tid] = !there ? -INFINITY
-             : !teacher ? 0.f
-             : teacher_dt == kF32 ? static_cast<const float *>(teacher)[t * k + tid] * inv_tau
-             : teacher_dt == kF16 ? bits16_to_f32<kF16>(static_cast<const uint16_t *>(teacher)[t * k + tid]) * inv_tau
-                                  : bits16_to_f32<kBF16>(static_cast<const uint16_t *>(teacher)[t * k + tid]) * inv_tau;
+    z[tid] = !there ? -INFINITY : teacher ? teacher_logit(teacher, teacher_dt, t * k + tid) * inv_tau : 0.f;
   }
   __syncthreads();
   float zm = -INFINITY, zs = 0.f;
-  for (int j = 0; j < k; ++j) zm = fmaxf(zm, z[j]);
-  const bool live = zm > -INFINITY;  // with a NaN in z: not so, or p is NaN
-  if (!live && !(zm != zm)) {
-    bool nan = false;
-    for (int j = 0; j < k; ++j) nan |= z[j] != z[j];
-    if (!nan) {
-      if (tid == 0) store_elem<LDT>(loss, t, 0.f);
-      if (dx)
-        for (int64_t c = tid; c < K; c += 256) dx[t * K + c] = 0;
-      return;
-    }
+  bool live = false;
+  for (int j = 0; j < k; ++j) {
+    zm = fmaxf(zm, z[j]);
+    live |= !(z[j] == -INFINITY);  // a NaN counts, and p is NaN then
   }
+  if (!live) {
+    if (tid == 0) store_elem<LDT>(loss, t, 0.f);
+    if (dx)
+      for (int64_t c = tid; c < K; c += 256) dx[t * K + c] = 0;
+    return;
+  }
+  if (tid < k) lt[tid] = there ? rs.lt[i * k + tid] : -INFINITY;
   for (int j = 0; j < k; ++j) zs += expf(z[j] - zm);
   if (tid < k) {
     p[tid] = expf(z[tid] - zm) / zs;
@@ -151,9 +203,10 @@ __global__ __launch_bounds__(256) void loss_finish_kernel(const int64_t *__restr
   }
   __syncthreads();
   // the loss
-  float M = rs.m[t];
+  const float m = rs.m[i];
+  float M = m;
   for (int j = 0; j < k; ++j) M = fmaxf(M, lt[j]);
-  const float rest = rs.s[t] * (rs.m[t] == -INFINITY ? 0.f : expf(rs.m[t] - M));
+  const float rest = rs.s[i] * (m == -INFINITY ? 0.f : expf(m - M));
   const float mine = own ? expf(lt[tid] - M) : 0.f;
   const float targets = block_reduce(wave_sum(mine), buf, [](float a, float b) { return a + b; });
   const float Z = rest + targets;
@@ -189,63 +242,195 @@ __global__ __launch_bounds__(256) void loss_finish_kernel(const int64_t *__restr
   }
   if (tid >= 128 && tid < 128 + kTail) {
     const int j = tid - 128;
-    const float l = j < tail_n ? rs.tail[t * kTail + j] : -INFINITY;
+    const float l = j < tail_n ? rs.tail[i * kTail + j] : -INFINITY;
     coef[k + j] = l == -INFINITY ? 0.f : expf(l - M) / Z;
     id[k + j] = V - tail_n + j;
   }
   __syncthreads();
   const float gain = dloss[t] * inv_tau;
-  const float scale = rs.m[t] == -INFINITY ? 0.f : expf(rs.m[t] - M) / Z / kGain<DT>;
+  const float scale = m == -INFINITY ? 0.f : expf(m - M) / Z / kGain<DT>;
   const float offset = DQ ? sc.offset[0] : 0.f;
   for (int64_t c = tid * 8; c < K; c += 2048) {
     float acc[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) acc[i] = D[t * K + c + i] * scale;
+    for (int e = 0; e < 8; ++e) acc[e] = D[i * K + c + e];
+    for (int s = 1; s < parts; ++s)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) acc[e] += D[s * part + i * K + c + e];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc[e] *= scale;
     for (int j = 0; j < k + tail_n; ++j) {
       const float cj = coef[j];
       if (cj == 0.f) continue;
-      const int64_t e = id[j] * K + c;
-      const float a = cj * block_scale<DQ>(sc, e >> log2bs, offset);
-      const uint32_t w = *reinterpret_cast<const uint32_t *>(packed + e / 2);
+      const int64_t at = id[j] * K + c;
+      const float a = cj * block_scale<DQ>(sc, at >> log2bs, offset);
+      const uint32_t w = *reinterpret_cast<const uint32_t *>(packed + at / 2);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        acc[2 * i] = fmaf(a, tab[w >> (8 * i + 4) & 15], acc[2 * i]);
-        acc[2 * i + 1] = fmaf(a, tab[w >> (8 * i) & 15], acc[2 * i + 1]);
+      for (int e = 0; e < 4; ++e) {
+        acc[2 * e] = fmaf(a, tab[w >> (8 * e + 4) & 15], acc[2 * e]);
+        acc[2 * e + 1] = fmaf(a, tab[w >> (8 * e) & 15], acc[2 * e + 1]);
       }
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) store_elem<DT>(dx, t * K + c + i, acc[i] * gain);
+    for (int e = 0; e < 8; ++e) store_elem<DT>(dx, t * K + c + e, acc[e] * gain);
   }
 }
 
 // ---------------------------------------------------------------------------
+// Many tokens: a piece's logits and D by the tile product.
+//
+// One row of a piece in the registers of a workgroup of 256, 512 or 1024 threads,
+// 32 columns each; rows are those that count, list[i] the token of row i.
+// ---------------------------------------------------------------------------
+template <int DT, bool GRAD>
+__global__ __launch_bounds__(1024) void loss_rows_kernel(const float *__restrict__ logits, int64_t ld, int64_t v0, int n,
+                                                         int np, const int64_t *__restrict__ ids, int k, float inv_tau,
+                                                         bool first, RowState rs, const int32_t *__restrict__ list,
+                                                         const int32_t *__restrict__ count, uint16_t *__restrict__ P) {
+  __shared__ uint32_t out[kMostPiece / 32];  // columns of target ids
+  __shared__ float buf[2][16];
+  const int64_t i = blockIdx.x;
+  if (i >= *count) return;
+  const int64_t t = list[i];
+  const int tid = threadIdx.x, threads = blockDim.x, waves = threads >> 6;
+  const float *row = logits + i * ld;
+  for (int c = tid; c < threads; c += threads) out[c] = 0;  // 32 columns a thread
+  float l[8][4];
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    const int c = 4 * (q * threads + tid);
+    float4 v = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+    if (c + 3 < n) {
+      v = *reinterpret_cast<const float4 *>(row + c);
+    } else if (c < n) {
+      v.x = row[c];
+      if (c + 1 < n) v.y = row[c + 1];
+      if (c + 2 < n) v.z = row[c + 2];
+    }
+    l[q][0] = v.x * inv_tau, l[q][1] = v.y * inv_tau, l[q][2] = v.z * inv_tau, l[q][3] = v.w * inv_tau;
+  }
+  __syncthreads();
+  for (int j = tid; j < k; j += threads) {
+    const int64_t c = ids[t * k + j] - v0;
+    if (c >= 0 && c < n) {
+      atomicOr(&out[c >> 5], 1u << (c & 31));
+      rs.lt[i * k + j] = row[c] * inv_tau;
+    }
+  }
+  __syncthreads();
+  float m = -INFINITY;
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    const int c = 4 * (q * threads + tid);
+    const uint32_t gone = out[c >> 5] >> (c & 31) & 15;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (gone >> e & 1) l[q][e] = -INFINITY;
+      m = fmaxf(m, l[q][e]);
+    }
+  }
+  m = wave_max(m);
+  if ((tid & 63) == 0) buf[0][tid >> 6] = m;
+  __syncthreads();
+  for (int w = 0; w < waves; ++w) m = fmaxf(m, buf[0][w]);
+  const float m_old = first ? -INFINITY : rs.m[i];
+  m = fmaxf(m, m_old);
+  const float ref = m == -INFINITY ? 0.f : m;  // no column yet: exp(-inf) = 0
+  float s = 0.f;
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    const int c = 4 * (q * threads + tid);
+    float e[4];
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      e[x] = __expf(l[q][x] - ref);
+      s += e[x];
+    }
+    if constexpr (GRAD)
+      if (c < np)  // np is a multiple of 64; past n: zeros
+        *reinterpret_cast<uint2 *>(P + i * np + c) = make_uint2(cvt_pair<DT>(e[0] * kGain<DT>, e[1] * kGain<DT>),
+                                                                cvt_pair<DT>(e[2] * kGain<DT>, e[3] * kGain<DT>));
+  }
+  s = wave_sum(s);
+  if ((tid & 63) == 0) buf[1][tid >> 6] = s;
+  __syncthreads();
+  if (tid == 0) {
+    s = 0.f;
+    for (int w = 0; w < waves; ++w) s += buf[1][w];
+    const float f = m_old == -INFINITY ? 0.f : __expf(m_old - m);
+    rs.s[i] = (first ? 0.f : rs.s[i] * f) + s;
+    rs.m[i] = m;
+    rs.f[i] = f;
+  }
+}
+
+// D = D f + sums, the part of this workgroup's terms
+struct EpilogueAdd : EpilogueBase {
+  float *D;
+  const float *f;
+  int64_t K, part;
+  bool first;
+  struct Row {
+    float *p, f;
+  };
+  __device__ Row row(int m) const {
+    return Row{D + blockIdx.y * part + m * K, first ? 0.f : f[m]};
+  }
+  __device__ void store(const Row &r, int n, float v) const { r.p[n] = first ? v : fmaf(r.p[n], r.f, v); }
+};
+
+// ---------------------------------------------------------------------------
 struct LossPlan {
-  int64_t tokens;
-  int piece;
-  size_t logits, m, s, f, lt, tail, P, D, add, back, total;
+  bool tiled;
+  int64_t tokens;  // taken at a time
+  int piece, parts, split;
+  size_t logits, m, s, f, lt, tail, P, D, add, back, live, list, count, W, Wt, total;
 };
 
 static LossPlan loss_plan(int64_t T, int64_t V, int64_t K, int log2bs, int k, bool grad) {
   LossPlan p{};
   Carver c;
-  p.tokens = T < kTokens ? T : kTokens;
-  p.piece = (int)(V < kPieceV ? V : kPieceV);
+  p.tiled = T >= kTiledFrom && K % 64 == 0 && K <= 65536;
+  const int64_t turns = (T + kTokens - 1) / kTokens;
+  p.tokens = (T + turns - 1) / turns;
   const size_t n = (size_t)p.tokens;
-  p.logits = c.take(n * p.piece * 4);
   p.m = c.take(n * 4), p.s = c.take(n * 4), p.f = c.take(n * 4), p.lt = c.take(n * k * 4);
-  if (grad) {
-    p.tail = c.take(n * kTail * 4);
-    p.P = c.take(n * p.piece * 2);
-    p.D = c.take(n * K * 4);
-    p.add = c.take(n * K * 4);
-    size_t most = 0;  // the product's own workspace, over all sizes that come up
-    for (int64_t m : {p.tokens, T % p.tokens})
-      for (int64_t v : {(int64_t)p.piece & ~31ll, (V % p.piece) & ~31ll})
-        if (m > 0 && v > 0) {
-          const size_t b = gemm_backward_workspace_bytes(m, v, K, log2bs);
-          most = b > most ? b : most;
-        }
-    p.back = c.take(most);
+  if (p.tiled) {
+    // 512 tiles of logits or more; few tiles of D: the piece's terms in parts, each with a D of its own
+    const int64_t rows = (p.tokens + kTileM - 1) / kTileM;
+    p.piece = rows >= 16 ? 8192 : rows >= 8 ? 16384 : kMostPiece;
+    while (p.piece > 8192 && p.piece / 2 >= V) p.piece /= 2;
+    const int64_t tiles = rows * ((K + kTileN - 1) / kTileN);
+    p.parts = (int)(tiles >= 256 ? 1 : 256 / tiles);
+    if (p.parts > p.piece / 1024) p.parts = p.piece / 1024;
+    p.split = (p.piece / p.parts + 63) & ~63;
+    p.parts = (p.piece + p.split - 1) / p.split;
+    p.logits = c.take(n * p.piece * 4);
+    p.live = c.take(n * 4), p.list = c.take(n * 4), p.count = c.take(4);
+    p.W = c.take((size_t)p.piece * K * 2);
+    if (grad) {
+      p.Wt = c.take((size_t)p.piece * K * 2);
+      p.P = c.take(n * p.piece * 2);
+      p.D = c.take(n * K * 4 * p.parts);
+    }
+  } else {
+    p.parts = 1;
+    p.piece = (int)(V < kPieceV ? V : kPieceV);
+    p.logits = c.take(n * p.piece * 4);
+    if (grad) {
+      p.tail = c.take(n * kTail * 4);
+      p.P = c.take(n * p.piece * 2);
+      p.D = c.take(n * K * 4);
+      p.add = c.take(n * K * 4);
+      size_t most = 0;  // the product's own workspace, over all sizes that come up
+      for (int64_t m : {p.tokens, T % p.tokens})
+        for (int64_t v : {(int64_t)p.piece & ~31ll, (V % p.piece) & ~31ll})
+          if (m > 0 && v > 0) {
+            const size_t b = gemm_backward_workspace_bytes(m, v, K, log2bs);
+            most = b > most ? b : most;
+          }
+      p.back = c.take(most);
+    }
   }
   p.total = c.at;
   return p;
@@ -255,13 +440,79 @@ size_t loss_workspace(int64_t T, int64_t V, int64_t K, int log2bs, int k, bool g
   return loss_plan(T, V, K, log2bs, k, grad).total;
 }
 
+// m tokens by the tile product; what is left for loss_finish_kernel is in rs and D
+template <int DT>
+static hipError_t pieces_tiled(const LossPlan &p, const uint16_t *x, int64_t m, const Weight4 &w, const Targets &tg,
+                               const int64_t *ids, const void *teacher, bool grad, const RowState &rs, float *D,
+                               char *ws, hipStream_t st) {
+  float *logits = reinterpret_cast<float *>(ws + p.logits);
+  uint16_t *P = reinterpret_cast<uint16_t *>(ws + p.P), *W = reinterpret_cast<uint16_t *>(ws + p.W);
+  uint16_t *Wt = grad ? reinterpret_cast<uint16_t *>(ws + p.Wt) : nullptr;
+  int32_t *live = reinterpret_cast<int32_t *>(ws + p.live), *list = reinterpret_cast<int32_t *>(ws + p.list);
+  int32_t *count = reinterpret_cast<int32_t *>(ws + p.count);
+  hipLaunchKernelGGL(loss_live_kernel, dim3((unsigned)((m + 3) / 4)), dim3(256), 0, st, ids, teacher, tg.teacher_dt, tg.k,
+                     w.N, (int)m, live);
+  hipLaunchKernelGGL(loss_order_kernel, dim3(1), dim3(1024), 0, st, live, (int)m, list, count);
+  for (int64_t v = 0; v < w.N; v += p.piece) {
+    const int n = (int)(w.N - v < p.piece ? w.N - v : p.piece), np = (n + 63) & ~63;
+    const hipError_t e = launch_decode_piece(rows_of(w, v, n), DT, 0, w.K, W, w.K, Wt, np, st);
+    if (e != hipSuccess) return e;
+    TileArgs a = tile_args(x, w.K, W, w.K, m, n, w.K);
+    a.rows = list, a.count = count;
+    EpilogueF32 keep;
+    keep.C = logits, keep.ld = p.piece;
+    hipLaunchKernelGGL((tile_kernel<DT, EpilogueF32>), dim3(a.ncol * a.nrow), dim3(256), 0, st, a, keep);
+    const int threads = p.piece / 32;
+    if (!grad) {
+      hipLaunchKernelGGL((loss_rows_kernel<DT, false>), dim3((unsigned)m), dim3(threads), 0, st, logits, (int64_t)p.piece, v,
+                         n, np, ids, tg.k, tg.inv_tau, v == 0, rs, list, count, P);
+      continue;
+    }
+    hipLaunchKernelGGL((loss_rows_kernel<DT, true>), dim3((unsigned)m), dim3(threads), 0, st, logits, (int64_t)p.piece, v,
+                       n, np, ids, tg.k, tg.inv_tau, v == 0, rs, list, count, P);
+    TileArgs b = tile_args(P, np, Wt, np, m, w.K, np);
+    b.count = count, b.split = p.split;
+    EpilogueAdd add;
+    add.D = D, add.f = rs.f, add.K = w.K, add.part = p.tokens * w.K, add.first = v == 0;
+    hipLaunchKernelGGL((tile_kernel<DT, EpilogueAdd>), dim3(b.ncol * b.nrow, p.parts), dim3(256), 0, st, b, add);
+  }
+  return hipGetLastError();
+}
+
+// m tokens by the products of gemm_4bit and its backward
+template <int DT>
+static hipError_t pieces_plain(const LossPlan &p, const uint16_t *x, int64_t m, const Weight4 &w, const Targets &tg,
+                               const int64_t *ids, bool grad, const RowState &rs, float *D, int *tail_n, char *ws,
+                               hipStream_t st) {
+  float *logits = reinterpret_cast<float *>(ws + p.logits), *add = reinterpret_cast<float *>(ws + p.add);
+  uint16_t *P = reinterpret_cast<uint16_t *>(ws + p.P);
+  for (int64_t v = 0; v < w.N; v += p.piece) {
+    const int n = (int)(w.N - v < p.piece ? w.N - v : p.piece), np = n & ~31;
+    const Weight4 c = rows_of(w, v, n);
+    hipError_t e = launch_gemm_4bit(x, DT, m, n, w.K, c.packed, c.sc, c.dq, c.log2bs, c.qt, logits, kF32, nullptr, st);
+    if (e != hipSuccess) return e;
+    if (!grad) {
+      hipLaunchKernelGGL((loss_piece_kernel<DT, false>), dim3((unsigned)m), dim3(256), 0, st, logits, (int64_t)n, v, n, n,
+                         ids, tg.k, tg.inv_tau, v == 0, rs, P);
+      continue;
+    }
+    hipLaunchKernelGGL((loss_piece_kernel<DT, true>), dim3((unsigned)m), dim3(256), 0, st, logits, (int64_t)n, v, n, np,
+                       ids, tg.k, tg.inv_tau, v == 0, rs, P);
+    if (np) {
+      e = launch_gemm_4bit_backward(P, DT, m, np, w.K, c.packed, c.sc, c.dq, c.log2bs, c.qt, add, kF32, ws + p.back, st);
+      if (e != hipSuccess) return e;
+    }
+    hipLaunchKernelGGL(loss_add_kernel, dim3((unsigned)m), dim3(256), 0, st, D, np ? add : nullptr, rs.f, w.K, v == 0);
+    *tail_n = n - np;
+  }
+  return hipGetLastError();
+}
+
 template <int DT>
 static hipError_t loss_t(const uint16_t *x, int64_t T, const Weight4 &w, const Targets &tg, const float *dloss,
                          void *loss, int loss_dt, uint16_t *dx, char *ws, hipStream_t st) {
   const LossPlan p = loss_plan(T, w.N, w.K, w.log2bs, tg.k, dx != nullptr);
-  float *logits = reinterpret_cast<float *>(ws + p.logits);
-  uint16_t *P = reinterpret_cast<uint16_t *>(ws + p.P);
-  float *D = reinterpret_cast<float *>(ws + p.D), *add = reinterpret_cast<float *>(ws + p.add);
+  float *D = reinterpret_cast<float *>(ws + p.D);
   const RowState rs{reinterpret_cast<float *>(ws + p.m), reinterpret_cast<float *>(ws + p.s),
                     reinterpret_cast<float *>(ws + p.f), reinterpret_cast<float *>(ws + p.lt),
                     reinterpret_cast<float *>(ws + p.tail)};
@@ -269,34 +520,18 @@ static hipError_t loss_t(const uint16_t *x, int64_t T, const Weight4 &w, const T
   for (int64_t t = 0; t < T; t += p.tokens) {
     const int64_t m = T - t < p.tokens ? T - t : p.tokens;
     const int64_t *ids = tg.ids + t * tg.k;
-    int tail_n = 0;
-    for (int64_t v = 0; v < w.N; v += p.piece) {
-      const int n = (int)(w.N - v < p.piece ? w.N - v : p.piece), np = n & ~31;
-      const Weight4 c = rows_of(w, v, n);
-      hipError_t e = launch_gemm_4bit(x + t * w.K, DT, m, n, w.K, c.packed, c.sc, c.dq, c.log2bs, c.qt, logits, kF32,
-                                      nullptr, st);
-      if (e != hipSuccess) return e;
-      if (!dx) {
-        hipLaunchKernelGGL((loss_piece_kernel<DT, false>), dim3((unsigned)m), dim3(256), 0, st, logits, (int64_t)n, v, n, n,
-                           ids, tg.k, tg.inv_tau, v == 0, rs, P);
-        continue;
-      }
-      hipLaunchKernelGGL((loss_piece_kernel<DT, true>), dim3((unsigned)m), dim3(256), 0, st, logits, (int64_t)n, v, n, np,
-                         ids, tg.k, tg.inv_tau, v == 0, rs, P);
-      if (np) {
-        e = launch_gemm_4bit_backward(P, DT, m, np, w.K, c.packed, c.sc, c.dq, c.log2bs, c.qt, add, kF32, ws + p.back, st);
-        if (e != hipSuccess) return e;
-      }
-      hipLaunchKernelGGL(loss_add_kernel, dim3((unsigned)m), dim3(256), 0, st, D, np ? add : nullptr, rs.f, w.K, v == 0);
-      tail_n = n - np;
-    }
     const void *teacher = tg.teacher ? static_cast<const char *>(tg.teacher) + t * tg.k * tsize : nullptr;
+    int tail_n = 0;
+    const hipError_t e = p.tiled ? pieces_tiled<DT>(p, x + t * w.K, m, w, tg, ids, teacher, dx != nullptr, rs, D, ws, st)
+                                 : pieces_plain<DT>(p, x + t * w.K, m, w, tg, ids, dx != nullptr, rs, D, &tail_n, ws, st);
+    if (e != hipSuccess) return e;
+    const int32_t *list = p.tiled ? reinterpret_cast<int32_t *>(ws + p.list) : nullptr;
     char *lp = static_cast<char *>(loss) + t * lsize;
 #define QMV_L(LDT, DQV)                                                                                              \
   hipLaunchKernelGGL((loss_finish_kernel<DT, LDT, DQV>), dim3((unsigned)m), dim3(256), 0, st, ids, teacher,          \
-                     tg.teacher_dt, tg.k, tg.inv_tau, w.N, rs, tail_n, D, w.K, w.packed, w.sc, w.log2bs,             \
-                     code_values(w.qt), dloss ? dloss + t : nullptr, reinterpret_cast<typename Storage<LDT>::type *>(lp), \
-                     dx ? dx + t * w.K : nullptr)
+                     tg.teacher_dt, tg.k, tg.inv_tau, w.N, rs, tail_n, D, p.parts, p.tokens * w.K, w.K, list,        \
+                     w.packed, w.sc, w.log2bs, code_values(w.qt), dloss ? dloss + t : nullptr,                       \
+                     reinterpret_cast<typename Storage<LDT>::type *>(lp), dx ? dx + t * w.K : nullptr)
     if (loss_dt == kF32) {
       if (w.dq) QMV_L(kF32, true);
       else QMV_L(kF32, false);

@@ -30,6 +30,12 @@ inline Weight4 rows_of(const Weight4 &w, int64_t first, int64_t n) {
   return r;
 }
 
+// Rows of a weight and its columns [c0, c0 + cols) as 16-bit values W [N, cols] and
+// their transpose Wt [cols, N], either NULL; ldt reaches over N up to a multiple of
+// 64, whose last columns of Wt become zeros.
+hipError_t launch_decode_piece(const Weight4 &w, int dt, int64_t c0, int64_t cols, void *W, int64_t ldw, void *Wt,
+                               int64_t ldt, hipStream_t st);
+
 struct Lora {
   const uint16_t *down, *up;
   const float *scale;
