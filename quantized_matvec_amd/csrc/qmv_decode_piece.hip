@@ -8,62 +8,68 @@ namespace qmv {
 // dequantize_4bit returns them in DT, and its transpose Wt[c][v], rows past the
 // last as zeros there: each where it is wanted, from one read of the codes.
 //
-// A workgroup takes 64 rows x 64 columns.  A thread decodes 16 columns of a row
-// (8 bytes of codes, one block) and stores its 32 bytes of W; the transpose goes
-// through LDS, from which lane c of wave w takes column c's rows 16 w .. + 15.
-// Bound by the writes: 4 bytes for each half byte read.
+// A workgroup takes 64 rows x 128 columns.  A thread decodes 8 columns of four
+// rows (4 bytes of codes, one block), 16 threads a row, and stores their 16
+// bytes of W; the transpose goes through LDS, whose 16-byte chunks are swizzled
+// by row / 8, so that 8 lanes can take 8 rows each of a column, from 8 different
+// bank groups, and store one whole line of it.  Bound by the writes: 4 bytes
+// for each half byte read.
 // ---------------------------------------------------------------------------
 template <int DT, bool DQ>
 __global__ __launch_bounds__(256) void decode_piece_kernel(const uint8_t *__restrict__ packed, Scales sc, int log2bs,
-                                                           CodeValues table, int64_t K, int64_t c0, int n,
+                                                           CodeValues table, int64_t K, int64_t c0, int64_t cols, int n,
                                                            uint16_t *__restrict__ W, int64_t ldw,
                                                            uint16_t *__restrict__ Wt, int64_t ldt) {
   __shared__ float tab[16];
-  __shared__ __attribute__((aligned(16))) uint16_t tile[64][72];
-  const int tid = threadIdx.x, row = tid >> 2, col = 16 * (tid & 3);
-  const int v = blockIdx.y * 64 + row, c = blockIdx.x * 64 + col;
+  __shared__ __attribute__((aligned(16))) uint16_t tile[64][128];
+  const int tid = threadIdx.x, row = tid >> 4, col = 8 * (tid & 15);
+  const int64_t c = (int64_t)blockIdx.x * 128 + col;
   if (tid < 16) tab[tid] = table.v[tid];
-  __syncthreads();
-  uint32_t out[8] = {};
-  if (v < n && c0 + c < K) {  // K is a multiple of 32: a thread's 16 columns are all there or none is
-    const int64_t e = (int64_t)v * K + c0 + c;
-    const float a = block_scale<DQ>(sc, e >> log2bs, DQ ? sc.offset[0] : 0.f);
-    const uint2 w = *reinterpret_cast<const uint2 *>(packed + (e >> 1));
+  uint32_t w[4] = {};
+  float a[4] = {};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t b = (i < 4 ? w.x : w.y) >> (8 * (i & 3));
-      out[i] = cvt_pair<DT>(tab[b >> 4 & 15] * a, tab[b & 15] * a);
-    }
-    if (W) {
-      uint4 *dst = reinterpret_cast<uint4 *>(W + (int64_t)v * ldw + c);
-      dst[0] = make_uint4(out[0], out[1], out[2], out[3]);
-      dst[1] = make_uint4(out[4], out[5], out[6], out[7]);
+  for (int q = 0; q < 4; ++q) {
+    const int64_t v = (int64_t)blockIdx.y * 64 + 16 * q + row;
+    if (v < n && c < cols) {  // cols is a multiple of 32: a thread's 8 columns are all there or none is
+      const int64_t e = v * K + c0 + c;
+      w[q] = *reinterpret_cast<const uint32_t *>(packed + (e >> 1));
+      a[q] = block_scale<DQ>(sc, e >> log2bs, DQ ? sc.offset[0] : 0.f);
     }
   }
-  if (!Wt) return;
-  uint4 *t = reinterpret_cast<uint4 *>(&tile[row][col]);
-  t[0] = make_uint4(out[0], out[1], out[2], out[3]);
-  t[1] = make_uint4(out[4], out[5], out[6], out[7]);
   __syncthreads();
-  const int lane = tid & 63, wave = tid >> 6;
-  const int64_t oc = (int64_t)blockIdx.x * 64 + lane;
-  if (c0 + oc >= K) return;
-  uint32_t o[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    o[i] = tile[16 * wave + 2 * i][lane] | (uint32_t)tile[16 * wave + 2 * i + 1][lane] << 16;
-  uint4 *dst = reinterpret_cast<uint4 *>(Wt + oc * ldt + blockIdx.y * 64 + 16 * wave);
-  dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
-  dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+  for (int q = 0; q < 4; ++q) {
+    const int64_t v = (int64_t)blockIdx.y * 64 + 16 * q + row;
+    uint32_t o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = cvt_pair<DT>(tab[w[q] >> (8 * i + 4) & 15] * a[q], tab[w[q] >> (8 * i) & 15] * a[q]);
+    const uint4 out = make_uint4(o[0], o[1], o[2], o[3]);
+    if (W && v < n && c < cols) *reinterpret_cast<uint4 *>(W + v * ldw + c) = out;
+    *reinterpret_cast<uint4 *>(&tile[16 * q + row][col ^ (8 * ((16 * q + row) >> 3 & 7))]) = out;
+  }
+  if (!Wt) return;
+  __syncthreads();
+  const int r8 = tid & 7;  // rows 8 r8 .. + 7
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const int oc = 32 * q + (tid >> 3);
+    const int64_t at = (int64_t)blockIdx.x * 128 + oc;
+    if (at >= cols) return;
+    uint32_t o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      o[i] = tile[8 * r8 + 2 * i][oc ^ (8 * r8)] | (uint32_t)tile[8 * r8 + 2 * i + 1][oc ^ (8 * r8)] << 16;
+    *reinterpret_cast<uint4 *>(Wt + at * ldt + blockIdx.y * 64 + 8 * r8) = make_uint4(o[0], o[1], o[2], o[3]);
+  }
 }
 
 hipError_t launch_decode_piece(const Weight4 &w, int dt, int64_t c0, int64_t cols, void *W, int64_t ldw, void *Wt,
                                int64_t ldt, hipStream_t st) {
   const int n = (int)w.N, np = (n + 63) & ~63;
-  const dim3 grid((unsigned)((cols + 63) / 64), (unsigned)(np / 64));
+  const dim3 grid((unsigned)((cols + 127) / 128), (unsigned)(np / 64));
 #define QMV_D(DT, DQV)                                                                                              \
   hipLaunchKernelGGL((decode_piece_kernel<DT, DQV>), grid, dim3(256), 0, st, w.packed, w.sc, w.log2bs,              \
-                     code_values(w.qt), w.K, c0, n, static_cast<uint16_t *>(W), ldw, static_cast<uint16_t *>(Wt), ldt)
+                     code_values(w.qt), w.K, c0, cols, n, static_cast<uint16_t *>(W), ldw, static_cast<uint16_t *>(Wt), ldt)
   if (dt == kF16) {
     if (w.dq) QMV_D(kF16, true);
     else QMV_D(kF16, false);

@@ -166,7 +166,7 @@ __global__ __launch_bounds__(256) void loss_finish_kernel(const int64_t *__restr
                                                           CodeValues table, const float *__restrict__ dloss,
                                                           typename Storage<LDT>::type *__restrict__ loss,
                                                           uint16_t *__restrict__ dx) {
-  __shared__ float z[128], p[128], lt[128], coef[128 + kTail], tab[16], buf[4];
+  __shared__ float z[128], p[128], lt[128], each[128], coef[128 + kTail], tab[16], buf[4], by_block[8][64];
   __shared__ int64_t id[128 + kTail];
   const int64_t i = blockIdx.x;             // its place among the rows of D and rs
   const int64_t t = list ? list[i] : i;
@@ -221,22 +221,19 @@ __global__ __launch_bounds__(256) void loss_finish_kernel(const int64_t *__restr
   }
   if (!dx) return;
   // q - p of every id; by the complements where both are near 1
+  if (tid < k) each[tid] = mine;
+  __syncthreads();
   if (tid < k) {
     float c = 0.f;
     if (own) {
       float pj = 0.f, others_p = 0.f, others_q = rest;
       for (int j = 0; j < k; ++j) {
-        if (id[j] == id[tid]) {
-          pj += p[j];
-        } else {
-          others_p += p[j];
-          bool seen = id[j] < 0;
-          for (int i = 0; i < j; ++i) seen = seen || id[i] == id[j];
-          if (!seen) others_q += expf(lt[j] - M);
-        }
+        const bool same = id[j] == id[tid];
+        pj += same ? p[j] : 0.f;
+        others_p += same ? 0.f : p[j];
+        others_q += same ? 0.f : each[j];
       }
-      const float q = mine / Z;
-      c = pj > 0.5f ? others_p - others_q / Z : q - pj;
+      c = pj > 0.5f ? others_p - others_q / Z : mine / Z - pj;
     }
     coef[tid] = c;
   }
@@ -250,29 +247,55 @@ __global__ __launch_bounds__(256) void loss_finish_kernel(const int64_t *__restr
   const float gain = dloss[t] * inv_tau;
   const float scale = m == -INFINITY ? 0.f : expf(m - M) / Z / kGain<DT>;
   const float offset = DQ ? sc.offset[0] : 0.f;
-  for (int64_t c = tid * 8; c < K; c += 2048) {
-    float acc[8];
+  const int entries = k + tail_n;
+  // 2048 columns at a time, 8 a thread; the entries' rows eight at a time, whose
+  // coefficients times the scales of their blocks (32 columns at least) are in LDS
+  for (int64_t base = 0; base < K; base += 2048) {
+    const int64_t c = base + tid * 8;
+    const bool in = c < K;
+    float acc[8] = {};
+    if (in) {
+      for (int s = 0; s < parts; ++s) {
+        const float4 *d = reinterpret_cast<const float4 *>(D + s * part + i * K + c);
+        const float4 u = d[0], v = d[1];
+        acc[0] += u.x, acc[1] += u.y, acc[2] += u.z, acc[3] += u.w;
+        acc[4] += v.x, acc[5] += v.y, acc[6] += v.z, acc[7] += v.w;
+      }
 #pragma unroll
-    for (int e = 0; e < 8; ++e) acc[e] = D[i * K + c + e];
-    for (int s = 1; s < parts; ++s)
+      for (int e = 0; e < 8; ++e) acc[e] *= scale;
+    }
+    const int log2sub = log2bs < 11 ? log2bs : 11, subs = 2048 >> log2sub;  // blocks in the columns
+    for (int j0 = 0; j0 < entries; j0 += 8) {
+      __syncthreads();
+      for (int b = tid; b < 8 * subs; b += 256) {
+        const int j = j0 + b / subs;
+        const int64_t col = base + ((int64_t)(b % subs) << log2sub);
+        const float cj = j < entries && col < K ? coef[j] : 0.f;
+        by_block[b / subs][b % subs] = cj == 0.f ? 0.f : cj * block_scale<DQ>(sc, (id[j] * K + col) >> log2bs, offset);
+      }
+      __syncthreads();
+      if (!in) continue;
+      uint32_t w[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) acc[e] += D[s * part + i * K + c + e];
+      for (int e = 0; e < 8; ++e) {
+        const int j = j0 + e;
+        w[e] = j < entries && coef[j] != 0.f ? *reinterpret_cast<const uint32_t *>(packed + (id[j] * K + c) / 2) : 0;
+      }
 #pragma unroll
-    for (int e = 0; e < 8; ++e) acc[e] *= scale;
-    for (int j = 0; j < k + tail_n; ++j) {
-      const float cj = coef[j];
-      if (cj == 0.f) continue;
-      const int64_t at = id[j] * K + c;
-      const float a = cj * block_scale<DQ>(sc, at >> log2bs, offset);
-      const uint32_t w = *reinterpret_cast<const uint32_t *>(packed + at / 2);
+      for (int e = 0; e < 8; ++e) {
+        const float a = by_block[e][(8 * tid) >> log2sub];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        acc[2 * e] = fmaf(a, tab[w >> (8 * e + 4) & 15], acc[2 * e]);
-        acc[2 * e + 1] = fmaf(a, tab[w >> (8 * e) & 15], acc[2 * e + 1]);
+        for (int x = 0; x < 4; ++x) {
+          acc[2 * x] = fmaf(a, tab[w[e] >> (8 * x + 4) & 15], acc[2 * x]);
+          acc[2 * x + 1] = fmaf(a, tab[w[e] >> (8 * x) & 15], acc[2 * x + 1]);
+        }
       }
     }
+    if (!in) continue;
+    uint32_t o[4];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) store_elem<DT>(dx, t * K + c + e, acc[e] * gain);
+    for (int e = 0; e < 4; ++e) o[e] = cvt_pair<DT>(acc[2 * e] * gain, acc[2 * e + 1] * gain);
+    *reinterpret_cast<uint4 *>(dx + t * K + c) = make_uint4(o[0], o[1], o[2], o[3]);
   }
 }
 
@@ -366,17 +389,13 @@ __global__ __launch_bounds__(1024) void loss_rows_kernel(const float *__restrict
 
 // D = D f + sums, the part of this workgroup's terms
 struct EpilogueAdd : EpilogueBase {
-  float *D;
+  static constexpr bool kAdds = true;
+  float *C;
   const float *f;
-  int64_t K, part;
+  int64_t ld, part;
   bool first;
-  struct Row {
-    float *p, f;
-  };
-  __device__ Row row(int m) const {
-    return Row{D + blockIdx.y * part + m * K, first ? 0.f : f[m]};
-  }
-  __device__ void store(const Row &r, int n, float v) const { r.p[n] = first ? v : fmaf(r.p[n], r.f, v); }
+  __device__ float *row(int m) const { return C + blockIdx.y * part + m * ld; }
+  __device__ void store(float *row, int n, float v) const { row[n] = v; }
 };
 
 // ---------------------------------------------------------------------------
@@ -398,7 +417,7 @@ static LossPlan loss_plan(int64_t T, int64_t V, int64_t K, int log2bs, int k, bo
   if (p.tiled) {
     // 512 tiles of logits or more; few tiles of D: the piece's terms in parts, each with a D of its own
     const int64_t rows = (p.tokens + kTileM - 1) / kTileM;
-    p.piece = rows >= 16 ? 8192 : rows >= 8 ? 16384 : kMostPiece;
+    p.piece = rows >= 8 ? 16384 : kMostPiece;
     while (p.piece > 8192 && p.piece / 2 >= V) p.piece /= 2;
     const int64_t tiles = rows * ((K + kTileN - 1) / kTileN);
     p.parts = (int)(tiles >= 256 ? 1 : 256 / tiles);
@@ -473,7 +492,7 @@ static hipError_t pieces_tiled(const LossPlan &p, const uint16_t *x, int64_t m, 
     TileArgs b = tile_args(P, np, Wt, np, m, w.K, np);
     b.count = count, b.split = p.split;
     EpilogueAdd add;
-    add.D = D, add.f = rs.f, add.K = w.K, add.part = p.tokens * w.K, add.first = v == 0;
+    add.C = D, add.f = rs.f, add.ld = w.K, add.part = p.tokens * w.K, add.first = v == 0;
     hipLaunchKernelGGL((tile_kernel<DT, EpilogueAdd>), dim3(b.ncol * b.nrow, p.parts), dim3(256), 0, st, b, add);
   }
   return hipGetLastError();

@@ -59,11 +59,12 @@ __global__ __launch_bounds__(256, 1) void tile_kernel(TileArgs g, Epi epi) {
   __shared__ uint4 u0[2048], u1[2048], u2[2048], u3[2048], u4[2048];
   typedef __attribute__((address_space(3))) void lds_t;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  // the tiles that there are take the first workgroups, so that each XCD has its share of them
+  const int M = g.count ? min(g.M, *g.count) : g.M, nrow = (M + kTileM - 1) / kTileM;
+  if ((int)blockIdx.x >= nrow * g.ncol) return;
   int rb, cb;
-  tile_of((int)blockIdx.x, g.ncol, g.nrow, rb, cb);
+  tile_of((int)blockIdx.x, g.ncol, nrow, rb, cb);
   const int m0 = rb * kTileM, n0 = cb * kTileN;
-  const int M = g.count ? min(g.M, *g.count) : g.M;
-  if (m0 >= M) return;
   const int l0 = (int)blockIdx.y * g.split;
   const int KT = (g.L - l0 < g.split ? g.L - l0 : g.split) / kTileL;  // none: zeros
   // loads: wave w moves rows 64 w .. + 63 of A and of B, 8 rows an instruction;
@@ -87,8 +88,10 @@ __global__ __launch_bounds__(256, 1) void tile_kernel(TileArgs g, Epi epi) {
     for (int d = 0; d < 8; ++d)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_t *)(st + (8 * wave + d) * 64), 16, off[d], so, 0, 0);
   };
-  // wave (wm, wn) has rows 128 wm .. + 127 and columns 128 wn .. + 127 of the tile
+  // wave (wm, wn) has rows 128 wm .. + 127 and columns 128 wn .. + 127 of the tile, in 32 x 32
+  // accumulators: column lane % 32, rows 8 (r / 4) + 4 (lane / 32) + r % 4
   const int wm = wave >> 1, wn = wave & 1, h = lane >> 5, l32 = lane & 31;
+  const int mw = m0 + 128 * wm + 4 * h, nw = n0 + 128 * wn + l32;
   tile_acc_t acc[4][4];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
@@ -176,9 +179,36 @@ __global__ __launch_bounds__(256, 1) void tile_kernel(TileArgs g, Epi epi) {
     if (kt + 3 < KT) step(kt + 3, u1, u2, u3, u4, u0);
     __builtin_amdgcn_s_waitcnt((7 << 4) | (15 << 8));  // no load into LDS outlives the kernel
   }
-  // 32 x 32 accumulators: column lane % 32, rows 8 (r / 4) + 4 (lane / 32) + r % 4
-  const int mw = m0 + 128 * wm + 4 * h, nw = n0 + 128 * wn + l32;
   epi.begin(acc, g, M, m0, n0, wm, wn, lane);
+  if constexpr (Epi::kAdds) {
+    // C = C f[row] + sums, in parts of 32 x 128, whose 64 loads are in flight together: bounded
+    // resources (what is not there, or no rows yet, reads as 0 and is not written), no branches,
+    // and no part's loads before the last part's stores, which would not fit the registers
+    const __amdgpu_buffer_rsrc_t rc = make_rsrc(epi.row(m0) + n0, epi.first ? 0 : 0x7fffffffu);
+    const __amdgpu_buffer_rsrc_t ro = make_rsrc(epi.row(m0) + n0, 0x7fffffffu);
+    const __amdgpu_buffer_rsrc_t rf = make_rsrc(epi.f + m0, epi.first ? 0 : (uint32_t)mrows * 4);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      __builtin_amdgcn_sched_barrier(0);
+      float f[16], old[16][4];
+      auto place = [&](int r, int j) __attribute__((always_inline)) {
+        const int m = mw - m0 + 32 * i + 8 * (r >> 2) + (r & 3), n = nw - n0 + 32 * j;
+        return m < mrows && n < ncols ? (uint32_t)((m * (int)epi.ld + n) * 4) : 0x80000000u;
+      };
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        f[r] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rf, (uint32_t)(mw - m0 + 32 * i + 8 * (r >> 2) + (r & 3)) * 4, 0, 0));
+#pragma unroll
+        for (int j = 0; j < 4; ++j) old[r][j] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rc, place(r, j), 0, 0));
+      }
+#pragma unroll
+      for (int r = 0; r < 16; ++r)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(fmaf(old[r][j], f[r], acc[i][j][r])), ro, place(r, j), 0, 0);
+    }
+    return;
+  }
   auto store = [&](auto whole) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -198,6 +228,7 @@ __global__ __launch_bounds__(256, 1) void tile_kernel(TileArgs g, Epi epi) {
 
 // What becomes of the sums: begin() may add to them, row() gives what store() needs of a row.
 struct EpilogueBase {
+  static constexpr bool kAdds = false;  // C f + sums, of members C, f, ld, first
   __device__ void begin(tile_acc_t (&)[4][4], const TileArgs &, int, int, int, int, int, int) const {}
 };
 struct EpilogueF32 : EpilogueBase {  // C[m][n] in fp32
