@@ -42,7 +42,7 @@ typedef struct {
  *   down   [count, rank, K] device, of the activations' type
  *   up     [count, N, rank] device, of the activations' type
  *   scale  [count] device fp32
- *   count  1 .. 65535;  rank  a multiple of 8 in [8, 128], else QMV_ERR_UNSUPPORTED
+ *   count  1 .. 4096;  rank  a multiple of 8 in [8, 128], else QMV_ERR_UNSUPPORTED
  */
 typedef struct {
   const void *down;

@@ -1,22 +1,54 @@
 // Low-rank adapters beside a 4-bit projection (include/qmv/tuning.h):
 //   y[t] = W^ x[t] + bias + up[a] u[t],   u[t] = scale[a] down[a] x[t],   a = index[t]
-// and the gradients of x, down and up.
+// and, with g = dy and v[t] = scale[a] up[a]^T g[t],
+//   dx[t] = W^^T g[t] + down[a]^T v[t],   d_down[a] = sum v[t] x[t]^T,   d_up[a] = sum g[t] u[t]^T.
 //
-// u and v = scale up^T dy are a handful of values a token, held in fp32.  For a
-// few tokens their long sums are cut into pieces, one workgroup each, whose
-// results the next kernel adds up in order.
-#include "qmv_tuning.hpp"
+// A few tokens: the projection in fp32 by gemv_4bit's or gemm_4bit's kernels, then
+// a workgroup for each token and part of the columns.  More: tokens are put in
+// order of their adapters, so that tiles of the matrix cores meet one adapter,
+// or few; u and v, a handful of values a token, are summed in fp32 and carried
+// into the second products as two 16-bit terms.  Many: the weight is decoded
+// once, and the adapters' part is added to the tile product's sums before they
+// are rounded.
+#include "qmv_tile.hpp"
 
 namespace qmv {
 
-// ---------------------------------------------------------------------------
-// u[s][t][r] = scale[a] * sum over piece s of x[t][k] down[a][r][k]
-//
-// A workgroup of 4 waves takes one token and one piece; a wave goes through
-// every fourth r, its lanes along k (16-byte loads).
-// ---------------------------------------------------------------------------
+typedef __attribute__((__vector_size__(4 * sizeof(float)))) float acc4_t;
+
 template <int DT>
-__global__ __launch_bounds__(256) void lora_down_kernel(const uint16_t *__restrict__ x, int64_t K, int piece,
+__device__ __forceinline__ acc4_t mma16(const frag_t &a, const frag_t &b, const acc4_t &c) {
+  if constexpr (DT == kBF16)
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(frag_h_t, a), __builtin_bit_cast(frag_h_t, b), c, 0, 0, 0);
+}
+
+__device__ __forceinline__ frag_t no_frag() { return __builtin_bit_cast(frag_t, make_uint4(0, 0, 0, 0)); }
+
+// Eight values of one column out of rows in LDS (16-bit, `pitch` apart): within 16
+// lanes, lane 4 e + q names 4 columns of row e, and lane i gets column i of rows 0 .. 3.
+// p: this lane's first address; the second four rows lie 4 pitches on.
+__device__ __forceinline__ frag_t read_column(const uint16_t *p, int pitch) {
+  typedef short s4_t __attribute__((ext_vector_type(4)));
+  typedef __attribute__((address_space(3))) s4_t lds_s4_t;
+  const s4_t x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4_t *)p);
+  const s4_t y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4_t *)(p + 4 * pitch));
+  const uint2 a = __builtin_bit_cast(uint2, x), b = __builtin_bit_cast(uint2, y);
+  return __builtin_bit_cast(frag_t, make_uint4(a.x, a.y, b.x, b.y));
+}
+
+// ---------------------------------------------------------------------------
+// A few tokens
+//
+// u[s][t][r] = scale[a] * sum over piece s of x[t][k] down[a][r][k]: a workgroup of
+// 4 waves takes one token and one piece of 512 terms; a wave goes through every
+// fourth r, its lanes along k (16-byte loads, four rows of down in flight).
+// ---------------------------------------------------------------------------
+constexpr int kPiece = 512;
+
+template <int DT>
+__global__ __launch_bounds__(256) void lora_down_kernel(const uint16_t *__restrict__ x, int64_t K,
                                                         const uint16_t *__restrict__ down,
                                                         const float *__restrict__ scale, int count, int R,
                                                         const int32_t *__restrict__ index, float *__restrict__ u,
@@ -25,257 +57,813 @@ __global__ __launch_bounds__(256) void lora_down_kernel(const uint16_t *__restri
   const int a = index[t];
   if (a < 0 || a >= count) return;  // nothing reads this token's u
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t k0 = (int64_t)blockIdx.y * piece;
-  const int64_t k1 = k0 + piece < K ? k0 + piece : K;
+  const int64_t k = (int64_t)blockIdx.y * kPiece + 8 * lane;
+  const bool in = k < K;  // K is a multiple of 32
+  float xf[8] = {};
+  if (in) unpack8<DT>(*reinterpret_cast<const uint4 *>(x + t * K + k), xf);
   const float s = scale[a];
-  for (int r = wave; r < R; r += 4) {
-    const uint16_t *row = down + ((int64_t)a * R + r) * K;
-    float acc = 0.f;
-    for (int64_t k = k0 + 8 * lane; k < k1; k += 512) {
-      float xf[8], af[8];
-      unpack8<DT>(*reinterpret_cast<const uint4 *>(x + t * K + k), xf);
-      unpack8<DT>(*reinterpret_cast<const uint4 *>(row + k), af);
+  const uint16_t *rows = down + (int64_t)a * R * K + (in ? k : 0);
+  for (int r0 = wave; r0 < R; r0 += 16) {
+    uint4 w[4];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) acc = fmaf(xf[i], af[i], acc);
+    for (int q = 0; q < 4; ++q) w[q] = *reinterpret_cast<const uint4 *>(rows + (int64_t)min(r0 + 4 * q, R - 1) * K);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      float af[8], acc = 0.f;
+      unpack8<DT>(w[q], af);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) acc = fmaf(xf[i], in ? af[i] : 0.f, acc);
+      acc = wave_sum(acc);
+      if (lane == 0 && r0 + 4 * q < R) u[((int64_t)blockIdx.y * T + t) * R + r0 + 4 * q] = s * acc;
     }
-    acc = wave_sum(acc);
-    if (lane == 0) u[((int64_t)blockIdx.y * T + t) * R + r] = s * acc;
   }
 }
 
-// v[s][t][r] = scale[a] * sum over piece s of dy[t][n] up[a][n][r]: lanes take 8
-// r's of one n, the rows of a workgroup are added up in LDS.
-template <int DT>
-__global__ __launch_bounds__(256) void lora_down_t_kernel(const uint16_t *__restrict__ dy, int64_t N, int piece,
-                                                          const uint16_t *__restrict__ up,
-                                                          const float *__restrict__ scale, int count, int R,
-                                                          const int32_t *__restrict__ index, float *__restrict__ v,
-                                                          int64_t T) {
-  __shared__ float part[256][9];
-  const int64_t t = blockIdx.x;
-  const int a = index[t];
-  if (a < 0 || a >= count) return;
-  const int groups = R / 8, rows = 256 / groups;
-  const int g = threadIdx.x % groups, row = threadIdx.x / groups;
-  const int64_t n0 = (int64_t)blockIdx.y * piece;
-  const int64_t n1 = n0 + piece < N ? n0 + piece : N;
-  float acc[8] = {};
-  if (row < rows)
-    for (int64_t n = n0 + row; n < n1; n += rows) {
-      const float d = bits16_to_f32<DT>(dy[t * N + n]);
-      float b[8];
-      unpack8<DT>(*reinterpret_cast<const uint4 *>(up + ((int64_t)a * N + n) * R + 8 * g), b);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) acc[i] = fmaf(d, b[i], acc[i]);
-    }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) part[threadIdx.x][i] = acc[i];
-  __syncthreads();
-  if ((int)threadIdx.x < R) {
-    float sum = 0.f;
-    for (int j = 0; j < rows; ++j) sum += part[j * groups + threadIdx.x / 8][threadIdx.x % 8];
-    v[((int64_t)blockIdx.y * T + t) * R + threadIdx.x] = scale[a] * sum;
-  }
-}
-
-// The pieces of u (v), added up in order, into LDS; returns whether the token
-// has an adapter.  One barrier.
-__device__ __forceinline__ bool gather_u(const float *__restrict__ u, int pieces, int64_t T, int64_t t, int R, int a,
-                                         int count, float *dst) {
-  const bool there = a >= 0 && a < count;
-  if (there)
-    for (int r = threadIdx.x; r < R; r += blockDim.x) {
-      float sum = 0.f;
-      for (int s = 0; s < pieces; ++s) sum += u[((int64_t)s * T + t) * R + r];
-      dst[r] = sum;
-    }
-  __syncthreads();
-  return there;
-}
-
-// out[t][n] = round(base[t][n] + bias[n] + sum_r up[a][n][r] u[t][r])
+// out[t][n] = round(base[t][n] + bias[n] + sum_r up[a][n][r] u[t][r]), u's pieces
+// added up in order: 256 / R of them side by side, then those sums
 template <int DT, int ODT>
 __global__ __launch_bounds__(256) void lora_up_kernel(const float *__restrict__ base, int64_t N,
                                                       const uint16_t *__restrict__ up, int count, int R,
                                                       const int32_t *__restrict__ index, const float *__restrict__ u,
                                                       int pieces, int64_t T, const uint16_t *__restrict__ bias,
                                                       typename Storage<ODT>::type *__restrict__ out) {
-  __shared__ float us[128];
+  __shared__ float part[256], us[128];
   const int64_t t = blockIdx.y;
-  const int a = index[t];
-  const bool there = gather_u(u, pieces, T, t, R, a, count, us);
   const int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (n >= N) return;
-  float acc = 0.f;
-  if (there) {
-    const uint16_t *row = up + ((int64_t)a * N + n) * R;
-    for (int r = 0; r < R; r += 8) {
-      float b[8];
-      unpack8<DT>(*reinterpret_cast<const uint4 *>(row + r), b);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) acc = fmaf(us[r + i], b[i], acc);
-    }
-  }
-  acc += base[t * N + n];
-  if (bias) acc += bits16_to_f32<DT>(bias[n]);
-  store_elem<ODT>(out, t * N + n, acc);
-}
-
-// out[t][k] = round(base[t][k] + sum_r down[a][r][k] v[t][r]): 8 columns a thread
-template <int DT, int ODT>
-__global__ __launch_bounds__(256) void lora_up_t_kernel(const float *__restrict__ base, int64_t K,
-                                                        const uint16_t *__restrict__ down, int count, int R,
-                                                        const int32_t *__restrict__ index,
-                                                        const float *__restrict__ v, int pieces, int64_t T,
-                                                        typename Storage<ODT>::type *__restrict__ out) {
-  __shared__ float vs[128];
-  const int64_t t = blockIdx.y;
   const int a = index[t];
-  const bool there = gather_u(v, pieces, T, t, R, a, count, vs);
-  const int64_t k = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
-  if (k >= K) return;
-  float acc[8] = {};
-  if (there)
-    for (int r = 0; r < R; ++r) {
-      float d[8];
-      unpack8<DT>(*reinterpret_cast<const uint4 *>(down + ((int64_t)a * R + r) * K + k), d);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) acc[i] = fmaf(vs[r], d[i], acc[i]);
-    }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) store_elem<ODT>(out, t * K + k + i, acc[i] + base[t * K + k + i]);
-}
-
-// u[t][r] = the sum of its pieces, in order
-__global__ void lora_sum_kernel(const float *__restrict__ parts, int pieces, int64_t n, float *__restrict__ u) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= n) return;
-  float sum = 0.f;
-  for (int s = 0; s < pieces; ++s) sum += parts[s * n + i];
-  u[i] = sum;
-}
-
-// sum over the tokens t of adapter a of g[t][w] h[t][r]: at [a][w][r] (UP) or [a][r][w]
-template <int DT, int ODT, bool UP>
-__global__ __launch_bounds__(64) void lora_grad_kernel(const uint16_t *__restrict__ g, int64_t W,
-                                                       const float *__restrict__ h, int R,
-                                                       const int32_t *__restrict__ index, int64_t T,
-                                                       typename Storage<ODT>::type *__restrict__ out) {
-  const int64_t w = (int64_t)blockIdx.x * 64 + threadIdx.x;
-  const int r0 = 8 * blockIdx.y, a = blockIdx.z;
-  float acc[8] = {};
-  for (int64_t t = 0; t < T; ++t) {
-    if (index[t] != a) continue;
-    const float gv = w < W ? bits16_to_f32<DT>(g[t * W + w]) : 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) acc[i] = fmaf(gv, h[t * R + r0 + i], acc[i]);
+  float acc = 0.f, more = 0.f;
+  if (n < N) {
+    acc = base[t * N + n];
+    if (bias) more = bits16_to_f32<DT>(bias[n]);
   }
-  if (w >= W) return;
+  if (a >= 0 && a < count) {
+    const uint16_t *row = up + ((int64_t)a * N + (n < N ? n : N - 1)) * R;
+    uint4 first[2];  // in flight while u is added up
+    first[0] = *reinterpret_cast<const uint4 *>(row);
+    first[1] = *reinterpret_cast<const uint4 *>(row + (R > 8 ? 8 : 0));
+    const int side = 256 / R, r = threadIdx.x % R, g = threadIdx.x / R;
+    float sum = 0.f;
+    if (g < side)
+      for (int s = g; s < pieces; s += side) sum += u[((int64_t)s * T + t) * R + r];
+    part[threadIdx.x] = sum;
+    __syncthreads();
+    if ((int)threadIdx.x < R) {
+      sum = part[r];
+      for (int j = 1; j < side && j < pieces; ++j) sum += part[j * R + r];
+      us[r] = sum;
+    }
+    __syncthreads();
+    float adapter = 0.f;
+#pragma unroll 2
+    for (int c = 0; c < R; c += 8) {
+      float b[8];
+      unpack8<DT>(c == 0 ? first[0] : c == 8 ? first[1] : *reinterpret_cast<const uint4 *>(row + c), b);
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    store_elem<ODT>(out, UP ? ((int64_t)a * W + w) * R + r0 + i : ((int64_t)a * R + r0 + i) * W + w, acc[i]);
+      for (int i = 0; i < 8; ++i) adapter = fmaf(us[c + i], b[i], adapter);
+    }
+    acc += adapter;
+  }
+  if (n < N) store_elem<ODT>(out, t * N + n, acc + more);
 }
 
 // ---------------------------------------------------------------------------
-constexpr int64_t kRows = 4096;  // tokens whose projection is in the workspace at a time
-constexpr int kPiece = 512;      // terms of a piece of u and v for few tokens
+// Tokens in order of their adapters
+// ---------------------------------------------------------------------------
+constexpr int kMostAdapters = 4096;
+constexpr int kUnit = 64;  // most places of a unit
 
-static int pieces_of(int64_t T, int64_t width) { return T <= 64 ? (int)((width + kPiece - 1) / kPiece) : 1; }
-
-struct LoraPlan {
-  size_t base, u, v, parts, back, total;
+struct Places {
+  int32_t *order;    // [T] token at a place; those without an adapter come last
+  int32_t *adapter;  // [T] its adapter (count: none)
+  int32_t *start;    // [count + 2] first place of each adapter, of those without, and T
+  int4 *units;       // (adapter, first place, last place + 1): at most 64 places of one adapter
+  int32_t *n_units;
 };
 
-static LoraPlan lora_plan(int64_t T, int64_t N, int64_t K, int log2bs, int R, bool backward) {
+// Every workgroup counts all tokens (and those before its own 256), so that one
+// launch without atomics on global memory gives a stable order; the first one
+// writes the adapters' places and the units as well.
+__global__ __launch_bounds__(256) void lora_order_kernel(const int32_t *__restrict__ index, int T, int count, Places pl) {
+  __shared__ __attribute__((aligned(16))) int mine[256];
+  __shared__ int total[kMostAdapters + 1], before[kMostAdapters + 1], sums[4];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, t0 = blockIdx.x * 256;
+  const int buckets = count + 1;
+  auto bucket = [&](int t) {
+    const int a = index[t];
+    return a >= 0 && a < count ? a : count;
+  };
+  for (int b = tid; b < buckets; b += 256) total[b] = before[b] = 0;
+  const int my = t0 + tid < T ? bucket(t0 + tid) : -1;
+  mine[tid] = my;
+  __syncthreads();
+  for (int base = 0; base < T; base += 256) {
+    const int t = base + tid;
+    if (t >= T) break;
+    const int b = bucket(t);
+    const int one = __builtin_amdgcn_readfirstlane(b);
+    const uint64_t here = __ballot(1);
+    if (__ballot(b == one) == here) {  // prompts: neighbours have one adapter
+      if (lane == __builtin_ctzll(here)) {
+        atomicAdd(&total[one], __builtin_popcountll(here));
+        if (base < t0) atomicAdd(&before[one], __builtin_popcountll(here));
+      }
+    } else {
+      atomicAdd(&total[b], 1);
+      if (base < t0) atomicAdd(&before[b], 1);
+    }
+  }
+  __syncthreads();
+  // totals (and, in the first workgroup, units) to the sums before them
+  const int each = (buckets + 255) / 256, b0 = min(tid * each, buckets), b1 = min(b0 + each, buckets);
+  auto scan = [&](int v) {  // exclusive over the threads; the same barriers in every thread
+    int upto = v;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int w = __shfl_up(upto, o);
+      if (lane >= o) upto += w;
+    }
+    __syncthreads();
+    if (lane == 63) sums[wave] = upto;
+    __syncthreads();
+    for (int w = 0; w < wave; ++w) upto += sums[w];
+    return upto - v;
+  };
+  int tokens = 0, units = 0;
+  for (int b = b0; b < b1; ++b) {
+    tokens += total[b];
+    units += (total[b] + kUnit - 1) / kUnit;
+  }
+  int at = scan(tokens), unit = scan(units);
+  if (blockIdx.x == 0) {
+    int place = at;
+    for (int b = b0; b < b1; ++b) {
+      pl.start[b] = place;
+      const int end = place + total[b];
+      for (; place < end; place += kUnit) pl.units[unit++] = make_int4(b, place, min(place + kUnit, end), 0);
+      place = end;
+    }
+    if (tid == 255) {
+      pl.start[buckets] = T;
+      *pl.n_units = unit;
+    }
+  }
+  for (int b = b0; b < b1; ++b) {
+    const int n = total[b];
+    total[b] = at;
+    at += n;
+  }
+  __syncthreads();
+  if (my < 0) return;
+  int rank = 0;
+  const int4 *m4 = reinterpret_cast<const int4 *>(mine);
+  for (int i = 0; i < 64; ++i) {
+    if (4 * i >= tid) break;
+    const int4 m = m4[i];
+    rank += (m.x == my) + (4 * i + 1 < tid && m.y == my) + (4 * i + 2 < tid && m.z == my) + (4 * i + 3 < tid && m.w == my);
+  }
+  const int p = total[my] + before[my] + rank;
+  pl.order[p] = t0 + tid;
+  pl.adapter[p] = my;
+}
+
+// ---------------------------------------------------------------------------
+// parts[s][p][r] = scale[a] * sum over piece s of x[order[p]][l] down[a][r][l], or with
+// TRANS of dy[..][l] up[a][l][r]: the inner values of the tokens, by place.
+//
+// A workgroup takes a unit and a piece of the sum, a wave every fourth 64 terms of
+// it: 4 x NT tiles of v_mfma_f32_16x16x32, whose operands come straight from
+// memory (rows are read once, an adapter's factor from L2).  With TRANS the
+// factor's rows run the other way: 32 of them go through a part of LDS that is
+// the wave's own, and come back by columns.  Waves are added up through LDS in
+// order.  Bound by the read of the rows.
+// ---------------------------------------------------------------------------
+template <int DT, int NT, bool TRANS>
+__global__ __launch_bounds__(256) void lora_shrink_kernel(const uint16_t *__restrict__ x, int64_t L, int piece,
+                                                          const uint16_t *__restrict__ factor,
+                                                          const float *__restrict__ scale, int count, int R, Places pl,
+                                                          float *__restrict__ parts, int64_t T) {
+  constexpr int kPitch = 16 * NT + (NT == 1 ? 0 : 16);  // rows 8 (mod 64) banks apart
+  __shared__ __attribute__((aligned(16))) union {
+    float red[4][4 * NT][64];
+    uint16_t turn[TRANS ? 4 : 1][TRANS ? 32 * kPitch : 1];
+  } sh;
+  if ((int)blockIdx.x >= *pl.n_units) return;
+  const int4 unit = pl.units[blockIdx.x];
+  const int a = unit.x, places = unit.z - unit.y;
+  if (a >= count) return;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l16 = lane & 15, g = lane >> 4;
+  const uint16_t *row[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) row[i] = x + (int64_t)pl.order[unit.y + min(16 * i + l16, places - 1)] * L + 8 * g;
+  const uint16_t *frow[NT];  // columns past R: the last one again, not stored
+#pragma unroll
+  for (int j = 0; j < NT; ++j) frow[j] = factor + ((int64_t)a * R + min(16 * j + l16, R - 1)) * L + 8 * g;
+  int turn_from[NT], turn_to[NT];  // TRANS: 16-byte chunks of 32 rows of R
+  uint16_t *turn = sh.turn[TRANS ? wave : 0];
+#pragma unroll
+  for (int j = 0; j < NT; ++j) {
+    const int c = 64 * j + lane, per = R / 8;
+    turn_from[j] = c < 32 * per ? c * 8 : -1;
+    turn_to[j] = (c / per) * kPitch + 8 * (c % per);
+  }
+  acc4_t acc[4][NT];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < NT; ++j) acc[i][j] = acc4_t{0.f, 0.f, 0.f, 0.f};
+  const int64_t l0 = (int64_t)blockIdx.y * piece, l1 = l0 + piece < L ? l0 + piece : L;
+  for (int64_t l = l0 + 64 * wave; l < l1; l += 256) {
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      const int64_t k = l + 32 * s;
+      if (k >= l1) break;  // L is a multiple of 32
+      frag_t xa[4], fb[NT];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) xa[i] = __builtin_bit_cast(frag_t, *reinterpret_cast<const uint4 *>(row[i] + k));
+      if constexpr (TRANS) {
+        const uint16_t *from = factor + ((int64_t)a * L + k) * R;
+        uint4 v[NT];
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+          if (turn_from[j] >= 0) v[j] = *reinterpret_cast<const uint4 *>(from + turn_from[j]);
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+          if (turn_from[j] >= 0) *reinterpret_cast<uint4 *>(turn + turn_to[j]) = v[j];
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");  // the wave's own LDS, in order
+#pragma unroll
+        for (int j = 0; j < NT; ++j) fb[j] = read_column(turn + (8 * g + (l16 >> 2)) * kPitch + 16 * j + 4 * (l16 & 3), kPitch);
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      } else {
+#pragma unroll
+        for (int j = 0; j < NT; ++j) fb[j] = __builtin_bit_cast(frag_t, *reinterpret_cast<const uint4 *>(frow[j] + k));
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) acc[i][j] = mma16<DT>(xa[i], fb[j], acc[i][j]);
+    }
+  }
+  const float sc = scale[a];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (16 * i >= places) break;
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) sh.red[wave][4 * j + q][lane] = acc[i][j][q];
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      const float sum = ((sh.red[0][4 * j + wave][lane] + sh.red[1][4 * j + wave][lane]) + sh.red[2][4 * j + wave][lane]) +
+                        sh.red[3][4 * j + wave][lane];
+      const int p = 16 * i + 4 * g + wave, r = 16 * j + l16;
+      if (p < places && r < R) parts[((int64_t)blockIdx.y * T + unit.y + p) * R + r] = sc * sum;
+    }
+  }
+}
+
+// The parts added up in order, as two 16-bit terms [T][Rp] (Rp: R up to a multiple
+// of 16, zeros past R): the first is off by half a step, the second by half a step of that
+struct Split {
+  const float *parts;
+  int pieces;
+  uint16_t *hi, *lo;
+};
+template <int DT>
+__global__ __launch_bounds__(256) void lora_split_kernel(Split one, Split two, int64_t T, int R, int Rp, int count,
+                                                         const int32_t *__restrict__ start) {
+  const Split s = blockIdx.y ? two : one;
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= T * Rp) return;
+  const int64_t p = i / Rp;
+  const int r = (int)(i % Rp);
+  float sum = 0.f;
+  if (r < R && p < start[count])
+    for (int k = 0; k < s.pieces; ++k) sum += s.parts[(k * T + p) * R + r];
+  const uint32_t hi = f32_to_bits16<DT>(sum);
+  s.hi[i] = (uint16_t)hi;
+  s.lo[i] = (uint16_t)f32_to_bits16<DT>(sum - bits16_to_f32<DT>(hi));
+}
+
+// ---------------------------------------------------------------------------
+// The adapters' part of sums over places [p0, p0 + 32 MI) and columns: for each
+// run of one adapter, its inner values (rows of other runs as zeros) times its
+// factor, 16 ranks an instruction, the two terms one after the other.
+// ---------------------------------------------------------------------------
+struct LowRank {
+  const uint16_t *hi, *lo;  // [T][Rp]
+  const uint16_t *factor;   // up [count][width][R], or down [count][R][width]
+  int64_t width;
+  int R, Rp, count;
+  const int32_t *adapter, *start;
+};
+
+template <int DT, bool TRANS, int MI, int NJ>
+__device__ __forceinline__ void add_low_rank(tile_acc_t (&acc)[MI][NJ], const LowRank &lr, int p0, int end, int64_t c0,
+                                             int64_t cols, int lane) {
+  const int h = lane >> 5, l32 = lane & 31;
+  for (int p = p0; p < end;) {
+    const int a = __builtin_amdgcn_readfirstlane(lr.adapter[p]);
+    if (a >= lr.count) break;  // those without an adapter come last
+    const int past = __builtin_amdgcn_readfirstlane(min(lr.start[a + 1], end));
+    for (int k0 = 0; k0 < lr.Rp; k0 += 16) {
+      const int k = k0 + 8 * h;
+      frag_t b[NJ];
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) {
+        const int64_t c = c0 + 32 * j + l32;
+        b[j] = no_frag();
+        if (k < lr.R && c < cols) {
+          if constexpr (TRANS) {
+            const uint16_t *f = lr.factor + ((int64_t)a * lr.R + k) * lr.width + c;
+            uint32_t v[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = f[2 * e * lr.width] | (uint32_t)f[(2 * e + 1) * lr.width] << 16;
+            b[j] = __builtin_bit_cast(frag_t, make_uint4(v[0], v[1], v[2], v[3]));
+          } else {
+            b[j] = __builtin_bit_cast(frag_t, *reinterpret_cast<const uint4 *>(lr.factor + ((int64_t)a * lr.width + c) * lr.R + k));
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < MI; ++i) {
+        const int q = p0 + 32 * i + l32;
+        const bool in = q >= p && q < past;
+        const int64_t at = (int64_t)(in ? q : p) * lr.Rp + k;
+        const uint4 vh = *reinterpret_cast<const uint4 *>(lr.hi + at), vl = *reinterpret_cast<const uint4 *>(lr.lo + at);
+        const frag_t hi = in ? __builtin_bit_cast(frag_t, vh) : no_frag();
+        const frag_t lo = in ? __builtin_bit_cast(frag_t, vl) : no_frag();
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) acc[i][j] = tile_mma<DT>(lo, b[j], tile_mma<DT>(hi, b[j], acc[i][j]));
+      }
+    }
+    p = past;
+  }
+}
+
+// out[t][c] = round(base[t][c] + bias[c] + the adapter's part): a unit and 256 columns
+// a workgroup, 64 columns a wave.  Bound by base and out.
+template <int DT, int ODT, bool TRANS>
+__global__ __launch_bounds__(256) void lora_expand_kernel(const float *__restrict__ base, LowRank lr, Places pl,
+                                                          const uint16_t *__restrict__ bias,
+                                                          typename Storage<ODT>::type *__restrict__ out) {
+  if ((int)blockIdx.x >= *pl.n_units) return;
+  const int4 unit = pl.units[blockIdx.x];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, h = lane >> 5, l32 = lane & 31;
+  const int64_t c0 = (int64_t)blockIdx.y * 256 + 64 * wave;
+  if (c0 >= lr.width) return;
+  tile_acc_t acc[2][2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
+  if (unit.x < lr.count) add_low_rank<DT, TRANS, 2, 2>(acc, lr, unit.y, unit.z, c0, lr.width, lane);
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+      const int p = unit.y + 32 * i + 8 * (r >> 2) + 4 * h + (r & 3);
+      if (p >= unit.z) continue;
+      const int64_t t = pl.order[p];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int64_t c = c0 + 32 * j + l32;
+        if (c >= lr.width) continue;
+        float v = acc[i][j][r] + base[t * lr.width + c];
+        if (bias) v += bits16_to_f32<DT>(bias[c]);
+        store_elem<ODT>(out, t * lr.width + c, v);
+      }
+    }
+}
+
+// The tile product's sums, rows by place, with the adapters' part and the bias; row's token
+template <int DT, int ODT, bool TRANS>
+struct EpilogueLora : EpilogueBase {
+  using OT = typename Storage<ODT>::type;
+  LowRank lr;           // factor from this piece's first column on
+  const int32_t *order;
+  const uint16_t *bias;
+  OT *out;
+  int64_t ld;
+  __device__ void begin(tile_acc_t (&acc)[4][4], const TileArgs &g, int M, int m0, int n0, int wm, int wn, int lane) const {
+    add_low_rank<DT, TRANS, 4, 4>(acc, lr, m0 + 128 * wm, min(m0 + 128 * wm + 128, M), n0 + 128 * wn, g.N, lane);
+  }
+  __device__ OT *row(int m) const { return out + order[m] * ld; }
+  __device__ void store(OT *row, int n, float v) const {
+    store_elem<ODT>(row, n, bias ? v + bits16_to_f32<DT>(bias[n]) : v);
+  }
+};
+
+// ---------------------------------------------------------------------------
+// The adapters' gradients: sum over the places p of adapter a of g[order[p]][w] h[p][r],
+// at [a][w][r] (UP: g = dy, h = u) or [a][r][w] (g = x, h = v).
+//
+// A workgroup takes a window of places and 128 columns w; for each run of one
+// adapter in the window it multiplies 32 places at a time, rows outside of the
+// run as zeros: both operands are wanted by columns, and come out of LDS so.
+// A wave has 32 columns and all ranks.  An adapter whose places lie in one
+// window is done then; a part of a run that goes on is left in fp32 (a window
+// has two at most: one that began before it, and one that goes on after), and
+// lora_join_kernel adds an adapter's parts in order.  Bound by the read of g.
+// ---------------------------------------------------------------------------
+template <int DT, int ODT, int NT, bool UP>
+__global__ __launch_bounds__(256) void lora_grad_kernel(const uint16_t *__restrict__ gp, int64_t W,
+                                                        const uint16_t *__restrict__ hi, const uint16_t *__restrict__ lo,
+                                                        int R, int Rp, int count, int window, Places pl,
+                                                        float *__restrict__ parts,
+                                                        typename Storage<ODT>::type *__restrict__ out) {
+  constexpr int kG = 128 + 16, kH = 32 * NT + 16;  // pitches: rows 8 (mod 64) banks apart
+  __shared__ __attribute__((aligned(16))) uint16_t gs[32 * kG], hs[2][32 * kH];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, l32 = lane & 31, h = lane >> 5;
+  const int64_t w0 = (int64_t)blockIdx.x * 128;
+  const int first = blockIdx.y * window, there = pl.start[count];
+  const int last = min(first + window, there);
+  const int grow = tid >> 4, gcol = 8 * (tid & 15);
+  // this lane's address for a column of 8 places: read_column
+  const int i16 = lane & 15, part = (lane >> 4) & 1;
+  const int place = 8 * h + (i16 >> 2), col = 16 * part + 4 * (i16 & 3);
+  for (int p = first; p < last;) {
+    const int a = __builtin_amdgcn_readfirstlane(pl.adapter[p]);
+    const int begin = __builtin_amdgcn_readfirstlane(pl.start[a]), past = __builtin_amdgcn_readfirstlane(pl.start[a + 1]);
+    const int end = min(past, last);
+    tile_acc_t acc[NT];
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[j][r] = 0.f;
+    constexpr int NH = (NT + 1) / 2;  // 32 places x 32 NT ranks of a term, 16 bytes a thread
+    uint4 gv[2], hv[2][NH];
+    auto load = [&](int q) {
+      const uint4 none = make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const int at = q + grow + 16 * s;
+        gv[s] = at < end && w0 + gcol < W ? *reinterpret_cast<const uint4 *>(gp + (int64_t)pl.order[at] * W + w0 + gcol) : none;
+      }
+#pragma unroll
+      for (int j = 0; j < NH; ++j) {
+        const int c = 256 * j + tid, at = q + c / (4 * NT), r = 8 * (c % (4 * NT));
+        const bool in = c < 128 * NT && at < end && r < Rp;
+        hv[0][j] = in ? *reinterpret_cast<const uint4 *>(hi + (int64_t)at * Rp + r) : none;
+        hv[1][j] = in ? *reinterpret_cast<const uint4 *>(lo + (int64_t)at * Rp + r) : none;
+      }
+    };
+    load(p);
+    for (int q = p; q < end; q += 32) {
+      __syncthreads();
+#pragma unroll
+      for (int s = 0; s < 2; ++s) *reinterpret_cast<uint4 *>(gs + (grow + 16 * s) * kG + gcol) = gv[s];
+#pragma unroll
+      for (int j = 0; j < NH; ++j) {
+        const int c = 256 * j + tid;
+        if (c < 128 * NT) {
+          *reinterpret_cast<uint4 *>(hs[0] + (c / (4 * NT)) * kH + 8 * (c % (4 * NT))) = hv[0][j];
+          *reinterpret_cast<uint4 *>(hs[1] + (c / (4 * NT)) * kH + 8 * (c % (4 * NT))) = hv[1][j];
+        }
+      }
+      __syncthreads();
+      if (q + 32 < end) load(q + 32);
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const frag_t gf = read_column(gs + (16 * s + place) * kG + 32 * wave + col, kG);
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int term = 0; term < 2; ++term) {
+            const frag_t hf = read_column(hs[term] + (16 * s + place) * kH + 32 * j + col, kH);
+            acc[j] = UP ? tile_mma<DT>(gf, hf, acc[j]) : tile_mma<DT>(hf, gf, acc[j]);
+          }
+      }
+    }
+    const bool whole = begin >= first && past <= last;
+    float *keep = parts + (int64_t)(2 * blockIdx.y + (begin >= first)) * W * R;
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        const int in = 8 * (r >> 2) + 4 * h + (r & 3);  // row of the 32 x 32 sums, l32 its column
+        const int64_t w = w0 + 32 * wave + (UP ? in : l32);
+        const int rank = 32 * j + (UP ? l32 : in);
+        if (w >= W || rank >= R) continue;
+        const int64_t at = UP ? w * R + rank : rank * W + w;
+        if (whole) store_elem<ODT>(out, (int64_t)a * W * R + at, acc[j][r]);
+        else keep[at] = acc[j][r];
+      }
+    p = end;
+  }
+}
+
+// What lora_grad_kernel left: sums of an adapter's parts, and zeros for one without tokens.
+template <int ODT>
+__global__ __launch_bounds__(256) void lora_join_kernel(const float *__restrict__ parts, int64_t n, int window,
+                                                        const int32_t *__restrict__ start,
+                                                        typename Storage<ODT>::type *__restrict__ out) {
+  const int a = blockIdx.y, begin = start[a], past = start[a + 1];
+  const int from = begin / window, to = (past - 1) / window;
+  if (begin < past && from == to) return;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+    float sum = 0.f;
+    if (begin < past) {
+      sum = parts[(int64_t)(2 * from + 1) * n + i];
+      for (int w = from + 1; w <= to; ++w) sum += parts[(int64_t)(2 * w) * n + i];
+    }
+    store_elem<ODT>(out, a * n + i, sum);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// host
+// ---------------------------------------------------------------------------
+constexpr int64_t kFew = 32;        // tokens up to which a token is a workgroup's
+constexpr int64_t kTiledFrom = 768;  // tokens from which the weight is decoded for the tile product
+constexpr int64_t kRows = 4096;     // tokens of a fp32 projection in the workspace
+constexpr int64_t kTiledRows = 16384;
+constexpr int64_t kDecoded = (int64_t)1 << 27;  // elements of a decoded piece, about
+
+static int few_pieces(int64_t width) { return (int)((width + kPiece - 1) / kPiece); }
+static int64_t most_units(int64_t T, int count) { return (T + kUnit - 1) / kUnit + (T < count + 1 ? T : count + 1); }
+
+// Pieces of the inner values' sums: a workgroup for each of 512 units and pieces, 256 terms at least
+static int inner_pieces(int64_t T, int64_t L, int count) {
+  int64_t s = 512 / most_units(T, count);
+  if (s > L / 256) s = L / 256;
+  return s < 1 ? 1 : (int)s;
+}
+static int inner_piece(int64_t L, int pieces) { return (int)(((L + pieces - 1) / pieces + 63) & ~(int64_t)63); }
+
+struct InnerPlan {
+  int pieces, piece;
+  size_t parts, hi, lo;
+};
+static InnerPlan inner_plan(Carver &c, int64_t T, int64_t L, int R, int count) {
+  InnerPlan p{};
+  p.piece = inner_piece(L, inner_pieces(T, L, count));
+  p.pieces = (int)((L + p.piece - 1) / p.piece);
+  const int64_t Rp = (R + 15) & ~15;
+  p.parts = c.take((size_t)p.pieces * T * R * 4);
+  p.hi = c.take((size_t)T * Rp * 2), p.lo = c.take((size_t)T * Rp * 2);
+  return p;
+}
+
+struct PlacesPlan {
+  size_t order, adapter, start, units, n_units;
+};
+static PlacesPlan places_plan(Carver &c, int64_t T, int count) {
+  PlacesPlan p{};
+  p.order = c.take((size_t)T * 4), p.adapter = c.take((size_t)T * 4), p.start = c.take((size_t)(count + 2) * 4);
+  p.units = c.take((size_t)most_units(T, count) * 16), p.n_units = c.take(4);
+  return p;
+}
+static Places places_at(const PlacesPlan &p, char *ws) {
+  return Places{reinterpret_cast<int32_t *>(ws + p.order), reinterpret_cast<int32_t *>(ws + p.adapter),
+                reinterpret_cast<int32_t *>(ws + p.start), reinterpret_cast<int4 *>(ws + p.units),
+                reinterpret_cast<int32_t *>(ws + p.n_units)};
+}
+
+// The product of tokens with a 4-bit weight: width [N] outputs of sums over [K] (forward) or the other way round
+struct ProductPlan {
+  bool tiled;
+  int64_t tokens;      // at a time
+  int64_t piece;       // columns of the output whose weights are decoded at a time
+  size_t base, back;   // fp32 projection, the backward product's own workspace
+  size_t decoded;
+};
+static ProductPlan product_plan(Carver &c, int64_t T, int64_t N, int64_t K, int log2bs, bool backward) {
+  ProductPlan p{};
+  const int64_t L = backward ? N : K, width = backward ? K : N;
+  p.tiled = T >= kTiledFrom && L % 64 == 0 && L <= 65536 && width <= ((int64_t)1 << 30);
+  const int64_t most = p.tiled ? kTiledRows : kRows, turns = (T + most - 1) / most;
+  p.tokens = (T + turns - 1) / turns;
+  if (p.tiled) {
+    p.piece = kDecoded / L & ~(int64_t)4095;  // L is at most 2^16: 2048 .. ; rows_of wants 4096 rows
+    if (p.piece < 4096) p.piece = 4096;
+    if (p.piece > width) p.piece = width;
+    p.decoded = c.take((size_t)p.piece * L * 2);
+  } else {
+    p.base = c.take((size_t)p.tokens * width * 4);
+    if (backward) {
+      size_t need = 0;
+      for (int64_t m : {p.tokens, T % p.tokens})
+        if (m > 0) {
+          const size_t b = gemm_backward_workspace_bytes(m, N, K, log2bs);
+          need = b > need ? b : need;
+        }
+      p.back = c.take(need);
+    }
+  }
+  return p;
+}
+
+// Windows of the gradients: about 768 workgroups, 64 places at least
+static int grad_window(int64_t T, int64_t W) {
+  const int64_t tiles = (W + 127) / 128;
+  int64_t w = (T * tiles / 768 + 31) & ~(int64_t)31;
+  if (w < 64) w = 64;
+  return (int)(w < T ? w : T);
+}
+
+struct LoraPlan {
+  bool few;
+  ProductPlan product;
+  int64_t tokens;
+  size_t u_few;
+  PlacesPlan places;
+  InnerPlan inner;  // of the product: u forward, v backward
+  // backward: for all tokens
+  PlacesPlan all;
+  InnerPlan u, v;
+  int window_down, window_up;
+  size_t parts, total;
+};
+
+static LoraPlan lora_plan(int64_t T, int64_t N, int64_t K, int log2bs, int count, int R, bool backward) {
   LoraPlan p{};
   Carver c;
-  const int64_t rows = T < kRows ? T : kRows;
-  p.base = c.take((size_t)rows * (backward ? K : N) * 4);
-  p.u = c.take((size_t)T * R * 4 * pieces_of(T, K));
+  p.few = !backward && T <= kFew;
+  p.product = product_plan(c, T, N, K, log2bs, backward);
+  p.tokens = p.product.tokens;
+  if (p.few) {
+    p.u_few = c.take((size_t)few_pieces(K) * T * R * 4);
+  } else {
+    p.places = places_plan(c, p.tokens, count);
+    p.inner = inner_plan(c, p.tokens, backward ? N : K, R, count);
+  }
   if (backward) {
-    p.v = c.take((size_t)T * R * 4 * pieces_of(T, N));
-    p.parts = c.take((size_t)T * R * 4 * 2);
-    const size_t a = gemm_backward_workspace_bytes(rows, N, K, log2bs);
-    const size_t b = T > kRows && T % kRows ? gemm_backward_workspace_bytes(T % kRows, N, K, log2bs) : 0;
-    p.back = c.take(a > b ? a : b);
+    if (p.tokens < T) {
+      p.all = places_plan(c, T, count);
+      p.v = inner_plan(c, T, N, R, count);
+    } else {
+      p.all = p.places;
+      p.v = p.inner;
+    }
+    p.u = inner_plan(c, T, K, R, count);
+    p.window_down = grad_window(T, K), p.window_up = grad_window(T, N);
+    const size_t a = 2 * (size_t)((T + p.window_down - 1) / p.window_down) * K * R * 4;
+    const size_t b = 2 * (size_t)((T + p.window_up - 1) / p.window_up) * N * R * 4;
+    p.parts = c.take(a > b ? a : b);
   }
   p.total = c.at;
   return p;
 }
 
-size_t lora_workspace(int64_t T, int64_t N, int64_t K, int log2bs, int, int rank, bool backward) {
-  return lora_plan(T, N, K, log2bs, rank, backward).total;
+size_t lora_workspace(int64_t T, int64_t N, int64_t K, int log2bs, int count, int rank, bool backward) {
+  return lora_plan(T, N, K, log2bs, count, rank, backward).total;
+}
+
+#define QMV_RANKS(NT_OF, CALL)        \
+  switch (NT_OF) {                    \
+    case 1: { constexpr int NT = 1; CALL; break; } \
+    case 2: { constexpr int NT = 2; CALL; break; } \
+    case 3: case 4: { constexpr int NT = 4; CALL; break; } \
+    default: { constexpr int NT = 8; CALL; break; } \
+  }
+
+template <int DT, bool TRANS>
+static void shrink(const uint16_t *x, int64_t T, int64_t L, const uint16_t *factor, const Lora &l, const InnerPlan &p,
+                   const Places &pl, char *ws, hipStream_t st) {
+  const dim3 grid((unsigned)most_units(T, l.count), (unsigned)p.pieces);
+  QMV_RANKS((l.rank + 15) / 16,
+            hipLaunchKernelGGL((lora_shrink_kernel<DT, NT, TRANS>), grid, dim3(256), 0, st, x, L, p.piece, factor, l.scale,
+                               l.count, l.rank, pl, reinterpret_cast<float *>(ws + p.parts), T))
+}
+
+static Split split_of(const InnerPlan &p, char *ws) {
+  return Split{reinterpret_cast<float *>(ws + p.parts), p.pieces, reinterpret_cast<uint16_t *>(ws + p.hi),
+               reinterpret_cast<uint16_t *>(ws + p.lo)};
 }
 
 template <int DT>
-static hipError_t lora_t(const uint16_t *x, int64_t T, const Weight4 &w, const Lora &l, const int32_t *index,
-                         const uint16_t *bias, void *y, int y_dt, char *ws, hipStream_t st) {
-  const LoraPlan p = lora_plan(T, w.N, w.K, w.log2bs, l.rank, false);
-  float *base = reinterpret_cast<float *>(ws + p.base), *u = reinterpret_cast<float *>(ws + p.u);
-  const int pieces = pieces_of(T, w.K), piece = pieces > 1 ? kPiece : (int)w.K;
-  hipLaunchKernelGGL(lora_down_kernel<DT>, dim3((unsigned)T, (unsigned)pieces), dim3(256), 0, st, x, w.K, piece, l.down,
-                     l.scale, l.count, l.rank, index, u, T);
-  for (int64_t t = 0; t < T; t += kRows) {
-    const int64_t m = T - t < kRows ? T - t : kRows;
-    const hipError_t e = launch_gemm_4bit(x + t * w.K, DT, m, w.N, w.K, w.packed, w.sc, w.dq, w.log2bs, w.qt, base, kF32,
-                                          nullptr, st);
+static void split(const Split &one, const Split *two, int64_t T, const Lora &l, const Places &pl, hipStream_t st) {
+  const int Rp = (l.rank + 15) & ~15;
+  hipLaunchKernelGGL(lora_split_kernel<DT>, dim3((unsigned)((T * Rp + 255) / 256), two ? 2 : 1), dim3(256), 0, st, one,
+                     two ? *two : one, T, l.rank, Rp, l.count, pl.start);
+}
+
+static void order(const int32_t *index, int64_t T, const Lora &l, const Places &pl, hipStream_t st) {
+  hipLaunchKernelGGL(lora_order_kernel, dim3((unsigned)((T + 255) / 256)), dim3(256), 0, st, index, (int)T, l.count, pl);
+}
+
+// out = the product of m tokens with the weight, its transpose with TRANS, and the adapters' part
+template <int DT, int ODT, bool TRANS>
+static hipError_t product(const LoraPlan &p, const uint16_t *x, int64_t m, const Weight4 &w, const Lora &l,
+                          const Places &pl, const uint16_t *bias, typename Storage<ODT>::type *out, char *ws,
+                          hipStream_t st) {
+  const int64_t L = TRANS ? w.N : w.K, width = TRANS ? w.K : w.N;
+  const Split s = split_of(p.inner, ws);
+  const int Rp = (l.rank + 15) & ~15;
+  const LowRank lr{s.hi, s.lo, TRANS ? l.down : l.up, width, l.rank, Rp, l.count, pl.adapter, pl.start};
+  if (!p.product.tiled) {
+    float *base = reinterpret_cast<float *>(ws + p.product.base);
+    const hipError_t e =
+        TRANS ? launch_gemm_4bit_backward(x, DT, m, w.N, w.K, w.packed, w.sc, w.dq, w.log2bs, w.qt, base, kF32,
+                                          ws + p.product.back, st)
+              : launch_gemm_4bit(x, DT, m, w.N, w.K, w.packed, w.sc, w.dq, w.log2bs, w.qt, base, kF32, nullptr, st);
     if (e != hipSuccess) return e;
-    const dim3 grid((unsigned)((w.N + 255) / 256), (unsigned)m);
-    if (y_dt == kF32)
-      hipLaunchKernelGGL((lora_up_kernel<DT, kF32>), grid, dim3(256), 0, st, base, w.N, l.up, l.count, l.rank, index + t,
-                         u + t * l.rank, pieces, T, bias, static_cast<float *>(y) + t * w.N);
-    else
-      hipLaunchKernelGGL((lora_up_kernel<DT, DT>), grid, dim3(256), 0, st, base, w.N, l.up, l.count, l.rank, index + t,
-                         u + t * l.rank, pieces, T, bias, static_cast<uint16_t *>(y) + t * w.N);
+    const dim3 grid((unsigned)most_units(m, l.count), (unsigned)((width + 255) / 256));
+    hipLaunchKernelGGL((lora_expand_kernel<DT, ODT, TRANS>), grid, dim3(256), 0, st, base, lr, pl, bias, out);
+    return hipGetLastError();
+  }
+  uint16_t *W = reinterpret_cast<uint16_t *>(ws + p.product.decoded);
+  for (int64_t c = 0; c < width; c += p.product.piece) {
+    const int64_t n = width - c < p.product.piece ? width - c : p.product.piece;
+    const hipError_t e = TRANS ? launch_decode_piece(w, DT, c, n, nullptr, 0, W, L, st)
+                               : launch_decode_piece(rows_of(w, c, n), DT, 0, L, W, L, nullptr, 0, st);
+    if (e != hipSuccess) return e;
+    TileArgs a = tile_args(x, L, W, L, m, n, L);
+    a.rows = pl.order;
+    EpilogueLora<DT, ODT, TRANS> epi;
+    epi.lr = lr;
+    epi.lr.factor += TRANS ? c : c * l.rank;
+    epi.order = pl.order, epi.bias = bias ? bias + c : nullptr, epi.out = out + c, epi.ld = width;
+    hipLaunchKernelGGL((tile_kernel<DT, EpilogueLora<DT, ODT, TRANS>>), dim3(a.ncol * a.nrow), dim3(256), 0, st, a, epi);
   }
   return hipGetLastError();
 }
 
-template <int DT>
-static hipError_t lora_backward_t(const uint16_t *dy, const uint16_t *x, int64_t T, const Weight4 &w, const Lora &l,
-                                  const int32_t *index, uint16_t *dx, void *d_down, void *d_up, int grad_dt, char *ws,
-                                  hipStream_t st) {
-  const LoraPlan p = lora_plan(T, w.N, w.K, w.log2bs, l.rank, true);
-  float *base = reinterpret_cast<float *>(ws + p.base);
-  float *u = reinterpret_cast<float *>(ws + p.u), *v = reinterpret_cast<float *>(ws + p.v);
-  const int R = l.rank, pu = pieces_of(T, w.K), pv = pieces_of(T, w.N);
-  hipLaunchKernelGGL(lora_down_kernel<DT>, dim3((unsigned)T, (unsigned)pu), dim3(256), 0, st, x, w.K,
-                     pu > 1 ? kPiece : (int)w.K, l.down, l.scale, l.count, R, index, u, T);
-  hipLaunchKernelGGL(lora_down_t_kernel<DT>, dim3((unsigned)T, (unsigned)pv), dim3(256), 0, st, dy, w.N,
-                     pv > 1 ? kPiece : (int)w.N, l.up, l.scale, l.count, R, index, v, T);
-  for (int64_t t = 0; t < T; t += kRows) {
-    const int64_t m = T - t < kRows ? T - t : kRows;
-    const hipError_t e = launch_gemm_4bit_backward(dy + t * w.N, DT, m, w.N, w.K, w.packed, w.sc, w.dq, w.log2bs, w.qt,
-                                                   base, kF32, ws + p.back, st);
+template <int DT, int ODT>
+static hipError_t lora_t(const uint16_t *x, int64_t T, const Weight4 &w, const Lora &l, const int32_t *index,
+                         const uint16_t *bias, typename Storage<ODT>::type *y, char *ws, hipStream_t st) {
+  const LoraPlan p = lora_plan(T, w.N, w.K, w.log2bs, l.count, l.rank, false);
+  if (p.few) {
+    float *base = reinterpret_cast<float *>(ws + p.product.base), *u = reinterpret_cast<float *>(ws + p.u_few);
+    const int pieces = few_pieces(w.K);
+    hipLaunchKernelGGL(lora_down_kernel<DT>, dim3((unsigned)T, (unsigned)pieces), dim3(256), 0, st, x, w.K, l.down, l.scale,
+                       l.count, l.rank, index, u, T);
+    const hipError_t e =
+        T <= 8 ? launch_gemv_4bit(x, DT, (int)T, w.N, w.K, w.packed, w.sc, w.dq, w.log2bs, w.qt, base, kF32, nullptr, st)
+               : launch_gemm_4bit(x, DT, T, w.N, w.K, w.packed, w.sc, w.dq, w.log2bs, w.qt, base, kF32, nullptr, st);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((lora_up_t_kernel<DT, DT>), dim3((unsigned)((w.K + 2047) / 2048), (unsigned)m), dim3(256), 0, st,
-                       base, w.K, l.down, l.count, R, index + t, v + t * R, pv, T, dx + t * w.K);
+    hipLaunchKernelGGL((lora_up_kernel<DT, ODT>), dim3((unsigned)((w.N + 255) / 256), (unsigned)T), dim3(256), 0, st, base,
+                       w.N, l.up, l.count, l.rank, index, u, pieces, T, bias, y);
+    return hipGetLastError();
   }
-  float *us = reinterpret_cast<float *>(ws + p.parts), *vs = us + T * R;
-  const dim3 sum_grid((unsigned)((T * R + 255) / 256));
-  hipLaunchKernelGGL(lora_sum_kernel, sum_grid, dim3(256), 0, st, u, pu, T * R, us);
-  hipLaunchKernelGGL(lora_sum_kernel, sum_grid, dim3(256), 0, st, v, pv, T * R, vs);
-  const dim3 gd((unsigned)((w.K + 63) / 64), (unsigned)(R / 8), (unsigned)l.count);
-  const dim3 gu((unsigned)((w.N + 63) / 64), (unsigned)(R / 8), (unsigned)l.count);
-  if (grad_dt == kF32) {
-    hipLaunchKernelGGL((lora_grad_kernel<DT, kF32, false>), gd, dim3(64), 0, st, x, w.K, vs, R, index, T,
-                       static_cast<float *>(d_down));
-    hipLaunchKernelGGL((lora_grad_kernel<DT, kF32, true>), gu, dim3(64), 0, st, dy, w.N, us, R, index, T,
-                       static_cast<float *>(d_up));
-  } else {
-    hipLaunchKernelGGL((lora_grad_kernel<DT, DT, false>), gd, dim3(64), 0, st, x, w.K, vs, R, index, T,
-                       static_cast<uint16_t *>(d_down));
-    hipLaunchKernelGGL((lora_grad_kernel<DT, DT, true>), gu, dim3(64), 0, st, dy, w.N, us, R, index, T,
-                       static_cast<uint16_t *>(d_up));
+  const Places pl = places_at(p.places, ws);
+  for (int64_t t = 0; t < T; t += p.tokens) {
+    const int64_t m = T - t < p.tokens ? T - t : p.tokens;
+    order(index + t, m, l, pl, st);
+    shrink<DT, false>(x + t * w.K, m, w.K, l.down, l, p.inner, pl, ws, st);
+    split<DT>(split_of(p.inner, ws), nullptr, m, l, pl, st);
+    const hipError_t e = product<DT, ODT, false>(p, x + t * w.K, m, w, l, pl, bias, y + t * w.N, ws, st);
+    if (e != hipSuccess) return e;
   }
+  return hipGetLastError();
+}
+
+template <int DT, int ODT>
+static hipError_t lora_backward_t(const uint16_t *dy, const uint16_t *x, int64_t T, const Weight4 &w, const Lora &l,
+                                  const int32_t *index, uint16_t *dx, void *d_down, void *d_up, char *ws, hipStream_t st) {
+  using OT = typename Storage<ODT>::type;
+  const LoraPlan p = lora_plan(T, w.N, w.K, w.log2bs, l.count, l.rank, true);
+  const int R = l.rank, Rp = (R + 15) & ~15;
+  const bool once = p.tokens >= T;
+  if (!once) {  // the input's gradient in turns, with an order of its own each time
+    const Places pl = places_at(p.places, ws);
+    for (int64_t t = 0; t < T; t += p.tokens) {
+      const int64_t m = T - t < p.tokens ? T - t : p.tokens;
+      order(index + t, m, l, pl, st);
+      shrink<DT, true>(dy + t * w.N, m, w.N, l.up, l, p.inner, pl, ws, st);
+      split<DT>(split_of(p.inner, ws), nullptr, m, l, pl, st);
+      const hipError_t e = product<DT, DT, true>(p, dy + t * w.N, m, w, l, pl, nullptr, dx + t * w.K, ws, st);
+      if (e != hipSuccess) return e;
+    }
+  }
+  const Places pl = places_at(p.all, ws);
+  order(index, T, l, pl, st);
+  shrink<DT, true>(dy, T, w.N, l.up, l, p.v, pl, ws, st);
+  shrink<DT, false>(x, T, w.K, l.down, l, p.u, pl, ws, st);
+  const Split v = split_of(p.v, ws), u = split_of(p.u, ws);
+  split<DT>(v, &u, T, l, pl, st);
+  if (once) {
+    const hipError_t e = product<DT, DT, true>(p, dy, T, w, l, pl, nullptr, dx, ws, st);
+    if (e != hipSuccess) return e;
+  }
+  float *parts = reinterpret_cast<float *>(ws + p.parts);
+  auto grads = [&](const uint16_t *g, int64_t W, const Split &h, int window, auto up, void *out) {
+    constexpr bool UP = decltype(up)::value;
+    const dim3 grid((unsigned)((W + 127) / 128), (unsigned)((T + window - 1) / window));
+    QMV_RANKS((R + 31) / 32, hipLaunchKernelGGL((lora_grad_kernel<DT, ODT, (NT > 4 ? 4 : NT), UP>), grid, dim3(256), 0, st,
+                                                g, W, h.hi, h.lo, R, Rp, l.count, window, pl, parts, static_cast<OT *>(out)))
+    const int64_t n = W * R;
+    hipLaunchKernelGGL((lora_join_kernel<ODT>), dim3((unsigned)((n + 1023) / 1024), (unsigned)l.count), dim3(256), 0, st,
+                       parts, n, window, pl.start, static_cast<OT *>(out));
+  };
+  grads(x, w.K, v, p.window_down, std::false_type{}, d_down);
+  grads(dy, w.N, u, p.window_up, std::true_type{}, d_up);
   return hipGetLastError();
 }
 
 hipError_t launch_lora(const void *x, int dt, int64_t T, const Weight4 &w, const Lora &l, const int32_t *index,
                        const void *bias, void *y, int y_dt, char *ws, hipStream_t st) {
   const uint16_t *xp = static_cast<const uint16_t *>(x), *b = static_cast<const uint16_t *>(bias);
-  return dt == kF16 ? lora_t<kF16>(xp, T, w, l, index, b, y, y_dt, ws, st)
-                    : lora_t<kBF16>(xp, T, w, l, index, b, y, y_dt, ws, st);
+  if (y_dt == kF32) {
+    float *o = static_cast<float *>(y);
+    return dt == kF16 ? lora_t<kF16, kF32>(xp, T, w, l, index, b, o, ws, st) : lora_t<kBF16, kF32>(xp, T, w, l, index, b, o, ws, st);
+  }
+  uint16_t *o = static_cast<uint16_t *>(y);
+  return dt == kF16 ? lora_t<kF16, kF16>(xp, T, w, l, index, b, o, ws, st) : lora_t<kBF16, kBF16>(xp, T, w, l, index, b, o, ws, st);
 }
 
 hipError_t launch_lora_backward(const void *dy, const void *x, int dt, int64_t T, const Weight4 &w, const Lora &l,
@@ -283,8 +871,11 @@ hipError_t launch_lora_backward(const void *dy, const void *x, int dt, int64_t T
                                 hipStream_t st) {
   const uint16_t *g = static_cast<const uint16_t *>(dy), *xp = static_cast<const uint16_t *>(x);
   uint16_t *o = static_cast<uint16_t *>(dx);
-  return dt == kF16 ? lora_backward_t<kF16>(g, xp, T, w, l, index, o, d_down, d_up, grad_dt, ws, st)
-                    : lora_backward_t<kBF16>(g, xp, T, w, l, index, o, d_down, d_up, grad_dt, ws, st);
+  if (grad_dt == kF32)
+    return dt == kF16 ? lora_backward_t<kF16, kF32>(g, xp, T, w, l, index, o, d_down, d_up, ws, st)
+                      : lora_backward_t<kBF16, kF32>(g, xp, T, w, l, index, o, d_down, d_up, ws, st);
+  return dt == kF16 ? lora_backward_t<kF16, kF16>(g, xp, T, w, l, index, o, d_down, d_up, ws, st)
+                    : lora_backward_t<kBF16, kBF16>(g, xp, T, w, l, index, o, d_down, d_up, ws, st);
 }
 
 }  // namespace qmv

@@ -46,7 +46,7 @@ int check_weight(const qmv_weight_4bit *w, int64_t T, Weight4 *out) {
 
 int check_rank(int32_t count, int32_t rank) {
   if (count <= 0 || rank <= 0) return QMV_ERR_INVALID_ARG;
-  return count > 65535 || rank % 8 || rank > 128 ? QMV_ERR_UNSUPPORTED : QMV_OK;
+  return count > 4096 || rank % 8 || rank > 128 ? QMV_ERR_UNSUPPORTED : QMV_OK;
 }
 
 int check_lora(const qmv_lora *l, Lora *out) {
