@@ -107,7 +107,7 @@ int qmv_lora_4bit_backward(const void *dy, const void *x, qmv_dtype dtype, int64
  * Products are those of qmv_gemm_4bit and qmv_gemm_4bit_backward (weights
  * rounded to dtype, sums in fp32); maxima, sums and the target's part of the
  * gradient are fp32, exp(l - max) is rounded to dtype for the second product.
- *   w->rows at most 2^31 - 1, T below 2^31
+ *   w->rows below 2^31, w->cols below 2^22, T below 2^30 (here and above), else QMV_ERR_UNSUPPORTED
  */
 size_t qmv_cross_entropy_4bit_workspace(int64_t T, int64_t V, int64_t K, int32_t blocksize, int32_t grad);
 int qmv_cross_entropy_4bit(const void *x, qmv_dtype dtype, int64_t T, const qmv_weight_4bit *w,

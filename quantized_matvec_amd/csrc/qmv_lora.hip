@@ -144,7 +144,6 @@ struct Places {
 // launch without atomics on global memory gives a stable order; the first one
 // writes the adapters' places and the units as well.
 __global__ __launch_bounds__(256) void lora_order_kernel(const int32_t *__restrict__ index, int T, int count, Places pl) {
-  __shared__ __attribute__((aligned(16))) int mine[256];
   __shared__ int total[kMostAdapters + 1], before[kMostAdapters + 1], sums[4];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, t0 = blockIdx.x * 256;
   const int buckets = count + 1;
@@ -154,22 +153,27 @@ __global__ __launch_bounds__(256) void lora_order_kernel(const int32_t *__restri
   };
   for (int b = tid; b < buckets; b += 256) total[b] = before[b] = 0;
   const int my = t0 + tid < T ? bucket(t0 + tid) : -1;
-  mine[tid] = my;
   __syncthreads();
-  for (int base = 0; base < T; base += 256) {
-    const int t = base + tid;
-    if (t >= T) break;
-    const int b = bucket(t);
-    const int one = __builtin_amdgcn_readfirstlane(b);
-    const uint64_t here = __ballot(1);
-    if (__ballot(b == one) == here) {  // prompts: neighbours have one adapter
-      if (lane == __builtin_ctzll(here)) {
-        atomicAdd(&total[one], __builtin_popcountll(here));
-        if (base < t0) atomicAdd(&before[one], __builtin_popcountll(here));
+  for (int base = 0; base < T; base += 4096) {
+    int held[16];  // loads in flight
+#pragma unroll
+    for (int q = 0; q < 16; ++q) held[q] = index[min(base + 256 * q + tid, T - 1)];
+#pragma unroll
+    for (int q = 0; q < 16; ++q) {
+      const int chunk = base + 256 * q;
+      if (chunk + tid >= T) break;
+      const int b = held[q] >= 0 && held[q] < count ? held[q] : count;
+      const int one = __builtin_amdgcn_readfirstlane(b);
+      const uint64_t here = __ballot(1);
+      if (__ballot(b == one) == here) {  // prompts: neighbours have one adapter
+        if (lane == __builtin_ctzll(here)) {
+          atomicAdd(&total[one], __builtin_popcountll(here));
+          if (chunk < t0) atomicAdd(&before[one], __builtin_popcountll(here));
+        }
+      } else {
+        atomicAdd(&total[b], 1);
+        if (chunk < t0) atomicAdd(&before[b], 1);
       }
-    } else {
-      atomicAdd(&total[b], 1);
-      if (base < t0) atomicAdd(&before[b], 1);
     }
   }
   __syncthreads();
@@ -199,7 +203,10 @@ __global__ __launch_bounds__(256) void lora_order_kernel(const int32_t *__restri
     for (int b = b0; b < b1; ++b) {
       pl.start[b] = place;
       const int end = place + total[b];
-      for (; place < end; place += kUnit) pl.units[unit++] = make_int4(b, place, min(place + kUnit, end), 0);
+      const int n = (end - place + kUnit - 1) / kUnit;
+#pragma unroll 4
+      for (int i = 0; i < n; ++i) pl.units[unit + i] = make_int4(b, place + kUnit * i, min(place + kUnit * (i + 1), end), 0);
+      unit += n;
       place = end;
     }
     if (tid == 255) {
@@ -213,17 +220,24 @@ __global__ __launch_bounds__(256) void lora_order_kernel(const int32_t *__restri
     at += n;
   }
   __syncthreads();
-  if (my < 0) return;
-  int rank = 0;
-  const int4 *m4 = reinterpret_cast<const int4 *>(mine);
-  for (int i = 0; i < 64; ++i) {
-    if (4 * i >= tid) break;
-    const int4 m = m4[i];
-    rank += (m.x == my) + (4 * i + 1 < tid && m.y == my) + (4 * i + 2 < tid && m.z == my) + (4 * i + 3 < tid && m.w == my);
+  // this workgroup's tokens take the next places of their adapters, wave by wave
+  int place = 0;
+  for (int w = 0; w < 4; ++w) {
+    if (w == wave) {
+      for (uint64_t left = __ballot(my >= 0); left;) {
+        const int one = __builtin_amdgcn_readlane(my, __builtin_ctzll(left));
+        const uint64_t same = __ballot(my == one);
+        const int next = before[one];
+        if (my == one) place = total[one] + next + __builtin_popcountll(same & ((1ull << lane) - 1));
+        if (lane == 0) before[one] = next + __builtin_popcountll(same);
+        left &= ~same;
+      }
+    }
+    __syncthreads();
   }
-  const int p = total[my] + before[my] + rank;
-  pl.order[p] = t0 + tid;
-  pl.adapter[p] = my;
+  if (my < 0) return;
+  pl.order[place] = t0 + tid;
+  pl.adapter[place] = my;
 }
 
 // ---------------------------------------------------------------------------
@@ -340,6 +354,7 @@ __global__ __launch_bounds__(256) void lora_split_kernel(Split one, Split two, i
   const int r = (int)(i % Rp);
   float sum = 0.f;
   if (r < R && p < start[count])
+#pragma unroll 8
     for (int k = 0; k < s.pieces; ++k) sum += s.parts[(k * T + p) * R + r];
   const uint32_t hi = f32_to_bits16<DT>(sum);
   s.hi[i] = (uint16_t)hi;
@@ -402,8 +417,8 @@ __device__ __forceinline__ void add_low_rank(tile_acc_t (&acc)[MI][NJ], const Lo
   }
 }
 
-// out[t][c] = round(base[t][c] + bias[c] + the adapter's part): a unit and 256 columns
-// a workgroup, 64 columns a wave.  Bound by base and out.
+// out[t][c] = round(base[t][c] + bias[c] + the adapter's part): a unit and 128 columns
+// a workgroup, 32 columns a wave; base's loads go out first.  Bound by base and out.
 template <int DT, int ODT, bool TRANS>
 __global__ __launch_bounds__(256) void lora_expand_kernel(const float *__restrict__ base, LowRank lr, Places pl,
                                                           const uint16_t *__restrict__ bias,
@@ -411,32 +426,31 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(const float *__restric
   if ((int)blockIdx.x >= *pl.n_units) return;
   const int4 unit = pl.units[blockIdx.x];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, h = lane >> 5, l32 = lane & 31;
-  const int64_t c0 = (int64_t)blockIdx.y * 256 + 64 * wave;
+  const int64_t c0 = (int64_t)blockIdx.y * 128 + 32 * wave, c = c0 + l32, cin = min(c, lr.width - 1);
   if (c0 >= lr.width) return;
-  tile_acc_t acc[2][2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
-  if (unit.x < lr.count) add_low_rank<DT, TRANS, 2, 2>(acc, lr, unit.y, unit.z, c0, lr.width, lane);
+  float old[2][16];
+  int64_t token[2][16];
 #pragma unroll
   for (int i = 0; i < 2; ++i)
 #pragma unroll
     for (int r = 0; r < 16; ++r) {
-      const int p = unit.y + 32 * i + 8 * (r >> 2) + 4 * h + (r & 3);
-      if (p >= unit.z) continue;
-      const int64_t t = pl.order[p];
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int64_t c = c0 + 32 * j + l32;
-        if (c >= lr.width) continue;
-        float v = acc[i][j][r] + base[t * lr.width + c];
-        if (bias) v += bits16_to_f32<DT>(bias[c]);
-        store_elem<ODT>(out, t * lr.width + c, v);
-      }
+      token[i][r] = pl.order[min(unit.y + 32 * i + 8 * (r >> 2) + 4 * h + (r & 3), unit.z - 1)];
+      old[i][r] = base[token[i][r] * lr.width + cin];
     }
+  const float more = bias ? bits16_to_f32<DT>(bias[cin]) : 0.f;
+  tile_acc_t acc[2][1];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) acc[i][0][r] = 0.f;
+  if (unit.x < lr.count) add_low_rank<DT, TRANS, 2, 1>(acc, lr, unit.y, unit.z, c0, lr.width, lane);
+  if (c >= lr.width) return;
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int r = 0; r < 16; ++r)
+      if (unit.y + 32 * i + 8 * (r >> 2) + 4 * h + (r & 3) < unit.z)
+        store_elem<ODT>(out, token[i][r] * lr.width + c, acc[i][0][r] + old[i][r] + more);
 }
 
 // The tile product's sums, rows by place, with the adapters' part and the bias; row's token
@@ -448,11 +462,11 @@ struct EpilogueLora : EpilogueBase {
   const uint16_t *bias;
   OT *out;
   int64_t ld;
-  __device__ void begin(tile_acc_t (&acc)[4][4], const TileArgs &g, int M, int m0, int n0, int wm, int wn, int lane) const {
+  __device__ __forceinline__ void begin(tile_acc_t (&acc)[4][4], const TileArgs &g, int M, int m0, int n0, int wm, int wn, int lane) const {
     add_low_rank<DT, TRANS, 4, 4>(acc, lr, m0 + 128 * wm, min(m0 + 128 * wm + 128, M), n0 + 128 * wn, g.N, lane);
   }
-  __device__ OT *row(int m) const { return out + order[m] * ld; }
-  __device__ void store(OT *row, int n, float v) const {
+  __device__ __forceinline__ OT *row(int m) const { return out + order[m] * ld; }
+  __device__ __forceinline__ void store(OT *row, int n, float v) const {
     store_elem<ODT>(row, n, bias ? v + bits16_to_f32<DT>(bias[n]) : v);
   }
 };
@@ -462,7 +476,7 @@ struct EpilogueLora : EpilogueBase {
 // at [a][w][r] (UP: g = dy, h = u) or [a][r][w] (g = x, h = v).
 //
 // A workgroup takes a window of places and 128 columns w; for each run of one
-// adapter in the window it multiplies 32 places at a time, rows outside of the
+// adapter in the window it multiplies 64 places at a time, rows outside of the
 // run as zeros: both operands are wanted by columns, and come out of LDS so.
 // A wave has 32 columns and all ranks.  An adapter whose places lie in one
 // window is done then; a part of a run that goes on is left in fp32 (a window
@@ -476,12 +490,13 @@ __global__ __launch_bounds__(256) void lora_grad_kernel(const uint16_t *__restri
                                                         float *__restrict__ parts,
                                                         typename Storage<ODT>::type *__restrict__ out) {
   constexpr int kG = 128 + 16, kH = 32 * NT + 16;  // pitches: rows 8 (mod 64) banks apart
-  __shared__ __attribute__((aligned(16))) uint16_t gs[32 * kG], hs[2][32 * kH];
+  __shared__ __attribute__((aligned(16))) uint16_t gs[64 * kG], hs[2][64 * kH];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, l32 = lane & 31, h = lane >> 5;
   const int64_t w0 = (int64_t)blockIdx.x * 128;
   const int first = blockIdx.y * window, there = pl.start[count];
   const int last = min(first + window, there);
   const int grow = tid >> 4, gcol = 8 * (tid & 15);
+  const bool gin = w0 + gcol < W;
   // this lane's address for a column of 8 places: read_column
   const int i16 = lane & 15, part = (lane >> 4) & 1;
   const int place = 8 * h + (i16 >> 2), col = 16 * part + 4 * (i16 & 3);
@@ -494,40 +509,49 @@ __global__ __launch_bounds__(256) void lora_grad_kernel(const uint16_t *__restri
     for (int j = 0; j < NT; ++j)
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[j][r] = 0.f;
-    constexpr int NH = (NT + 1) / 2;  // 32 places x 32 NT ranks of a term, 16 bytes a thread
-    uint4 gv[2], hv[2][NH];
-    auto load = [&](int q) {
-      const uint4 none = make_uint4(0, 0, 0, 0);
+    // 64 places of 128 columns and of 32 NT ranks (two terms); their tokens a step before that.
+    // Loads without conditions, so that they are in flight together: what is not there is
+    // read at the run's last place, and zeroed on its way into LDS.
+    uint4 gv[4], hv[2][NT];
+    int token[4];
+    auto find = [&](int q) __attribute__((always_inline)) {
 #pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        const int at = q + grow + 16 * s;
-        gv[s] = at < end && w0 + gcol < W ? *reinterpret_cast<const uint4 *>(gp + (int64_t)pl.order[at] * W + w0 + gcol) : none;
-      }
+      for (int s = 0; s < 4; ++s) token[s] = pl.order[min(q + grow + 16 * s, end - 1)];
+    };
+    auto load = [&](int q) __attribute__((always_inline)) {
 #pragma unroll
-      for (int j = 0; j < NH; ++j) {
-        const int c = 256 * j + tid, at = q + c / (4 * NT), r = 8 * (c % (4 * NT));
-        const bool in = c < 128 * NT && at < end && r < Rp;
-        hv[0][j] = in ? *reinterpret_cast<const uint4 *>(hi + (int64_t)at * Rp + r) : none;
-        hv[1][j] = in ? *reinterpret_cast<const uint4 *>(lo + (int64_t)at * Rp + r) : none;
+      for (int s = 0; s < 4; ++s) gv[s] = *reinterpret_cast<const uint4 *>(gp + (int64_t)token[s] * W + (gin ? w0 + gcol : 0));
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        const int c = 256 * j + tid;
+        const int64_t from = (int64_t)min(q + c / (4 * NT), end - 1) * Rp + min(8 * (c % (4 * NT)), Rp - 8);
+        hv[0][j] = *reinterpret_cast<const uint4 *>(hi + from);
+        hv[1][j] = *reinterpret_cast<const uint4 *>(lo + from);
       }
     };
+    find(p);
     load(p);
-    for (int q = p; q < end; q += 32) {
+    find(p + 64);
+    for (int q = p; q < end; q += 64) {
+      const uint4 none = make_uint4(0, 0, 0, 0);
       __syncthreads();
 #pragma unroll
-      for (int s = 0; s < 2; ++s) *reinterpret_cast<uint4 *>(gs + (grow + 16 * s) * kG + gcol) = gv[s];
+      for (int s = 0; s < 4; ++s) {
+        const int row = grow + 16 * s;
+        *reinterpret_cast<uint4 *>(gs + row * kG + gcol) = q + row < end ? gv[s] : none;
+      }
 #pragma unroll
-      for (int j = 0; j < NH; ++j) {
-        const int c = 256 * j + tid;
-        if (c < 128 * NT) {
-          *reinterpret_cast<uint4 *>(hs[0] + (c / (4 * NT)) * kH + 8 * (c % (4 * NT))) = hv[0][j];
-          *reinterpret_cast<uint4 *>(hs[1] + (c / (4 * NT)) * kH + 8 * (c % (4 * NT))) = hv[1][j];
-        }
+      for (int j = 0; j < NT; ++j) {
+        const int c = 256 * j + tid, row = c / (4 * NT), at = row * kH + 8 * (c % (4 * NT));
+        const bool in = q + row < end;
+        *reinterpret_cast<uint4 *>(hs[0] + at) = in ? hv[0][j] : none;
+        *reinterpret_cast<uint4 *>(hs[1] + at) = in ? hv[1][j] : none;
       }
       __syncthreads();
-      if (q + 32 < end) load(q + 32);
+      load(q + 64);
+      find(q + 128);
 #pragma unroll
-      for (int s = 0; s < 2; ++s) {
+      for (int s = 0; s < 4; ++s) {
         const frag_t gf = read_column(gs + (16 * s + place) * kG + 32 * wave + col, kG);
 #pragma unroll
         for (int j = 0; j < NT; ++j)
@@ -564,14 +588,20 @@ __global__ __launch_bounds__(256) void lora_join_kernel(const float *__restrict_
   const int a = blockIdx.y, begin = start[a], past = start[a + 1];
   const int from = begin / window, to = (past - 1) / window;
   if (begin < past && from == to) return;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
-    float sum = 0.f;
-    if (begin < past) {
-      sum = parts[(int64_t)(2 * from + 1) * n + i];
-      for (int w = from + 1; w <= to; ++w) sum += parts[(int64_t)(2 * w) * n + i];
+  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;  // n is a multiple of 8
+  if (i >= n) return;
+  float sum[4] = {};
+  if (begin < past) {
+    const float4 v = *reinterpret_cast<const float4 *>(parts + (int64_t)(2 * from + 1) * n + i);
+    sum[0] = v.x, sum[1] = v.y, sum[2] = v.z, sum[3] = v.w;
+#pragma unroll 4
+    for (int w = from + 1; w <= to; ++w) {
+      const float4 u = *reinterpret_cast<const float4 *>(parts + (int64_t)(2 * w) * n + i);
+      sum[0] += u.x, sum[1] += u.y, sum[2] += u.z, sum[3] += u.w;
     }
-    store_elem<ODT>(out, a * n + i, sum);
   }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) store_elem<ODT>(out, a * n + i + e, sum[e]);
 }
 
 // ---------------------------------------------------------------------------
@@ -586,10 +616,12 @@ constexpr int64_t kDecoded = (int64_t)1 << 27;  // elements of a decoded piece, 
 static int few_pieces(int64_t width) { return (int)((width + kPiece - 1) / kPiece); }
 static int64_t most_units(int64_t T, int count) { return (T + kUnit - 1) / kUnit + (T < count + 1 ? T : count + 1); }
 
-// Pieces of the inner values' sums: a workgroup for each of 512 units and pieces, 256 terms at least
-static int inner_pieces(int64_t T, int64_t L, int count) {
-  int64_t s = 512 / most_units(T, count);
+// Pieces of the inner values' sums: a workgroup for each of about 1024 units and pieces, 256 terms
+// at least, and no more parts than about 32 MB of them
+static int inner_pieces(int64_t T, int64_t L, int count, int R) {
+  int64_t s = 1024 / most_units(T, count);
   if (s > L / 256) s = L / 256;
+  if (s > (32 << 20) / (T * R * 4)) s = (32 << 20) / (T * R * 4);
   return s < 1 ? 1 : (int)s;
 }
 static int inner_piece(int64_t L, int pieces) { return (int)(((L + pieces - 1) / pieces + 63) & ~(int64_t)63); }
@@ -600,7 +632,7 @@ struct InnerPlan {
 };
 static InnerPlan inner_plan(Carver &c, int64_t T, int64_t L, int R, int count) {
   InnerPlan p{};
-  p.piece = inner_piece(L, inner_pieces(T, L, count));
+  p.piece = inner_piece(L, inner_pieces(T, L, count, R));
   p.pieces = (int)((L + p.piece - 1) / p.piece);
   const int64_t Rp = (R + 15) & ~15;
   p.parts = c.take((size_t)p.pieces * T * R * 4);
@@ -657,11 +689,15 @@ static ProductPlan product_plan(Carver &c, int64_t T, int64_t N, int64_t K, int 
   return p;
 }
 
-// Windows of the gradients: about 768 workgroups, 64 places at least
-static int grad_window(int64_t T, int64_t W) {
-  const int64_t tiles = (W + 127) / 128;
-  int64_t w = (T * tiles / 768 + 31) & ~(int64_t)31;
-  if (w < 64) w = 64;
+// Windows of the gradients: about 2048 workgroups, 128 places at least, and no more parts than
+// about 32 MB of them
+static int grad_window(int64_t T, int64_t W, int R) {
+  const int64_t tiles = (W + 127) / 128, part = W * R * 4;
+  int64_t windows = 2048 / tiles;
+  if (windows > (32 << 20) / part) windows = (32 << 20) / part;
+  if (windows < 4) windows = 4;
+  int64_t w = ((T + windows - 1) / windows + 63) & ~(int64_t)63;
+  if (w < 128) w = 128;
   return (int)(w < T ? w : T);
 }
 
@@ -700,7 +736,7 @@ static LoraPlan lora_plan(int64_t T, int64_t N, int64_t K, int log2bs, int count
       p.v = p.inner;
     }
     p.u = inner_plan(c, T, K, R, count);
-    p.window_down = grad_window(T, K), p.window_up = grad_window(T, N);
+    p.window_down = grad_window(T, K, R), p.window_up = grad_window(T, N, R);
     const size_t a = 2 * (size_t)((T + p.window_down - 1) / p.window_down) * K * R * 4;
     const size_t b = 2 * (size_t)((T + p.window_up - 1) / p.window_up) * N * R * 4;
     p.parts = c.take(a > b ? a : b);
@@ -762,7 +798,7 @@ static hipError_t product(const LoraPlan &p, const uint16_t *x, int64_t m, const
                                           ws + p.product.back, st)
               : launch_gemm_4bit(x, DT, m, w.N, w.K, w.packed, w.sc, w.dq, w.log2bs, w.qt, base, kF32, nullptr, st);
     if (e != hipSuccess) return e;
-    const dim3 grid((unsigned)most_units(m, l.count), (unsigned)((width + 255) / 256));
+    const dim3 grid((unsigned)most_units(m, l.count), (unsigned)((width + 127) / 128));
     hipLaunchKernelGGL((lora_expand_kernel<DT, ODT, TRANS>), grid, dim3(256), 0, st, base, lr, pl, bias, out);
     return hipGetLastError();
   }
@@ -770,7 +806,7 @@ static hipError_t product(const LoraPlan &p, const uint16_t *x, int64_t m, const
   for (int64_t c = 0; c < width; c += p.product.piece) {
     const int64_t n = width - c < p.product.piece ? width - c : p.product.piece;
     const hipError_t e = TRANS ? launch_decode_piece(w, DT, c, n, nullptr, 0, W, L, st)
-                               : launch_decode_piece(rows_of(w, c, n), DT, 0, L, W, L, nullptr, 0, st);
+                               : launch_decode_rows(rows_of(w, c, n), DT, W, st);
     if (e != hipSuccess) return e;
     TileArgs a = tile_args(x, L, W, L, m, n, L);
     a.rows = pl.order;

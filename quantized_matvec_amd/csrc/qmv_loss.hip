@@ -474,7 +474,8 @@ static hipError_t pieces_tiled(const LossPlan &p, const uint16_t *x, int64_t m, 
   hipLaunchKernelGGL(loss_order_kernel, dim3(1), dim3(1024), 0, st, live, (int)m, list, count);
   for (int64_t v = 0; v < w.N; v += p.piece) {
     const int n = (int)(w.N - v < p.piece ? w.N - v : p.piece), np = (n + 63) & ~63;
-    const hipError_t e = launch_decode_piece(rows_of(w, v, n), DT, 0, w.K, W, w.K, Wt, np, st);
+    const hipError_t e = grad ? launch_decode_piece(rows_of(w, v, n), DT, 0, w.K, W, w.K, Wt, np, st)
+                              : launch_decode_rows(rows_of(w, v, n), DT, W, st);
     if (e != hipSuccess) return e;
     TileArgs a = tile_args(x, w.K, W, w.K, m, n, w.K);
     a.rows = list, a.count = count;

@@ -36,6 +36,11 @@ inline Weight4 rows_of(const Weight4 &w, int64_t first, int64_t n) {
 hipError_t launch_decode_piece(const Weight4 &w, int dt, int64_t c0, int64_t cols, void *W, int64_t ldw, void *Wt,
                                int64_t ldt, hipStream_t st);
 
+// All of W alone: dequantize_4bit's kernel.
+inline hipError_t launch_decode_rows(const Weight4 &w, int dt, void *W, hipStream_t st) {
+  return launch_dequantize_4bit(w.packed, w.sc, w.dq, w.N * w.K, w.log2bs, w.qt, W, dt, st);
+}
+
 struct Lora {
   const uint16_t *down, *up;
   const float *scale;

@@ -20,8 +20,8 @@ int launch_status(hipError_t e) { return e == hipSuccess ? QMV_OK : QMV_ERR_LAUN
 int check_sizes(int64_t T, int64_t N, int64_t K, int32_t blocksize) {
   if (T <= 0 || N <= 0 || K <= 0) return QMV_ERR_INVALID_ARG;
   if (!valid_blocksize(blocksize) || K % 32 || K % blocksize) return QMV_ERR_UNSUPPORTED;
-  // the products' kernels hold a row tile's and a weight tile's offsets in 32 bits
-  if (T >= kMost || N >= kMost || K >= (1 << 22)) return QMV_ERR_UNSUPPORTED;
+  // tokens are counted, and a row tile's and a weight tile's offsets held, in 32 bits
+  if (T >= kMost / 2 || N >= kMost || K >= (1 << 22)) return QMV_ERR_UNSUPPORTED;
   return QMV_OK;
 }
 
