@@ -15,7 +15,12 @@
 namespace qmv {
 
 typedef __attribute__((__vector_size__(4 * sizeof(float)))) float acc4_t;
+typedef __attribute__((ext_vector_type(4))) uint32_t u32x4_t;
 
+// The smaller kernels ask for two waves a SIMD: with one the compiler may use 512
+// registers, puts sums into the accumulation half, and moves loads in flight there
+// as well, each with a wait of its own (a gradient's step then takes six round trips
+// to memory, 123 us for 4096 tokens x 14336).
 template <int DT>
 __device__ __forceinline__ acc4_t mma16(const frag_t &a, const frag_t &b, const acc4_t &c) {
   if constexpr (DT == kBF16)
@@ -252,7 +257,7 @@ __global__ __launch_bounds__(256) void lora_order_kernel(const int32_t *__restri
 // order.  Bound by the read of the rows.
 // ---------------------------------------------------------------------------
 template <int DT, int NT, bool TRANS>
-__global__ __launch_bounds__(256) void lora_shrink_kernel(const uint16_t *__restrict__ x, int64_t L, int piece,
+__global__ __launch_bounds__(256, 2) void lora_shrink_kernel(const uint16_t *__restrict__ x, int64_t L, int piece,
                                                           const uint16_t *__restrict__ factor,
                                                           const float *__restrict__ scale, int count, int R, Places pl,
                                                           float *__restrict__ parts, int64_t T) {
@@ -420,7 +425,7 @@ __device__ __forceinline__ void add_low_rank(tile_acc_t (&acc)[MI][NJ], const Lo
 // out[t][c] = round(base[t][c] + bias[c] + the adapter's part): a unit and 128 columns
 // a workgroup, 32 columns a wave; base's loads go out first.  Bound by base and out.
 template <int DT, int ODT, bool TRANS>
-__global__ __launch_bounds__(256) void lora_expand_kernel(const float *__restrict__ base, LowRank lr, Places pl,
+__global__ __launch_bounds__(256, 2) void lora_expand_kernel(const float *__restrict__ base, LowRank lr, Places pl,
                                                           const uint16_t *__restrict__ bias,
                                                           typename Storage<ODT>::type *__restrict__ out) {
   if ((int)blockIdx.x >= *pl.n_units) return;
@@ -484,7 +489,7 @@ struct EpilogueLora : EpilogueBase {
 // lora_join_kernel adds an adapter's parts in order.  Bound by the read of g.
 // ---------------------------------------------------------------------------
 template <int DT, int ODT, int NT, bool UP>
-__global__ __launch_bounds__(256) void lora_grad_kernel(const uint16_t *__restrict__ gp, int64_t W,
+__global__ __launch_bounds__(256, 2) void lora_grad_kernel(const uint16_t *__restrict__ gp, int64_t W,
                                                         const uint16_t *__restrict__ hi, const uint16_t *__restrict__ lo,
                                                         int R, int Rp, int count, int window, Places pl,
                                                         float *__restrict__ parts,
@@ -511,8 +516,9 @@ __global__ __launch_bounds__(256) void lora_grad_kernel(const uint16_t *__restri
       for (int r = 0; r < 16; ++r) acc[j][r] = 0.f;
     // 64 places of 128 columns and of 32 NT ranks (two terms); their tokens a step before that.
     // Loads without conditions, so that they are in flight together: what is not there is
-    // read at the run's last place, and zeroed on its way into LDS.
-    uint4 gv[4], hv[2][NT];
+    // read at the run's last place, and zeroed on its way into LDS.  (As vectors: taken apart into
+    // words they would be copied, each with a wait, before the loop's end.)
+    u32x4_t gv[4], hv[2][NT];
     int token[4];
     auto find = [&](int q) __attribute__((always_inline)) {
 #pragma unroll
@@ -520,32 +526,31 @@ __global__ __launch_bounds__(256) void lora_grad_kernel(const uint16_t *__restri
     };
     auto load = [&](int q) __attribute__((always_inline)) {
 #pragma unroll
-      for (int s = 0; s < 4; ++s) gv[s] = *reinterpret_cast<const uint4 *>(gp + (int64_t)token[s] * W + (gin ? w0 + gcol : 0));
+      for (int s = 0; s < 4; ++s) gv[s] = *reinterpret_cast<const u32x4_t *>(gp + (int64_t)token[s] * W + (gin ? w0 + gcol : 0));
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
         const int c = 256 * j + tid;
         const int64_t from = (int64_t)min(q + c / (4 * NT), end - 1) * Rp + min(8 * (c % (4 * NT)), Rp - 8);
-        hv[0][j] = *reinterpret_cast<const uint4 *>(hi + from);
-        hv[1][j] = *reinterpret_cast<const uint4 *>(lo + from);
+        hv[0][j] = *reinterpret_cast<const u32x4_t *>(hi + from);
+        hv[1][j] = *reinterpret_cast<const u32x4_t *>(lo + from);
       }
     };
     find(p);
     load(p);
     find(p + 64);
     for (int q = p; q < end; q += 64) {
-      const uint4 none = make_uint4(0, 0, 0, 0);
       __syncthreads();
 #pragma unroll
       for (int s = 0; s < 4; ++s) {
         const int row = grow + 16 * s;
-        *reinterpret_cast<uint4 *>(gs + row * kG + gcol) = q + row < end ? gv[s] : none;
+        *reinterpret_cast<u32x4_t *>(gs + row * kG + gcol) = gv[s] & (q + row < end ? ~0u : 0u);
       }
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
         const int c = 256 * j + tid, row = c / (4 * NT), at = row * kH + 8 * (c % (4 * NT));
-        const bool in = q + row < end;
-        *reinterpret_cast<uint4 *>(hs[0] + at) = in ? hv[0][j] : none;
-        *reinterpret_cast<uint4 *>(hs[1] + at) = in ? hv[1][j] : none;
+        const uint32_t in = q + row < end ? ~0u : 0u;
+        *reinterpret_cast<u32x4_t *>(hs[0] + at) = hv[0][j] & in;
+        *reinterpret_cast<u32x4_t *>(hs[1] + at) = hv[1][j] & in;
       }
       __syncthreads();
       load(q + 64);
