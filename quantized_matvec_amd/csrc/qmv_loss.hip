@@ -17,11 +17,12 @@
 
 namespace qmv {
 
-constexpr int kPieceV = 8192;    // columns of a piece: a multiple of 4096 (rows_of)
+constexpr int kSegment = 8192;   // columns of a logits row that a workgroup takes
 constexpr int64_t kTokens = 4096;  // most tokens taken at a time
 constexpr int kTail = 32;
 constexpr int kMostPiece = 32768;   // of the tile product's pieces
-constexpr int64_t kTiledFrom = 448;  // tokens from which it is used
+constexpr int64_t kTiledFrom = 65;   // tokens from which it is used
+constexpr int64_t kLogits = (int64_t)1 << 26;  // logits of a piece where it is not
 
 // What exp(l - m) is multiplied by before its rounding.  fp16 has no normal
 // numbers below 2^-14: with 2^14 (sums are fp32, and D is divided by it at the
@@ -98,61 +99,110 @@ __device__ __forceinline__ float block_reduce(float v, float *buf, F op) {  // 2
   return v;
 }
 
-// One piece's columns [v0, v0 + n) of one token: m, s, f, the target ids'
-// logits and, with a gradient, P = exp(l - m) in 16 bits, [T, np] with np the
-// multiple of 32 below n (the columns from np on go to `tail`).
-template <int DT, bool GRAD>
-__global__ __launch_bounds__(256) void loss_piece_kernel(const float *__restrict__ logits, int64_t ld, int64_t v0, int n,
-                                                         int np, const int64_t *__restrict__ ids, int k, float inv_tau,
-                                                         bool first, RowState rs, uint16_t *__restrict__ P) {
-  __shared__ uint32_t out[kPieceV / 32];  // columns of target ids
-  __shared__ float buf[4];
-  const int64_t t = blockIdx.x;
-  const float *row = logits + t * ld;
-  for (int i = threadIdx.x; i < kPieceV / 32; i += 256) out[i] = 0;
-  __syncthreads();
+// ---------------------------------------------------------------------------
+// Few tokens: a token's logits are shared out among workgroups of 8192 columns.
+// loss_part_kernel leaves each segment's maximum and sum (and takes the target ids'
+// logits); loss_merge_kernel puts them together with what was before the piece
+// and, with a gradient, writes P = exp(l - m) in 16 bits, [T, np] with np the
+// multiple of 32 below n (the columns from np on go to `tail`).  Two launches,
+// but no workgroup reads more than 32 kB.
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ void mark_ids(uint32_t *out, const int64_t *ids, int k, int64_t v0, int n, const float *row,
+                                         float inv_tau, float *lt) {  // one barrier
   for (int j = threadIdx.x; j < k; j += 256) {
-    const int64_t c = ids[t * k + j] - v0;
+    const int64_t c = ids[j] - v0;
     if (c >= 0 && c < n) {
       atomicOr(&out[c >> 5], 1u << (c & 31));
-      rs.lt[t * k + j] = row[c] * inv_tau;
+      if (lt) lt[j] = row[c] * inv_tau;
     }
   }
   __syncthreads();
-  auto held = [&](int c) { return (out[c >> 5] >> (c & 31) & 1) == 0; };
-  float m = -INFINITY;
-  for (int c = threadIdx.x; c < n; c += 256)
-    if (held(c)) m = fmaxf(m, row[c] * inv_tau);
-  m = block_reduce(wave_max(m), buf, [](float a, float b) { return fmaxf(a, b); });
-  const float m_old = first ? -INFINITY : rs.m[t];
-  m = fmaxf(m, m_old);
-  float s = 0.f;
-  for (int c = threadIdx.x; c < n; c += 256) {
-    const float l = row[c] * inv_tau;
-    const float e = held(c) ? expf(l - m) : 0.f;
-    s += e;
-    if constexpr (GRAD) {
-      if (c < np) P[t * np + c] = (uint16_t)f32_to_bits16<DT>(e * kGain<DT>);
-      else rs.tail[t * kTail + c - np] = held(c) ? l : -INFINITY;
-    }
+}
+
+__global__ __launch_bounds__(256) void loss_part_kernel(const float *__restrict__ logits, int64_t v0, int n,
+                                                        const int64_t *__restrict__ ids, int k, float inv_tau,
+                                                        float *__restrict__ lt, float2 *__restrict__ segments) {
+  __shared__ uint32_t out[kSegment / 32];  // columns of target ids
+  __shared__ float buf[4];
+  const int64_t t = blockIdx.y;
+  const int c0 = blockIdx.x * kSegment, cols = min(n - c0, kSegment);
+  const float *row = logits + t * n + c0;
+  out[threadIdx.x] = 0;
+  float l[32];
+#pragma unroll
+  for (int q = 0; q < 32; ++q) {
+    const int c = 256 * q + threadIdx.x;
+    l[q] = row[min(c, cols - 1)] * inv_tau;
   }
+  __syncthreads();
+  mark_ids(out, ids + t * k, k, v0 + c0, cols, row, inv_tau, lt + t * k);
+  float m = -INFINITY;
+#pragma unroll
+  for (int q = 0; q < 32; ++q) {
+    const int c = 256 * q + threadIdx.x;
+    if (c >= cols || (out[c >> 5] >> (c & 31) & 1)) l[q] = -INFINITY;
+    m = fmaxf(m, l[q]);
+  }
+  m = block_reduce(wave_max(m), buf, [](float a, float b) { return fmaxf(a, b); });
+  const float ref = m == -INFINITY ? 0.f : m;
+  float s = 0.f;
+#pragma unroll
+  for (int q = 0; q < 32; ++q) s += __expf(l[q] - ref);
   s = block_reduce(wave_sum(s), buf, [](float a, float b) { return a + b; });
-  if (threadIdx.x == 0) {
-    const float f = m_old == -INFINITY ? 0.f : expf(m_old - m);
-    rs.s[t] = (first ? 0.f : rs.s[t] * f) + s;
+  if (threadIdx.x == 0) segments[t * gridDim.x + blockIdx.x] = make_float2(m, s);
+}
+
+// before, after: (maximum, sum) of each token before and after this piece
+template <int DT, bool GRAD>
+__global__ __launch_bounds__(256) void loss_merge_kernel(const float *__restrict__ logits, int64_t v0, int n, int np,
+                                                         const int64_t *__restrict__ ids, int k, float inv_tau, bool first,
+                                                         const float2 *__restrict__ segments, int n_segments,
+                                                         const float2 *__restrict__ before, float2 *__restrict__ after,
+                                                         RowState rs, uint16_t *__restrict__ P) {
+  __shared__ uint32_t out[kSegment / 32];
+  const int64_t t = blockIdx.y;
+  const int c0 = blockIdx.x * kSegment, cols = min(n - c0, kSegment);
+  const float *row = logits + t * n + c0;
+  const float2 old = first ? make_float2(-INFINITY, 0.f) : before[t];
+  float m = old.x;
+  for (int i = 0; i < n_segments; ++i) m = fmaxf(m, segments[t * n_segments + i].x);
+  const float ref = m == -INFINITY ? 0.f : m;
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    const float f = __expf(old.x - ref);  // 0 at first
+    float s = old.y * f;
+    for (int i = 0; i < n_segments; ++i) {
+      const float2 seg = segments[t * n_segments + i];
+      s += seg.y * __expf(seg.x - ref);
+    }
+    after[t] = make_float2(m, s);
     rs.m[t] = m;
+    rs.s[t] = s;
     rs.f[t] = f;
+  }
+  if constexpr (GRAD) {
+    out[threadIdx.x] = 0;
+    __syncthreads();
+    mark_ids(out, ids + t * k, k, v0 + c0, cols, row, inv_tau, nullptr);
+#pragma unroll 8
+    for (int q = 0; q < 32; ++q) {
+      const int c = 256 * q + threadIdx.x;
+      if (c >= cols) break;
+      const bool gone = out[c >> 5] >> (c & 31) & 1;
+      const float l = gone ? -INFINITY : row[c] * inv_tau;
+      if (c0 + c < np) P[t * np + c0 + c] = (uint16_t)f32_to_bits16<DT>(__expf(l - ref) * kGain<DT>);
+      else rs.tail[t * kTail + c0 + c - np] = l;
+    }
   }
 }
 
-// D = D f + what a piece adds (f of the row; the first piece stores)
+// D = D f + what a piece adds (nothing: NULL), f of the row; `first`: D = 0
 __global__ __launch_bounds__(256) void loss_add_kernel(float *__restrict__ D, const float *__restrict__ add,
                                                        const float *__restrict__ f, int64_t K, bool first) {
   const int64_t t = blockIdx.x;
   const float ft = f[t];
   for (int64_t c = threadIdx.x; c < K; c += 256) {
     const int64_t i = t * K + c;
-    D[i] = (first ? 0.f : D[i] * ft) + (add ? add[i] : 0.f);
+    D[i] = first ? 0.f : fmaf(D[i], ft, add ? add[i] : 0.f);
   }
 }
 
@@ -403,7 +453,7 @@ struct LossPlan {
   bool tiled;
   int64_t tokens;  // taken at a time
   int piece, parts, split;
-  size_t logits, m, s, f, lt, tail, P, D, add, back, live, list, count, W, Wt, total;
+  size_t logits, m, s, f, lt, tail, P, D, add, back, segments, carry, live, list, count, W, Wt, total;
 };
 
 static LossPlan loss_plan(int64_t T, int64_t V, int64_t K, int log2bs, int k, bool grad) {
@@ -434,13 +484,17 @@ static LossPlan loss_plan(int64_t T, int64_t V, int64_t K, int log2bs, int k, bo
     }
   } else {
     p.parts = 1;
-    p.piece = (int)(V < kPieceV ? V : kPieceV);
+    int64_t piece = (kLogits / p.tokens) & ~(int64_t)4095;  // rows_of wants 4096 rows
+    if (piece < 4096) piece = 4096;
+    p.piece = (int)(V < piece ? V : piece);
     p.logits = c.take(n * p.piece * 4);
+    p.segments = c.take(n * ((p.piece + kSegment - 1) / kSegment) * 8);
+    p.carry = c.take(n * 16);
     if (grad) {
       p.tail = c.take(n * kTail * 4);
       p.P = c.take(n * p.piece * 2);
       p.D = c.take(n * K * 4);
-      p.add = c.take(n * K * 4);
+      if (p.piece < V) p.add = c.take(n * K * 4);
       size_t most = 0;  // the product's own workspace, over all sizes that come up
       for (int64_t m : {p.tokens, T % p.tokens})
         for (int64_t v : {(int64_t)p.piece & ~31ll, (V % p.piece) & ~31ll})
@@ -506,23 +560,30 @@ static hipError_t pieces_plain(const LossPlan &p, const uint16_t *x, int64_t m, 
                                hipStream_t st) {
   float *logits = reinterpret_cast<float *>(ws + p.logits), *add = reinterpret_cast<float *>(ws + p.add);
   uint16_t *P = reinterpret_cast<uint16_t *>(ws + p.P);
-  for (int64_t v = 0; v < w.N; v += p.piece) {
-    const int n = (int)(w.N - v < p.piece ? w.N - v : p.piece), np = n & ~31;
+  float2 *segments = reinterpret_cast<float2 *>(ws + p.segments), *carry = reinterpret_cast<float2 *>(ws + p.carry);
+  int turn = 0;
+  for (int64_t v = 0; v < w.N; v += p.piece, turn ^= 1) {
+    const int n = (int)(w.N - v < p.piece ? w.N - v : p.piece), np = n & ~31, n_segments = (n + kSegment - 1) / kSegment;
     const Weight4 c = rows_of(w, v, n);
     hipError_t e = launch_gemm_4bit(x, DT, m, n, w.K, c.packed, c.sc, c.dq, c.log2bs, c.qt, logits, kF32, nullptr, st);
     if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(loss_part_kernel, dim3(n_segments, (unsigned)m), dim3(256), 0, st, logits, v, n, ids, tg.k, tg.inv_tau,
+                       rs.lt, segments);
+    float2 *before = carry + (turn ? p.tokens : 0), *after = carry + (turn ? 0 : p.tokens);
     if (!grad) {
-      hipLaunchKernelGGL((loss_piece_kernel<DT, false>), dim3((unsigned)m), dim3(256), 0, st, logits, (int64_t)n, v, n, n,
-                         ids, tg.k, tg.inv_tau, v == 0, rs, P);
+      hipLaunchKernelGGL((loss_merge_kernel<DT, false>), dim3(1, (unsigned)m), dim3(64), 0, st, logits, v, n, np, ids, tg.k,
+                         tg.inv_tau, v == 0, segments, n_segments, before, after, rs, P);
       continue;
     }
-    hipLaunchKernelGGL((loss_piece_kernel<DT, true>), dim3((unsigned)m), dim3(256), 0, st, logits, (int64_t)n, v, n, np,
-                       ids, tg.k, tg.inv_tau, v == 0, rs, P);
+    hipLaunchKernelGGL((loss_merge_kernel<DT, true>), dim3(n_segments, (unsigned)m), dim3(256), 0, st, logits, v, n, np, ids,
+                       tg.k, tg.inv_tau, v == 0, segments, n_segments, before, after, rs, P);
     if (np) {
-      e = launch_gemm_4bit_backward(P, DT, m, np, w.K, c.packed, c.sc, c.dq, c.log2bs, c.qt, add, kF32, ws + p.back, st);
+      e = launch_gemm_4bit_backward(P, DT, m, np, w.K, c.packed, c.sc, c.dq, c.log2bs, c.qt, v == 0 ? D : add, kF32,
+                                    ws + p.back, st);
       if (e != hipSuccess) return e;
     }
-    hipLaunchKernelGGL(loss_add_kernel, dim3((unsigned)m), dim3(256), 0, st, D, np ? add : nullptr, rs.f, w.K, v == 0);
+    if (v > 0 || !np)
+      hipLaunchKernelGGL(loss_add_kernel, dim3((unsigned)m), dim3(256), 0, st, D, np ? add : nullptr, rs.f, w.K, v == 0);
     *tail_n = n - np;
   }
   return hipGetLastError();
