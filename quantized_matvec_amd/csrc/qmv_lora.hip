@@ -613,7 +613,7 @@ __global__ __launch_bounds__(256) void lora_join_kernel(const float *__restrict_
 // host
 // ---------------------------------------------------------------------------
 constexpr int64_t kFew = 32;        // tokens up to which a token is a workgroup's
-constexpr int64_t kTiledFrom = 768;  // tokens from which the weight is decoded for the tile product
+constexpr int64_t kTiledFrom = 640, kTiledTiles = 144;  // tokens and tiles from which the tile product is used
 constexpr int64_t kRows = 4096;     // tokens of a fp32 projection in the workspace
 constexpr int64_t kTiledRows = 16384;
 constexpr int64_t kDecoded = (int64_t)1 << 27;  // elements of a decoded piece, about
@@ -671,7 +671,12 @@ struct ProductPlan {
 static ProductPlan product_plan(Carver &c, int64_t T, int64_t N, int64_t K, int log2bs, bool backward) {
   ProductPlan p{};
   const int64_t L = backward ? N : K, width = backward ? K : N;
-  p.tiled = T >= kTiledFrom && L % 64 == 0 && L <= 65536 && width <= ((int64_t)1 << 30);
+  // The tile product wants the decoding spread over many tokens, and tiles for half the compute units
+  // or more.  Both sides, us of a call with it / with gemm_4bit's kernels (rank 16): 14336 x 4096 outputs x
+  // sums, 448 tokens 155 / 108, 768 tokens (168 tiles) 151 / 187, 4096 tokens 495 / 727; 4096 x 4096, 2048 tokens
+  // (128 tiles) 126 / 122, 4096 tokens 154 / 226; 4096 x 14336, 2048 tokens 357 / 303, 4096 tokens 429 / 588
+  const int64_t tiles = ((T + kTileM - 1) / kTileM) * ((width + kTileN - 1) / kTileN);
+  p.tiled = T >= kTiledFrom && tiles >= kTiledTiles && L % 64 == 0 && L <= 65536 && width <= ((int64_t)1 << 30);
   const int64_t most = p.tiled ? kTiledRows : kRows, turns = (T + most - 1) / most;
   p.tokens = (T + turns - 1) / turns;
   if (p.tiled) {

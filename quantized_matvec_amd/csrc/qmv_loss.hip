@@ -21,7 +21,7 @@ constexpr int kSegment = 8192;   // columns of a logits row that a workgroup tak
 constexpr int64_t kTokens = 4096;  // most tokens taken at a time
 constexpr int kTail = 32;
 constexpr int kMostPiece = 32768;   // of the tile product's pieces
-constexpr int64_t kTiledFrom = 65;   // tokens from which it is used
+constexpr int64_t kTiledFrom = 448;  // tokens from which it is used
 constexpr int64_t kLogits = (int64_t)1 << 26;  // logits of a piece where it is not
 
 // What exp(l - m) is multiplied by before its rounding.  fp16 has no normal
@@ -459,6 +459,8 @@ struct LossPlan {
 static LossPlan loss_plan(int64_t T, int64_t V, int64_t K, int log2bs, int k, bool grad) {
   LossPlan p{};
   Carver c;
+  // both sides, us with the gradient by the tile product / by gemm_4bit's kernels: 256 tokens x 128256 x 4096
+  // 1488 / 848, 448 tokens 1663 / 1584, 512 tokens 1680 / 1665, and the latter grows with every token
   p.tiled = T >= kTiledFrom && K % 64 == 0 && K <= 65536;
   const int64_t turns = (T + kTokens - 1) / kTokens;
   p.tokens = (T + turns - 1) / turns;

@@ -81,6 +81,36 @@ def test_odd_widths_forward(N, K, T):
     check_forward(c, forward(c))
 
 
+# enough tokens and columns for the tile product (640 tokens, 144 tiles of 256 x 256), whole tiles and
+# parts of them, of the outputs (forward: N, backward: K) or sums; turns of 16384 and of 4096 tokens
+@pytest.mark.parametrize("T,N,K,rank", [(640, 12320, 64, 16), (700, 12544, 192, 8), (1100, 7456, 128, 40), (768, 12288, 64, 128),
+                                        (16400, 768, 64, 16), (4100, 96, 96, 8), (5000, 320, 32, 24)])
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_tiles(T, N, K, rank, dtype):
+    g = torch.Generator().manual_seed(T)
+    cuts = torch.sort(torch.randint(T, (6,), generator=g))[0].tolist() + [T]
+    index, at = [], 0
+    for a, c in zip([2, -1, 0, 2, 4, 1, 0], cuts):  # runs, an adapter that comes back, one (3) without tokens
+        index += [a] * (c - at)
+        at = c
+    c = case(T, N, K, 5, rank, dtype, index, bs=32 if K % 64 else 64, dq=True)
+    bias = torch.randn(N, generator=g).to(dtype).cuda()
+    check_forward(c, forward(c, bias=bias), bias)
+    check_forward(c, forward(c, out_dtype=torch.float32))
+    c = case(T, K, N, 5, rank, dtype, index, bs=32, dq=True)  # backward: its outputs are K wide
+    check_backward(c, backward(c))
+
+
+@pytest.mark.parametrize("T", [700, 1000])
+def test_tiles_of_many_adapters(T):
+    """Every row of a tile with another adapter, in no order."""
+    g = torch.Generator().manual_seed(3)
+    c = case(T, 12320, 64, 90, 16, BF, torch.randint(-1, 90, (T,), generator=g))
+    check_forward(c, forward(c))
+    c = case(T, 64, 12320, 90, 16, BF, torch.randint(-1, 90, (T,), generator=g), bs=32)
+    check_backward(c, backward(c))
+
+
 def sorted_parts(T, parts):
     out = []
     for a, n in parts:
@@ -192,21 +222,21 @@ def test_no_tokens():
 
 
 def test_a_row_that_is_not_finite_stays_alone():
-    for T in (40, 600):
-        c = case(T, 128, 256, 3, 16, BF)
+    for T, N, K in ((5, 128, 256), (40, 128, 256), (600, 128, 256), (700, 12320, 64)):
+        c = case(T, N, K, 3, 16, BF)
         ref = forward(c)
         x = c["x"].clone()
-        x[7, 3], x[11, 200] = float("nan"), float("inf")
+        x[1, 3], x[T - 2, 50] = float("nan"), float("inf")
         y = qmv.lora_4bit(x, c["packed"], c["state"], c["adapters"], c["index"])
-        rest = [t for t in range(T) if t not in (7, 11)]
-        assert torch.equal(y[rest], ref[rest]) and not torch.isfinite(y[7]).any()
+        rest = [t for t in range(T) if t not in (1, T - 2)]
+        assert torch.equal(y[rest], ref[rest]) and not torch.isfinite(y[1]).any()
 
 
-@pytest.mark.parametrize("T", [5, 90, 600])
-def test_repeats_and_graphs(T):
+@pytest.mark.parametrize("T,N,K", [(5, 192, 320), (90, 192, 320), (600, 192, 320), (700, 12320, 64)])
+def test_repeats_and_graphs(T, N, K):
     """The same bits every time, in a captured graph too, whose replays follow
     new inputs, with eager calls of other sizes between them."""
-    c, other = case(T, 192, 320, 4, 16, BF), case(T + 70, 192, 320, 4, 16, BF)
+    c, other = case(T, N, K, 4, 16, BF), case(T + 70, N, K, 4, 16, BF)
     y, grads = forward(c), backward(c)
     assert torch.equal(forward(c), y) and all(torch.equal(a, b) for a, b in zip(backward(c), grads))
     s = torch.cuda.Stream()

@@ -105,6 +105,12 @@ def test_widths(K, bs, qt, dq, T):
     both(rows(T, K, BF), weight(V, K, bs, qt, dq), targets(T, V), dlosses(T))
 
 
+# tokens in turns, pieces of the vocabulary where the tile product is not used (a width of 32)
+@pytest.mark.parametrize("T,V,K", [(4500, 600, 64), (4000, 16400, 32), (5000, 300, 96)])
+def test_turns_and_pieces(T, V, K):
+    both(rows(T, K, BF, whole=True), whole_weight(V, K, bs=32), targets(T, V), dlosses(T), whole=True)
+
+
 @pytest.mark.parametrize("T", [9, 300, 600])
 def test_loss_types(T):
     for dtype in (BF, HF):
