@@ -439,13 +439,13 @@ __global__ __launch_bounds__(1024) void loss_rows_kernel(const float *__restrict
 
 // D = D f + sums, the part of this workgroup's terms
 struct EpilogueAdd : EpilogueBase {
-  static constexpr bool kAdds = true;
+  static constexpr bool kPlain = true, kAdds = true;
   float *C;
   const float *f;
   int64_t ld, part;
   bool first;
-  __device__ float *row(int m) const { return C + blockIdx.y * part + m * ld; }
-  __device__ void store(float *row, int n, float v) const { row[n] = v; }
+  __device__ __forceinline__ float *row(int m) const { return C + blockIdx.y * part + m * ld; }
+  __device__ __forceinline__ void store(float *, int, float) const {}
 };
 
 // ---------------------------------------------------------------------------

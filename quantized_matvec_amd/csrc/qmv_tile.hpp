@@ -180,32 +180,39 @@ __global__ __launch_bounds__(256, 1) void tile_kernel(TileArgs g, Epi epi) {
     __builtin_amdgcn_s_waitcnt((7 << 4) | (15 << 8));  // no load into LDS outlives the kernel
   }
   epi.begin(acc, g, M, m0, n0, wm, wn, lane);
-  if constexpr (Epi::kAdds) {
-    // C = C f[row] + sums, in parts of 32 x 128, whose 64 loads are in flight together: bounded
-    // resources (what is not there, or no rows yet, reads as 0 and is not written), no branches,
-    // and no part's loads before the last part's stores, which would not fit the registers
-    const __amdgpu_buffer_rsrc_t rc = make_rsrc(epi.row(m0) + n0, epi.first ? 0 : 0x7fffffffu);
+  if constexpr (Epi::kPlain) {
+    // C = sums, or C f[row] + sums, in parts of 32 x 128: bounded resources (what is not there, or
+    // no rows yet, reads as 0 and is not written), so no branches, and the loads of a part are in
+    // flight together; no part's loads before the last part's stores, which would not fit the registers
     const __amdgpu_buffer_rsrc_t ro = make_rsrc(epi.row(m0) + n0, 0x7fffffffu);
-    const __amdgpu_buffer_rsrc_t rf = make_rsrc(epi.f + m0, epi.first ? 0 : (uint32_t)mrows * 4);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       __builtin_amdgcn_sched_barrier(0);
-      float f[16], old[16][4];
       auto place = [&](int r, int j) __attribute__((always_inline)) {
         const int m = mw - m0 + 32 * i + 8 * (r >> 2) + (r & 3), n = nw - n0 + 32 * j;
         return m < mrows && n < ncols ? (uint32_t)((m * (int)epi.ld + n) * 4) : 0x80000000u;
       };
+      if constexpr (Epi::kAdds) {
+        const __amdgpu_buffer_rsrc_t rc = make_rsrc(epi.row(m0) + n0, epi.first ? 0 : 0x7fffffffu);
+        const __amdgpu_buffer_rsrc_t rf = make_rsrc(epi.f + m0, epi.first ? 0 : (uint32_t)mrows * 4);
+        float f[16], old[16][4];
 #pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        f[r] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rf, (uint32_t)(mw - m0 + 32 * i + 8 * (r >> 2) + (r & 3)) * 4, 0, 0));
+        for (int r = 0; r < 16; ++r) {
+          f[r] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rf, (uint32_t)(mw - m0 + 32 * i + 8 * (r >> 2) + (r & 3)) * 4, 0, 0));
 #pragma unroll
-        for (int j = 0; j < 4; ++j) old[r][j] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rc, place(r, j), 0, 0));
+          for (int j = 0; j < 4; ++j) old[r][j] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rc, place(r, j), 0, 0));
+        }
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(fmaf(old[r][j], f[r], acc[i][j][r])), ro, place(r, j), 0, 0);
+      } else {
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(acc[i][j][r]), ro, place(r, j), 0, 0);
       }
-#pragma unroll
-      for (int r = 0; r < 16; ++r)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(fmaf(old[r][j], f[r], acc[i][j][r])), ro, place(r, j), 0, 0);
     }
     return;
   }
@@ -228,14 +235,16 @@ __global__ __launch_bounds__(256, 1) void tile_kernel(TileArgs g, Epi epi) {
 
 // What becomes of the sums: begin() may add to them, row() gives what store() needs of a row.
 struct EpilogueBase {
-  static constexpr bool kAdds = false;  // C f + sums, of members C, f, ld, first
-  __device__ void begin(tile_acc_t (&)[4][4], const TileArgs &, int, int, int, int, int, int) const {}
+  static constexpr bool kPlain = false;  // into C in fp32 as they are, of rows C, ld apart (256 of them: below 2^31 bytes)
+  static constexpr bool kAdds = false;   // plain, C f + sums, but for `first`
+  __device__ __forceinline__ void begin(tile_acc_t (&)[4][4], const TileArgs &, int, int, int, int, int, int) const {}
 };
-struct EpilogueF32 : EpilogueBase {  // C[m][n] in fp32
+struct EpilogueF32 : EpilogueBase {
+  static constexpr bool kPlain = true;
   float *C;
   int64_t ld;
-  __device__ float *row(int m) const { return C + m * ld; }
-  __device__ void store(float *row, int n, float v) const { row[n] = v; }
+  __device__ __forceinline__ float *row(int m) const { return C + m * ld; }
+  __device__ __forceinline__ void store(float *, int, float) const {}
 };
 
 }  // namespace qmv

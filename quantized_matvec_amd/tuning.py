@@ -24,6 +24,7 @@ from typing import Optional, Union
 
 import torch
 
+from .attention import _raw_stream
 from .qmv import _DT, _QT, QuantState, _Absmax, _check, _check_state, _dev, lib as _lib
 
 __all__ = ["LoraAdapters", "cross_entropy_4bit", "distill_4bit", "lora_4bit", "lora_4bit_backward"]
@@ -71,14 +72,35 @@ def lib() -> ctypes.CDLL:
 # --------------------------------------------------------------------------
 # operands
 # --------------------------------------------------------------------------
+# A decode step is a handful of calls on small tensors, where the host decides:
+# each attribute of a tensor is asked for once, and what fits is seen to fit
+# before the checks that say what does not.
+def _holds(t: torch.Tensor, n: int, dtype, device) -> bool:
+    return t.numel() == n and t.dtype is dtype and t.device == device
+
+
 def _weight(packed: torch.Tensor, state: QuantState, device):
     """The packed codes as the kernels take them, and the weight's descriptor."""
-    if len(state.shape) != 2:
+    shape = state.shape
+    if len(shape) != 2:
         raise ValueError("the quantized weight must be 2-D [N, K]")
-    _check_state(packed, state, device)
+    rows, cols = shape
+    n, bs = rows * cols, state.blocksize
+    nb = -(-n // bs)
+    q, a2, off, c2, bs2 = state.absmax_q, state.absmax2, state.offset, state.code2, state.blocksize2
+    if state.absmax is not None:
+        fits = q is None and a2 is None and off is None and c2 is None and _holds(state.absmax, nb, torch.float32, device)
+        scales = _Absmax(state.absmax.data_ptr(), None, None, None, None, 0) if fits else None
+    else:
+        fits = (q is not None and a2 is not None and off is not None and c2 is not None and _holds(q, nb, torch.uint8, device)
+                and _holds(a2, -(-nb // bs2), torch.float32, device) and _holds(off, 1, torch.float32, device)
+                and _holds(c2, 256, torch.float32, device))
+        scales = _Absmax(None, q.data_ptr(), a2.data_ptr(), c2.data_ptr(), off.data_ptr(), bs2) if fits else None
+    if not fits or not _holds(packed, (n + 1) // 2, torch.uint8, device):
+        _check_state(packed, state, device)  # says what does not fit
+        raise ValueError("the quantized weight's tensors do not fit its shape")
     packed = _dev(packed, "packed")
-    rows, cols = state.shape
-    return packed, _Weight(packed.data_ptr(), state._c(), rows, cols, state.blocksize, _QT[state.quant_type])
+    return packed, _Weight(packed.data_ptr(), scales, rows, cols, bs, _QT[state.quant_type])
 
 
 def _tokens(x: torch.Tensor, name: str, width: int) -> torch.Tensor:
@@ -114,11 +136,13 @@ def _call(name: str, device: torch.device, nbytes: int, call) -> None:
     """call(workspace, its size, stream) on the operands' device.  The workspace
     is the allocator's again afterwards, which hands it out to later work of
     this stream (of this graph, in a capture) only."""
-    if device.index != torch.cuda.current_device():
+    index = device.index
+    if index != torch.cuda.current_device():
         with torch.cuda.device(device):
             return _call(name, device, nbytes, call)
     ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
-    _check(call(ws.data_ptr(), nbytes, torch.cuda.current_stream(device).cuda_stream), name)
+    st = torch.cuda.current_stream(device).cuda_stream if _raw_stream is None else _raw_stream(index)
+    _check(call(ws.data_ptr(), nbytes, st), name)
 
 
 class LoraAdapters:
