@@ -84,10 +84,10 @@ __global__ __launch_bounds__(256) void lora_down_kernel(const uint16_t *__restri
   }
 }
 
-// out[t][n] = round(base[t][n] + bias[n] + sum_r up[a][n][r] u[t][r]), u's pieces
-// added up in order: 256 / R of them side by side, then those sums
+// out[t][n] = round(base[t][n] + bias[n] + sum_r up[a][n][r] u[t][r]), base in parts
+// that are added up in order, and u's pieces: 256 / R of them side by side, then those sums
 template <int DT, int ODT>
-__global__ __launch_bounds__(256) void lora_up_kernel(const float *__restrict__ base, int64_t N,
+__global__ __launch_bounds__(256) void lora_up_kernel(const float *__restrict__ base, int base_parts, int64_t N,
                                                       const uint16_t *__restrict__ up, int count, int R,
                                                       const int32_t *__restrict__ index, const float *__restrict__ u,
                                                       int pieces, int64_t T, const uint16_t *__restrict__ bias,
@@ -99,6 +99,8 @@ __global__ __launch_bounds__(256) void lora_up_kernel(const float *__restrict__ 
   float acc = 0.f, more = 0.f;
   if (n < N) {
     acc = base[t * N + n];
+#pragma unroll 8
+    for (int s = 1; s < base_parts; ++s) acc += base[(s * T + t) * N + n];
     if (bias) more = bits16_to_f32<DT>(bias[n]);
   }
   if (a >= 0 && a < count) {
@@ -612,7 +614,7 @@ __global__ __launch_bounds__(256) void lora_join_kernel(const float *__restrict_
 // ---------------------------------------------------------------------------
 // host
 // ---------------------------------------------------------------------------
-constexpr int64_t kFew = 32;        // tokens up to which a token is a workgroup's
+constexpr int64_t kFew = 64;        // tokens up to which a token is a workgroup's
 constexpr int64_t kTiledFrom = 640, kTiledTiles = 144;  // tokens and tiles from which the tile product is used
 constexpr int64_t kRows = 4096;     // tokens of a fp32 projection in the workspace
 constexpr int64_t kTiledRows = 16384;
@@ -668,7 +670,7 @@ struct ProductPlan {
   size_t base, back;   // fp32 projection, the backward product's own workspace
   size_t decoded;
 };
-static ProductPlan product_plan(Carver &c, int64_t T, int64_t N, int64_t K, int log2bs, bool backward) {
+static ProductPlan product_plan(Carver &c, int64_t T, int64_t N, int64_t K, int log2bs, bool backward, bool few) {
   ProductPlan p{};
   const int64_t L = backward ? N : K, width = backward ? K : N;
   // The tile product wants the decoding spread over many tokens, and tiles for half the compute units
@@ -685,7 +687,7 @@ static ProductPlan product_plan(Carver &c, int64_t T, int64_t N, int64_t K, int 
     if (p.piece > width) p.piece = width;
     p.decoded = c.take((size_t)p.piece * L * 2);
   } else {
-    p.base = c.take((size_t)p.tokens * width * 4);
+    p.base = c.take((size_t)p.tokens * width * 4 * (few && skinny_fits(T, K, log2bs) ? skinny_parts(K) : 1));
     if (backward) {
       size_t need = 0;
       for (int64_t m : {p.tokens, T % p.tokens})
@@ -729,7 +731,7 @@ static LoraPlan lora_plan(int64_t T, int64_t N, int64_t K, int log2bs, int count
   LoraPlan p{};
   Carver c;
   p.few = !backward && T <= kFew;
-  p.product = product_plan(c, T, N, K, log2bs, backward);
+  p.product = product_plan(c, T, N, K, log2bs, backward, p.few);
   p.tokens = p.product.tokens;
   if (p.few) {
     p.u_few = c.take((size_t)few_pieces(K) * T * R * 4);
@@ -838,12 +840,14 @@ static hipError_t lora_t(const uint16_t *x, int64_t T, const Weight4 &w, const L
     const int pieces = few_pieces(w.K);
     hipLaunchKernelGGL(lora_down_kernel<DT>, dim3((unsigned)T, (unsigned)pieces), dim3(256), 0, st, x, w.K, l.down, l.scale,
                        l.count, l.rank, index, u, T);
+    const bool skinny = skinny_fits(T, w.K, w.log2bs);
     const hipError_t e =
-        T <= 8 ? launch_gemv_4bit(x, DT, (int)T, w.N, w.K, w.packed, w.sc, w.dq, w.log2bs, w.qt, base, kF32, nullptr, st)
-               : launch_gemm_4bit(x, DT, T, w.N, w.K, w.packed, w.sc, w.dq, w.log2bs, w.qt, base, kF32, nullptr, st);
+        skinny   ? launch_skinny(x, DT, T, w, base, st)
+        : T <= 8 ? launch_gemv_4bit(x, DT, (int)T, w.N, w.K, w.packed, w.sc, w.dq, w.log2bs, w.qt, base, kF32, nullptr, st)
+                 : launch_gemm_4bit(x, DT, T, w.N, w.K, w.packed, w.sc, w.dq, w.log2bs, w.qt, base, kF32, nullptr, st);
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL((lora_up_kernel<DT, ODT>), dim3((unsigned)((w.N + 255) / 256), (unsigned)T), dim3(256), 0, st, base,
-                       w.N, l.up, l.count, l.rank, index, u, pieces, T, bias, y);
+                       skinny ? skinny_parts(w.K) : 1, w.N, l.up, l.count, l.rank, index, u, pieces, T, bias, y);
     return hipGetLastError();
   }
   const Places pl = places_at(p.places, ws);

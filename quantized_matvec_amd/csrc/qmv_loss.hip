@@ -107,16 +107,27 @@ __device__ __forceinline__ float block_reduce(float v, float *buf, F op) {  // 2
 // multiple of 32 below n (the columns from np on go to `tail`).  Two launches,
 // but no workgroup reads more than 32 kB.
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ void mark_ids(uint32_t *out, const int64_t *ids, int k, int64_t v0, int n, const float *row,
-                                         float inv_tau, float *lt) {  // one barrier
+__device__ __forceinline__ void mark_ids(uint32_t *out, const int64_t *ids, int k, int64_t v0, int n) {  // one barrier
   for (int j = threadIdx.x; j < k; j += 256) {
     const int64_t c = ids[j] - v0;
-    if (c >= 0 && c < n) {
-      atomicOr(&out[c >> 5], 1u << (c & 31));
-      if (lt) lt[j] = row[c] * inv_tau;
-    }
+    if (c >= 0 && c < n) atomicOr(&out[c >> 5], 1u << (c & 31));
   }
   __syncthreads();
+}
+
+// Logits that came in parts, n apart: added up in order, the sum left in the first.
+__global__ __launch_bounds__(256) void loss_sum_kernel(float *__restrict__ logits, int parts, int64_t n) {
+  const int64_t i = (int64_t)blockIdx.x * 1024 + threadIdx.x;
+  float sum[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) sum[q] = i + 256 * q < n ? logits[i + 256 * q] : 0.f;
+#pragma unroll 4
+  for (int s = 1; s < parts; ++s)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) sum[q] += logits[s * n + min(i + 256 * q, n - 1)];
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    if (i + 256 * q < n) logits[i + 256 * q] = sum[q];
 }
 
 __global__ __launch_bounds__(256) void loss_part_kernel(const float *__restrict__ logits, int64_t v0, int n,
@@ -130,12 +141,13 @@ __global__ __launch_bounds__(256) void loss_part_kernel(const float *__restrict_
   out[threadIdx.x] = 0;
   float l[32];
 #pragma unroll
-  for (int q = 0; q < 32; ++q) {
-    const int c = 256 * q + threadIdx.x;
-    l[q] = row[min(c, cols - 1)] * inv_tau;
-  }
+  for (int q = 0; q < 32; ++q) l[q] = row[min(256 * q + (int)threadIdx.x, cols - 1)] * inv_tau;
   __syncthreads();
-  mark_ids(out, ids + t * k, k, v0 + c0, cols, row, inv_tau, lt + t * k);
+  mark_ids(out, ids + t * k, k, v0 + c0, cols);
+  for (int j = threadIdx.x; j < k; j += 256) {
+    const int64_t c = ids[t * k + j] - v0 - c0;
+    if (c >= 0 && c < cols) lt[t * k + j] = row[c] * inv_tau;
+  }
   float m = -INFINITY;
 #pragma unroll
   for (int q = 0; q < 32; ++q) {
@@ -182,7 +194,7 @@ __global__ __launch_bounds__(256) void loss_merge_kernel(const float *__restrict
   if constexpr (GRAD) {
     out[threadIdx.x] = 0;
     __syncthreads();
-    mark_ids(out, ids + t * k, k, v0 + c0, cols, row, inv_tau, nullptr);
+    mark_ids(out, ids + t * k, k, v0 + c0, cols);
 #pragma unroll 8
     for (int q = 0; q < 32; ++q) {
       const int c = 256 * q + threadIdx.x;
@@ -489,7 +501,7 @@ static LossPlan loss_plan(int64_t T, int64_t V, int64_t K, int log2bs, int k, bo
     int64_t piece = (kLogits / p.tokens) & ~(int64_t)4095;  // rows_of wants 4096 rows
     if (piece < 4096) piece = 4096;
     p.piece = (int)(V < piece ? V : piece);
-    p.logits = c.take(n * p.piece * 4);
+    p.logits = c.take(n * p.piece * 4 * (skinny_fits(p.tokens, K, log2bs) ? skinny_parts(K) : 1));
     p.segments = c.take(n * ((p.piece + kSegment - 1) / kSegment) * 8);
     p.carry = c.take(n * 16);
     if (grad) {
@@ -567,8 +579,13 @@ static hipError_t pieces_plain(const LossPlan &p, const uint16_t *x, int64_t m, 
   for (int64_t v = 0; v < w.N; v += p.piece, turn ^= 1) {
     const int n = (int)(w.N - v < p.piece ? w.N - v : p.piece), np = n & ~31, n_segments = (n + kSegment - 1) / kSegment;
     const Weight4 c = rows_of(w, v, n);
-    hipError_t e = launch_gemm_4bit(x, DT, m, n, w.K, c.packed, c.sc, c.dq, c.log2bs, c.qt, logits, kF32, nullptr, st);
+    const bool skinny = skinny_fits(m, w.K, w.log2bs);
+    hipError_t e = skinny ? launch_skinny(x, DT, m, c, logits, st)
+                          : launch_gemm_4bit(x, DT, m, n, w.K, c.packed, c.sc, c.dq, c.log2bs, c.qt, logits, kF32, nullptr, st);
     if (e != hipSuccess) return e;
+    if (skinny && skinny_parts(w.K) > 1)
+      hipLaunchKernelGGL(loss_sum_kernel, dim3((unsigned)((m * n + 1023) / 1024)), dim3(256), 0, st, logits,
+                         skinny_parts(w.K), m * n);
     hipLaunchKernelGGL(loss_part_kernel, dim3(n_segments, (unsigned)m), dim3(256), 0, st, logits, v, n, ids, tg.k, tg.inv_tau,
                        rs.lt, segments);
     float2 *before = carry + (turn ? p.tokens : 0), *after = carry + (turn ? 0 : p.tokens);

@@ -41,6 +41,11 @@ inline hipError_t launch_decode_rows(const Weight4 &w, int dt, void *W, hipStrea
   return launch_dequantize_4bit(w.packed, w.sc, w.dq, w.N * w.K, w.log2bs, w.qt, W, dt, st);
 }
 
+// Up to 64 rows times a weight, in fp32, in parts [skinny_parts][M][N] that the caller adds up.
+bool skinny_fits(int64_t M, int64_t K, int log2bs);
+int skinny_parts(int64_t K);
+hipError_t launch_skinny(const void *A, int dt, int64_t M, const Weight4 &w, float *parts, hipStream_t st);
+
 struct Lora {
   const uint16_t *down, *up;
   const float *scale;

@@ -16,12 +16,12 @@ def weight(V, K, bs=64, qt="nf4", dq=False, seed=0, dtype=BF, gain=2.0):
 
 
 # The product's kernels round the weight T * a to 16 bits, except those for up
-# to 16 rows, which round T alone (qmv_gemm.hip, qmv_gemv.hip) and multiply by a
-# in fp32.  Of FP4's values only 0, 1/4, 1/2 and 1 are the same in 16 bits (1/6 is
-# off by up to 2^-9 of itself in bf16).  So weights that are whole multiples of a
-# power of two by their scale of 6 are exact from 17 rows on; below, a weight is
-# off by up to the type's rounding, and the exact ones take those four values.
-NARROW = 16
+# to 64 rows, which round T alone (qmv_gemm.hip, qmv_gemv.hip, qmv_skinny.hip) and
+# multiply by a in fp32.  Of FP4's values only 0, 1/4, 1/2 and 1 are the same in 16
+# bits (1/6 is off by up to 2^-9 of itself in bf16).  So weights that are whole
+# multiples of a power of two by their scale of 6 are exact from 65 rows on; below,
+# a weight is off by up to the type's rounding, and the exact ones take those four values.
+NARROW = 64
 SAME_IN_16_BITS = [0, 3, 5, 7, 8, 11, 13, 15]
 
 
@@ -88,7 +88,7 @@ def test_tokens(T, dtype, whole):
 
 # fewer columns than a matrix-core tile, pieces and tails of the vocabulary
 @pytest.mark.parametrize("V", [1, 2, 31, 32, 33, 63, 255, 257, 4095, 8191, 8192, 8193, 8223, 16384, 20001])
-@pytest.mark.parametrize("T,whole", [(3, True), (3, "table"), (40, True), (300, True), (500, True)])
+@pytest.mark.parametrize("T,whole", [(3, True), (3, "table"), (40, True), (40, "table"), (300, True), (500, True)])
 def test_vocabularies(V, T, whole):
     K = 128
     w = whole_weight(V, K, table=whole == "table")
