@@ -5,8 +5,9 @@ namespace qmv {
 
 // ---------------------------------------------------------------------------
 // W[v][c] = round(T[code] a) of rows v and columns c0 + c, exactly as
-// dequantize_4bit returns them in DT, and its transpose Wt[c][v], rows past the
-// last as zeros there: each where it is wanted, from one read of the codes.
+// dequantize_4bit returns them in DT, and its transpose Wt[c][v], both up to a
+// multiple of 64 along the sum with zeros: each where it is wanted, from one read
+// of the codes.
 //
 // A workgroup takes 64 rows x 128 columns.  A thread decodes 8 columns of four
 // rows (4 bytes of codes, one block), 16 threads a row, and stores their 16
@@ -44,7 +45,7 @@ __global__ __launch_bounds__(256) void decode_piece_kernel(const uint8_t *__rest
 #pragma unroll
     for (int i = 0; i < 4; ++i) o[i] = cvt_pair<DT>(tab[w[q] >> (8 * i + 4) & 15] * a[q], tab[w[q] >> (8 * i) & 15] * a[q]);
     const uint4 out = make_uint4(o[0], o[1], o[2], o[3]);
-    if (W && v < n && c < cols) *reinterpret_cast<uint4 *>(W + v * ldw + c) = out;
+    if (W && v < n && c < ldw) *reinterpret_cast<uint4 *>(W + v * ldw + c) = out;  // past cols: zeros
     *reinterpret_cast<uint4 *>(&tile[16 * q + row][col ^ (8 * ((16 * q + row) >> 3 & 7))]) = out;
   }
   if (!Wt) return;
@@ -78,6 +79,23 @@ hipError_t launch_decode_piece(const Weight4 &w, int dt, int64_t c0, int64_t col
     else QMV_D(kBF16, false);
   }
 #undef QMV_D
+  return hipGetLastError();
+}
+
+// Rows [T, L] with zeros up to Lp elements (multiples of 8, L of 32): a sum's last
+// 32 terms must not meet what lies behind a row.
+__global__ __launch_bounds__(256) void pad_rows_kernel(const uint4 *__restrict__ in, int64_t T, int L8, int Lp8,
+                                                       uint4 *__restrict__ out) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= T * Lp8) return;
+  const int64_t t = i / Lp8;
+  const int c = (int)(i % Lp8);
+  out[i] = c < L8 ? in[t * L8 + c] : make_uint4(0, 0, 0, 0);
+}
+
+hipError_t launch_pad_rows(const void *in, int64_t T, int64_t L, int64_t Lp, void *out, hipStream_t st) {
+  hipLaunchKernelGGL(pad_rows_kernel, dim3((unsigned)((T * (Lp / 8) + 255) / 256)), dim3(256), 0, st,
+                     static_cast<const uint4 *>(in), T, (int)(L / 8), (int)(Lp / 8), static_cast<uint4 *>(out));
   return hipGetLastError();
 }
 

@@ -425,9 +425,10 @@ __device__ __forceinline__ void add_low_rank(tile_acc_t (&acc)[MI][NJ], const Lo
 }
 
 // out[t][c] = round(base[t][c] + bias[c] + the adapter's part): a unit and 128 columns
-// a workgroup, 32 columns a wave; base's loads go out first.  Bound by base and out.
+// a workgroup, 32 columns a wave; base (in parts, added up in order) is asked for first.  Bound by base and out.
 template <int DT, int ODT, bool TRANS>
-__global__ __launch_bounds__(256, 2) void lora_expand_kernel(const float *__restrict__ base, LowRank lr, Places pl,
+__global__ __launch_bounds__(256, 2) void lora_expand_kernel(const float *__restrict__ base, int base_parts,
+                                                             int64_t part, LowRank lr, Places pl,
                                                           const uint16_t *__restrict__ bias,
                                                           typename Storage<ODT>::type *__restrict__ out) {
   if ((int)blockIdx.x >= *pl.n_units) return;
@@ -444,6 +445,11 @@ __global__ __launch_bounds__(256, 2) void lora_expand_kernel(const float *__rest
       token[i][r] = pl.order[min(unit.y + 32 * i + 8 * (r >> 2) + 4 * h + (r & 3), unit.z - 1)];
       old[i][r] = base[token[i][r] * lr.width + cin];
     }
+  for (int s = 1; s < base_parts; ++s)
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) old[i][r] += base[s * part + token[i][r] * lr.width + cin];
   const float more = bias ? bits16_to_f32<DT>(bias[cin]) : 0.f;
   tile_acc_t acc[2][1];
 #pragma unroll
@@ -664,11 +670,12 @@ static Places places_at(const PlacesPlan &p, char *ws) {
 
 // The product of tokens with a 4-bit weight: width [N] outputs of sums over [K] (forward) or the other way round
 struct ProductPlan {
+  // tiled: the tile product, with the adapters' part added to its sums; parts > 0: the tile product in
+  // fp32, in parts of the sum; else gemm_4bit's kernels in fp32
   bool tiled;
-  int64_t tokens;      // at a time
-  int64_t piece;       // columns of the output whose weights are decoded at a time
-  size_t base, back;   // fp32 projection, the backward product's own workspace
-  size_t decoded;
+  int parts;
+  int64_t split, tokens, piece, Lp;  // terms of a part, tokens at a time, columns whose weights are decoded at a time
+  size_t base, back, decoded, x;     // fp32 projection, gemm_4bit_backward's own, decoded weights, rows padded to Lp
 };
 static ProductPlan product_plan(Carver &c, int64_t T, int64_t N, int64_t K, int log2bs, bool backward, bool few) {
   ProductPlan p{};
@@ -678,17 +685,32 @@ static ProductPlan product_plan(Carver &c, int64_t T, int64_t N, int64_t K, int 
   // sums, 448 tokens 155 / 108, 768 tokens (168 tiles) 151 / 187, 4096 tokens 495 / 727; 4096 x 4096, 2048 tokens
   // (128 tiles) 126 / 122, 4096 tokens 154 / 226; 4096 x 14336, 2048 tokens 357 / 303, 4096 tokens 429 / 588
   const int64_t tiles = ((T + kTileM - 1) / kTileM) * ((width + kTileN - 1) / kTileN);
-  p.tiled = T >= kTiledFrom && tiles >= kTiledTiles && L % 64 == 0 && L <= 65536 && width <= ((int64_t)1 << 30);
+  const bool can = L <= 65536 && width <= ((int64_t)1 << 30);
+  p.tiled = can && T >= kTiledFrom && tiles >= kTiledTiles;
+  const bool parts = can && !p.tiled && backward && T >= kTiledFrom && !fast_backward(N, K, log2bs);
   const int64_t most = p.tiled ? kTiledRows : kRows, turns = (T + most - 1) / most;
   p.tokens = (T + turns - 1) / turns;
-  if (p.tiled) {
-    p.piece = kDecoded / L & ~(int64_t)4095;  // L is at most 2^16: 2048 .. ; rows_of wants 4096 rows
+  p.Lp = to64(L);
+  if (p.tiled || parts) {
+    p.piece = kDecoded / p.Lp & ~(int64_t)4095;  // L is at most 2^16: 2048 .. ; rows_of wants 4096 rows
     if (p.piece < 4096) p.piece = 4096;
     if (p.piece > width) p.piece = width;
-    p.decoded = c.take((size_t)p.piece * L * 2);
-  } else {
-    p.base = c.take((size_t)p.tokens * width * 4 * (few && skinny_fits(T, K, log2bs) ? skinny_parts(K) : 1));
-    if (backward) {
+    p.decoded = c.take((size_t)p.piece * p.Lp * 2);
+    if (p.Lp != L) p.x = c.take((size_t)p.tokens * p.Lp * 2);
+  }
+  if (parts) {
+    // gemm_4bit_backward's other kernel does not divide the sum; us of a call in parts / with it: 2111 tokens, 832 x
+    // 3712, rank 8, 90 / 122; few tokens do not pay for the decoding: 468 tokens, 8768 x 1408, rank 16, 244 / 161
+    const int64_t there = ((p.tokens + kTileM - 1) / kTileM) * ((width + kTileN - 1) / kTileN);
+    int64_t n = there >= 256 ? 1 : 256 / there;
+    if (n > p.Lp / 256) n = p.Lp / 256 > 0 ? p.Lp / 256 : 1;
+    p.split = to64((p.Lp + n - 1) / n);
+    p.parts = (int)((p.Lp + p.split - 1) / p.split);
+  }
+  if (!p.tiled) {
+    const int in = parts ? p.parts : few && skinny_fits(T, K, log2bs) ? skinny_parts(K) : 1;
+    p.base = c.take((size_t)p.tokens * width * 4 * in);
+    if (backward && !parts) {
       size_t need = 0;
       for (int64_t m : {p.tokens, T % p.tokens})
         if (m > 0) {
@@ -803,31 +825,47 @@ static hipError_t product(const LoraPlan &p, const uint16_t *x, int64_t m, const
   const Split s = split_of(p.inner, ws);
   const int Rp = (l.rank + 15) & ~15;
   const LowRank lr{s.hi, s.lo, TRANS ? l.down : l.up, width, l.rank, Rp, l.count, pl.adapter, pl.start};
-  if (!p.product.tiled) {
-    float *base = reinterpret_cast<float *>(ws + p.product.base);
+  const ProductPlan &pp = p.product;
+  float *base = reinterpret_cast<float *>(ws + pp.base);
+  if (pp.tiled || pp.parts) {
+    uint16_t *W = reinterpret_cast<uint16_t *>(ws + pp.decoded);
+    if (pp.Lp != L) {
+      uint16_t *padded = reinterpret_cast<uint16_t *>(ws + pp.x);
+      const hipError_t e = launch_pad_rows(x, m, L, pp.Lp, padded, st);
+      if (e != hipSuccess) return e;
+      x = padded;
+    }
+    for (int64_t c = 0; c < width; c += pp.piece) {
+      const int64_t n = width - c < pp.piece ? width - c : pp.piece;
+      const hipError_t e = TRANS ? launch_decode_piece(w, DT, c, n, nullptr, 0, W, pp.Lp, st)
+                                 : launch_decode_rows(rows_of(w, c, n), DT, W, pp.Lp, st);
+      if (e != hipSuccess) return e;
+      TileArgs a = tile_args(x, pp.Lp, W, pp.Lp, m, n, pp.Lp);
+      if (pp.tiled) {
+        a.rows = pl.order;
+        EpilogueLora<DT, ODT, TRANS> epi;
+        epi.lr = lr;
+        epi.lr.factor += TRANS ? c : c * l.rank;
+        epi.order = pl.order, epi.bias = bias ? bias + c : nullptr, epi.out = out + c, epi.ld = width;
+        hipLaunchKernelGGL((tile_kernel<DT, EpilogueLora<DT, ODT, TRANS>>), dim3(a.ncol * a.nrow), dim3(256), 0, st, a, epi);
+      } else {
+        a.split = (int)pp.split;
+        EpilogueF32 epi;
+        epi.C = base + c, epi.ld = width, epi.part = m * width;
+        hipLaunchKernelGGL((tile_kernel<DT, EpilogueF32>), dim3(a.ncol * a.nrow, pp.parts), dim3(256), 0, st, a, epi);
+      }
+    }
+    if (pp.tiled) return hipGetLastError();
+  } else {
     const hipError_t e =
         TRANS ? launch_gemm_4bit_backward(x, DT, m, w.N, w.K, w.packed, w.sc, w.dq, w.log2bs, w.qt, base, kF32,
-                                          ws + p.product.back, st)
+                                          ws + pp.back, st)
               : launch_gemm_4bit(x, DT, m, w.N, w.K, w.packed, w.sc, w.dq, w.log2bs, w.qt, base, kF32, nullptr, st);
     if (e != hipSuccess) return e;
-    const dim3 grid((unsigned)most_units(m, l.count), (unsigned)((width + 127) / 128));
-    hipLaunchKernelGGL((lora_expand_kernel<DT, ODT, TRANS>), grid, dim3(256), 0, st, base, lr, pl, bias, out);
-    return hipGetLastError();
   }
-  uint16_t *W = reinterpret_cast<uint16_t *>(ws + p.product.decoded);
-  for (int64_t c = 0; c < width; c += p.product.piece) {
-    const int64_t n = width - c < p.product.piece ? width - c : p.product.piece;
-    const hipError_t e = TRANS ? launch_decode_piece(w, DT, c, n, nullptr, 0, W, L, st)
-                               : launch_decode_rows(rows_of(w, c, n), DT, W, st);
-    if (e != hipSuccess) return e;
-    TileArgs a = tile_args(x, L, W, L, m, n, L);
-    a.rows = pl.order;
-    EpilogueLora<DT, ODT, TRANS> epi;
-    epi.lr = lr;
-    epi.lr.factor += TRANS ? c : c * l.rank;
-    epi.order = pl.order, epi.bias = bias ? bias + c : nullptr, epi.out = out + c, epi.ld = width;
-    hipLaunchKernelGGL((tile_kernel<DT, EpilogueLora<DT, ODT, TRANS>>), dim3(a.ncol * a.nrow), dim3(256), 0, st, a, epi);
-  }
+  const dim3 grid((unsigned)most_units(m, l.count), (unsigned)((width + 127) / 128));
+  hipLaunchKernelGGL((lora_expand_kernel<DT, ODT, TRANS>), grid, dim3(256), 0, st, base, pp.parts ? pp.parts : 1, m * width,
+                     lr, pl, bias, out);
   return hipGetLastError();
 }
 

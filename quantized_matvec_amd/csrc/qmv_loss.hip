@@ -19,7 +19,7 @@ namespace qmv {
 
 constexpr int kSegment = 8192;   // columns of a logits row that a workgroup takes
 constexpr int64_t kTokens = 4096;  // most tokens taken at a time
-constexpr int kTail = 32;
+constexpr int kTail = 64;
 constexpr int kMostPiece = 32768;   // of the tile product's pieces
 constexpr int64_t kTiledFrom = 448;  // tokens from which it is used
 constexpr int64_t kLogits = (int64_t)1 << 26;  // logits of a piece where it is not
@@ -33,7 +33,7 @@ constexpr float kGain = DT == kF16 ? 16384.f : 1.f;
 struct RowState {
   float *m, *s, *f;  // running maximum, sum, and the factor of what D held before this piece
   float *lt;         // [T, k] logits of the target ids
-  float *tail;       // [T, 32] logits of the last V % 32 columns (-inf: none, or a target)
+  float *tail;       // [T, 64] logits of the last V % 64 columns (-inf: none, or a target)
 };
 
 // ---------------------------------------------------------------------------
@@ -104,7 +104,7 @@ __device__ __forceinline__ float block_reduce(float v, float *buf, F op) {  // 2
 // loss_part_kernel leaves each segment's maximum and sum (and takes the target ids'
 // logits); loss_merge_kernel puts them together with what was before the piece
 // and, with a gradient, writes P = exp(l - m) in 16 bits, [T, np] with np the
-// multiple of 32 below n (the columns from np on go to `tail`).  Two launches,
+// multiple of 64 below n (the columns from np on go to `tail`).  Two launches,
 // but no workgroup reads more than 32 kB.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ void mark_ids(uint32_t *out, const int64_t *ids, int k, int64_t v0, int n) {  // one barrier
@@ -204,6 +204,7 @@ __global__ __launch_bounds__(256) void loss_merge_kernel(const float *__restrict
       if (c0 + c < np) P[t * np + c0 + c] = (uint16_t)f32_to_bits16<DT>(__expf(l - ref) * kGain<DT>);
       else rs.tail[t * kTail + c0 + c - np] = l;
     }
+    if (c0 + cols == n && (int)threadIdx.x < np - n) P[t * np + n + threadIdx.x] = 0;
   }
 }
 
@@ -228,7 +229,7 @@ __global__ __launch_bounds__(256) void loss_finish_kernel(const int64_t *__restr
                                                           CodeValues table, const float *__restrict__ dloss,
                                                           typename Storage<LDT>::type *__restrict__ loss,
                                                           uint16_t *__restrict__ dx) {
-  __shared__ float z[128], p[128], lt[128], each[128], coef[128 + kTail], tab[16], buf[4], by_block[8][64];
+  __shared__ float z[128], p[128], lt[128], each[128], coef[128 + kTail], tab[16], buf[4], by_block[64][64];
   __shared__ int64_t id[128 + kTail];
   const int64_t i = blockIdx.x;             // its place among the rows of D and rs
   const int64_t t = list ? list[i] : i;
@@ -310,8 +311,8 @@ __global__ __launch_bounds__(256) void loss_finish_kernel(const int64_t *__restr
   const float scale = m == -INFINITY ? 0.f : expf(m - M) / Z / kGain<DT>;
   const float offset = DQ ? sc.offset[0] : 0.f;
   const int entries = k + tail_n;
-  // 2048 columns at a time, 8 a thread; the entries' rows eight at a time, whose
-  // coefficients times the scales of their blocks (32 columns at least) are in LDS
+  // 2048 columns at a time, 8 a thread; 64 entries at a time have their coefficients
+  // times the scales of their blocks (32 columns at least) in LDS, eight rows are in flight
   for (int64_t base = 0; base < K; base += 2048) {
     const int64_t c = base + tid * 8;
     const bool in = c < K;
@@ -327,29 +328,34 @@ __global__ __launch_bounds__(256) void loss_finish_kernel(const int64_t *__restr
       for (int e = 0; e < 8; ++e) acc[e] *= scale;
     }
     const int log2sub = log2bs < 11 ? log2bs : 11, subs = 2048 >> log2sub;  // blocks in the columns
-    for (int j0 = 0; j0 < entries; j0 += 8) {
+    for (int j0 = 0; j0 < entries; j0 += 64) {
+      const int some = min(entries - j0, 64);
       __syncthreads();
-      for (int b = tid; b < 8 * subs; b += 256) {
+#pragma unroll 4
+      for (int b = tid; b < some * subs; b += 256) {
         const int j = j0 + b / subs;
         const int64_t col = base + ((int64_t)(b % subs) << log2sub);
-        const float cj = j < entries && col < K ? coef[j] : 0.f;
-        by_block[b / subs][b % subs] = cj == 0.f ? 0.f : cj * block_scale<DQ>(sc, (id[j] * K + col) >> log2bs, offset);
+        const float cj = coef[j];
+        by_block[b / subs][b % subs] =
+            cj == 0.f || col >= K ? 0.f : cj * block_scale<DQ>(sc, (id[j] * K + col) >> log2bs, offset);
       }
       __syncthreads();
       if (!in) continue;
-      uint32_t w[8];
+      for (int j1 = 0; j1 < some; j1 += 8) {
+        uint32_t w[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int j = j0 + e;
-        w[e] = j < entries && coef[j] != 0.f ? *reinterpret_cast<const uint32_t *>(packed + (id[j] * K + c) / 2) : 0;
-      }
+        for (int e = 0; e < 8; ++e) {
+          const int j = j1 + e;
+          w[e] = j < some && coef[j0 + j] != 0.f ? *reinterpret_cast<const uint32_t *>(packed + (id[j0 + j] * K + c) / 2) : 0;
+        }
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float a = by_block[e][(8 * tid) >> log2sub];
+        for (int e = 0; e < 8; ++e) {
+          const float a = j1 + e < some ? by_block[j1 + e][(8 * tid) >> log2sub] : 0.f;
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          acc[2 * x] = fmaf(a, tab[w[e] >> (8 * x + 4) & 15], acc[2 * x]);
-          acc[2 * x + 1] = fmaf(a, tab[w[e] >> (8 * x) & 15], acc[2 * x + 1]);
+          for (int x = 0; x < 4; ++x) {
+            acc[2 * x] = fmaf(a, tab[w[e] >> (8 * x + 4) & 15], acc[2 * x]);
+            acc[2 * x + 1] = fmaf(a, tab[w[e] >> (8 * x) & 15], acc[2 * x + 1]);
+          }
         }
       }
     }
@@ -462,56 +468,71 @@ struct EpilogueAdd : EpilogueBase {
 
 // ---------------------------------------------------------------------------
 struct LossPlan {
-  bool tiled;
-  int64_t tokens;  // taken at a time
+  bool tiled, mixed;
+  int64_t tokens, Kp;  // taken at a time; K up to a multiple of 64
   int piece, parts, split;
-  size_t logits, m, s, f, lt, tail, P, D, add, back, segments, carry, live, list, count, W, Wt, total;
+  size_t x, logits, m, s, f, lt, tail, P, D, add, back, segments, carry, live, list, count, W, Wt, total;
 };
 
 static LossPlan loss_plan(int64_t T, int64_t V, int64_t K, int log2bs, int k, bool grad) {
   LossPlan p{};
   Carver c;
-  // both sides, us with the gradient by the tile product / by gemm_4bit's kernels: 256 tokens x 128256 x 4096
-  // 1488 / 848, 448 tokens 1663 / 1584, 512 tokens 1680 / 1665, and the latter grows with every token
-  p.tiled = T >= kTiledFrom && K % 64 == 0 && K <= 65536;
+  // The tile product from many tokens on: both sides, us with the gradient, by it / by gemm_4bit's kernels: 256 tokens
+  // x 128256 x 4096 1488 / 848, 448 tokens 1663 / 1584, 512 tokens 1680 / 1665, and the latter grows with every
+  // token.  Fewer tokens where the backward has no kernel that divides the sum: gemm_4bit's logits, and D by the
+  // tile product: 1 token x 29158 x 640 ONETOKEN / 404, 223 tokens x 56425 x 1152 TWOTOKENS / 832.
+  p.tiled = K <= 65536 && T >= kTiledFrom;
+  p.mixed = K <= 65536 && !p.tiled && grad && !fast_backward(64, K, log2bs);
   const int64_t turns = (T + kTokens - 1) / kTokens;
   p.tokens = (T + turns - 1) / turns;
   const size_t n = (size_t)p.tokens;
+  // few tiles of D: the piece's terms in parts, each with a D of its own
+  auto d_parts = [&]() {
+    const int64_t tiles = ((p.tokens + kTileM - 1) / kTileM) * ((K + kTileN - 1) / kTileN);
+    p.parts = (int)(tiles >= 256 ? 1 : 256 / tiles);
+    if (p.parts > p.piece / 1024) p.parts = p.piece / 1024 > 0 ? p.piece / 1024 : 1;
+    p.split = (int)to64((p.piece + p.parts - 1) / p.parts);
+    p.parts = (int)((to64(p.piece) + p.split - 1) / p.split);
+  };
   p.m = c.take(n * 4), p.s = c.take(n * 4), p.f = c.take(n * 4), p.lt = c.take(n * k * 4);
   if (p.tiled) {
-    // 512 tiles of logits or more; few tiles of D: the piece's terms in parts, each with a D of its own
+    // 512 tiles of logits or more
     const int64_t rows = (p.tokens + kTileM - 1) / kTileM;
     p.piece = rows >= 8 ? 16384 : kMostPiece;
     while (p.piece > 8192 && p.piece / 2 >= V) p.piece /= 2;
-    const int64_t tiles = rows * ((K + kTileN - 1) / kTileN);
-    p.parts = (int)(tiles >= 256 ? 1 : 256 / tiles);
-    if (p.parts > p.piece / 1024) p.parts = p.piece / 1024;
-    p.split = (p.piece / p.parts + 63) & ~63;
-    p.parts = (p.piece + p.split - 1) / p.split;
+    d_parts();
+    p.Kp = to64(K);
+    if (p.Kp != K) p.x = c.take(n * p.Kp * 2);
     p.logits = c.take(n * p.piece * 4);
     p.live = c.take(n * 4), p.list = c.take(n * 4), p.count = c.take(4);
-    p.W = c.take((size_t)p.piece * K * 2);
+    p.W = c.take((size_t)p.piece * p.Kp * 2);
     if (grad) {
-      p.Wt = c.take((size_t)p.piece * K * 2);
-      p.P = c.take(n * p.piece * 2);
+      p.Wt = c.take((size_t)to64(p.piece) * K * 2);
+      p.P = c.take(n * to64(p.piece) * 2);
       p.D = c.take(n * K * 4 * p.parts);
     }
   } else {
     p.parts = 1;
     int64_t piece = (kLogits / p.tokens) & ~(int64_t)4095;  // rows_of wants 4096 rows
     if (piece < 4096) piece = 4096;
+    if (p.mixed && piece > kMostPiece) piece = kMostPiece;
     p.piece = (int)(V < piece ? V : piece);
+    if (p.mixed) d_parts();
     p.logits = c.take(n * p.piece * 4 * (skinny_fits(p.tokens, K, log2bs) ? skinny_parts(K) : 1));
     p.segments = c.take(n * ((p.piece + kSegment - 1) / kSegment) * 8);
     p.carry = c.take(n * 16);
     if (grad) {
+      p.P = c.take(n * to64(p.piece) * 2);
+      p.D = c.take(n * K * 4 * p.parts);
+    }
+    if (p.mixed) {
+      p.Wt = c.take((size_t)to64(p.piece) * K * 2);
+    } else if (grad) {
       p.tail = c.take(n * kTail * 4);
-      p.P = c.take(n * p.piece * 2);
-      p.D = c.take(n * K * 4);
       if (p.piece < V) p.add = c.take(n * K * 4);
       size_t most = 0;  // the product's own workspace, over all sizes that come up
       for (int64_t m : {p.tokens, T % p.tokens})
-        for (int64_t v : {(int64_t)p.piece & ~31ll, (V % p.piece) & ~31ll})
+        for (int64_t v : {(int64_t)p.piece & ~63ll, (V % p.piece) & ~63ll})
           if (m > 0 && v > 0) {
             const size_t b = gemm_backward_workspace_bytes(m, v, K, log2bs);
             most = b > most ? b : most;
@@ -527,6 +548,17 @@ size_t loss_workspace(int64_t T, int64_t V, int64_t K, int log2bs, int k, bool g
   return loss_plan(T, V, K, log2bs, k, grad).total;
 }
 
+// D = D f + P Wt^T, in the plan's parts
+template <int DT>
+static void add_to_D(const LossPlan &p, const uint16_t *P, int np, const uint16_t *Wt, int64_t m, int64_t K,
+                     const int32_t *count, const float *f, float *D, bool first, hipStream_t st) {
+  TileArgs b = tile_args(P, np, Wt, np, m, K, np);
+  b.count = count, b.split = p.split;
+  EpilogueAdd add;
+  add.C = D, add.f = f, add.ld = K, add.part = p.tokens * K, add.first = first;
+  hipLaunchKernelGGL((tile_kernel<DT, EpilogueAdd>), dim3(b.ncol * b.nrow, p.parts), dim3(256), 0, st, b, add);
+}
+
 // m tokens by the tile product; what is left for loss_finish_kernel is in rs and D
 template <int DT>
 static hipError_t pieces_tiled(const LossPlan &p, const uint16_t *x, int64_t m, const Weight4 &w, const Targets &tg,
@@ -540,12 +572,18 @@ static hipError_t pieces_tiled(const LossPlan &p, const uint16_t *x, int64_t m, 
   hipLaunchKernelGGL(loss_live_kernel, dim3((unsigned)((m + 3) / 4)), dim3(256), 0, st, ids, teacher, tg.teacher_dt, tg.k,
                      w.N, (int)m, live);
   hipLaunchKernelGGL(loss_order_kernel, dim3(1), dim3(1024), 0, st, live, (int)m, list, count);
+  if (p.Kp != w.K) {
+    uint16_t *padded = reinterpret_cast<uint16_t *>(ws + p.x);
+    const hipError_t e = launch_pad_rows(x, m, w.K, p.Kp, padded, st);
+    if (e != hipSuccess) return e;
+    x = padded;
+  }
   for (int64_t v = 0; v < w.N; v += p.piece) {
     const int n = (int)(w.N - v < p.piece ? w.N - v : p.piece), np = (n + 63) & ~63;
-    const hipError_t e = grad ? launch_decode_piece(rows_of(w, v, n), DT, 0, w.K, W, w.K, Wt, np, st)
-                              : launch_decode_rows(rows_of(w, v, n), DT, W, st);
+    const hipError_t e = grad ? launch_decode_piece(rows_of(w, v, n), DT, 0, w.K, W, p.Kp, Wt, np, st)
+                              : launch_decode_rows(rows_of(w, v, n), DT, W, p.Kp, st);
     if (e != hipSuccess) return e;
-    TileArgs a = tile_args(x, w.K, W, w.K, m, n, w.K);
+    TileArgs a = tile_args(x, p.Kp, W, p.Kp, m, n, p.Kp);
     a.rows = list, a.count = count;
     EpilogueF32 keep;
     keep.C = logits, keep.ld = p.piece;
@@ -558,11 +596,7 @@ static hipError_t pieces_tiled(const LossPlan &p, const uint16_t *x, int64_t m, 
     }
     hipLaunchKernelGGL((loss_rows_kernel<DT, true>), dim3((unsigned)m), dim3(threads), 0, st, logits, (int64_t)p.piece, v,
                        n, np, ids, tg.k, tg.inv_tau, v == 0, rs, list, count, P);
-    TileArgs b = tile_args(P, np, Wt, np, m, w.K, np);
-    b.count = count, b.split = p.split;
-    EpilogueAdd add;
-    add.C = D, add.f = rs.f, add.ld = w.K, add.part = p.tokens * w.K, add.first = v == 0;
-    hipLaunchKernelGGL((tile_kernel<DT, EpilogueAdd>), dim3(b.ncol * b.nrow, p.parts), dim3(256), 0, st, b, add);
+    add_to_D<DT>(p, P, np, Wt, m, w.K, count, rs.f, D, v == 0, st);
   }
   return hipGetLastError();
 }
@@ -577,7 +611,8 @@ static hipError_t pieces_plain(const LossPlan &p, const uint16_t *x, int64_t m, 
   float2 *segments = reinterpret_cast<float2 *>(ws + p.segments), *carry = reinterpret_cast<float2 *>(ws + p.carry);
   int turn = 0;
   for (int64_t v = 0; v < w.N; v += p.piece, turn ^= 1) {
-    const int n = (int)(w.N - v < p.piece ? w.N - v : p.piece), np = n & ~31, n_segments = (n + kSegment - 1) / kSegment;
+    const int n = (int)(w.N - v < p.piece ? w.N - v : p.piece);
+    const int np = p.mixed ? (int)to64(n) : n & ~63, n_segments = (n + kSegment - 1) / kSegment;
     const Weight4 c = rows_of(w, v, n);
     const bool skinny = skinny_fits(m, w.K, w.log2bs);
     hipError_t e = skinny ? launch_skinny(x, DT, m, c, logits, st)
@@ -596,6 +631,13 @@ static hipError_t pieces_plain(const LossPlan &p, const uint16_t *x, int64_t m, 
     }
     hipLaunchKernelGGL((loss_merge_kernel<DT, true>), dim3(n_segments, (unsigned)m), dim3(256), 0, st, logits, v, n, np, ids,
                        tg.k, tg.inv_tau, v == 0, segments, n_segments, before, after, rs, P);
+    if (p.mixed) {
+      uint16_t *Wt = reinterpret_cast<uint16_t *>(ws + p.Wt);
+      e = launch_decode_piece(c, DT, 0, w.K, nullptr, 0, Wt, np, st);
+      if (e != hipSuccess) return e;
+      add_to_D<DT>(p, P, np, Wt, m, w.K, nullptr, rs.f, D, v == 0, st);
+      continue;
+    }
     if (np) {
       e = launch_gemm_4bit_backward(P, DT, m, np, w.K, c.packed, c.sc, c.dq, c.log2bs, c.qt, v == 0 ? D : add, kF32,
                                     ws + p.back, st);

@@ -242,8 +242,8 @@ struct EpilogueBase {
 struct EpilogueF32 : EpilogueBase {
   static constexpr bool kPlain = true;
   float *C;
-  int64_t ld;
-  __device__ __forceinline__ float *row(int m) const { return C + m * ld; }
+  int64_t ld, part = 0;  // the sums' parts along the grid's y
+  __device__ __forceinline__ float *row(int m) const { return C + blockIdx.y * part + m * ld; }
   __device__ __forceinline__ void store(float *, int, float) const {}
 };
 

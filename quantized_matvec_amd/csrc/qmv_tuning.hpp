@@ -30,16 +30,23 @@ inline Weight4 rows_of(const Weight4 &w, int64_t first, int64_t n) {
   return r;
 }
 
-// Rows of a weight and its columns [c0, c0 + cols) as 16-bit values W [N, cols] and
-// their transpose Wt [cols, N], either NULL; ldt reaches over N up to a multiple of
-// 64, whose last columns of Wt become zeros.
+// Rows of a weight and its columns [c0, c0 + cols) as 16-bit values W [N, ldw] and
+// their transpose Wt [cols, ldt], either NULL; ldw and ldt reach over cols and N up to
+// a multiple of 64, with zeros.
 hipError_t launch_decode_piece(const Weight4 &w, int dt, int64_t c0, int64_t cols, void *W, int64_t ldw, void *Wt,
                                int64_t ldt, hipStream_t st);
+hipError_t launch_pad_rows(const void *in, int64_t T, int64_t L, int64_t Lp, void *out, hipStream_t st);
 
-// All of W alone: dequantize_4bit's kernel.
-inline hipError_t launch_decode_rows(const Weight4 &w, int dt, void *W, hipStream_t st) {
+// All of W alone: dequantize_4bit's kernel, where no zeros are needed.
+inline hipError_t launch_decode_rows(const Weight4 &w, int dt, void *W, int64_t ldw, hipStream_t st) {
+  if (ldw != w.K) return launch_decode_piece(w, dt, 0, w.K, W, ldw, nullptr, 0, st);
   return launch_dequantize_4bit(w.packed, w.sc, w.dq, w.N * w.K, w.log2bs, w.qt, W, dt, st);
 }
+
+inline int64_t to64(int64_t v) { return (v + 63) & ~(int64_t)63; }
+
+// Whether gemm_4bit_backward takes its fast kernel, which divides the sum among workgroups.
+inline bool fast_backward(int64_t N, int64_t K, int log2bs) { return N % 64 == 0 && K % 256 == 0 && log2bs >= 6; }
 
 // Up to 64 rows times a weight, in fp32, in parts [skinny_parts][M][N] that the caller adds up.
 bool skinny_fits(int64_t M, int64_t K, int log2bs);
