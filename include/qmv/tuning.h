@@ -12,8 +12,13 @@
  * targets, a teacher's rows) is checked by the kernels: a value out of range
  * never reaches memory, and what it means is stated at each call.  Nothing is
  * summed by atomics: results repeat bit for bit.  Inputs must be finite; one
- * that is not spoils its own token's outputs (and the gradients that are sums
- * over tokens), no other token's.
+ * that is not spoils its own token's outputs (and its adapter's gradients), no
+ * other token's.  Outputs must not overlap inputs, the workspace or each other.
+ *
+ * Sizes: T below 2^30, columns below 2^22, rows below 2^31 (with adapters 2^22),
+ * else QMV_ERR_UNSUPPORTED.  A workspace may hold anything, is 16-byte aligned
+ * and as large as its size query says for the call's sizes (QMV_ERR_WORKSPACE);
+ * calls that overlap must not share one.
  */
 #ifndef QMV_TUNING_H
 #define QMV_TUNING_H
@@ -42,7 +47,7 @@ typedef struct {
  *   down   [count, rank, K] device, of the activations' type
  *   up     [count, N, rank] device, of the activations' type
  *   scale  [count] device fp32
- *   count  1 .. 4096;  rank  a multiple of 8 in [8, 128], else QMV_ERR_UNSUPPORTED
+ *   count  1 .. 4096, else QMV_ERR_UNSUPPORTED;  rank  a multiple of 8 in [8, 128], else QMV_ERR_UNSUPPORTED
  */
 typedef struct {
   const void *down;
@@ -56,16 +61,16 @@ typedef struct {
  * lora_4bit: with a = index[t],
  *   y[t] = W_hat x[t] + bias + up[a] (scale[a] down[a] x[t]),
  * rounded once to y_dtype; a token whose index is outside [0, count) has no
- * adapter.  The projection's operands are those of qmv_gemm_4bit; the
- * adapter's term is computed from its operands as they are, with sums in fp32
- * and the rank's values carried in two 16-bit terms (relative error 2^-16 for
- * bf16, 2^-21 for fp16, below which they are fp16's subnormals).
+ * adapter.  The projection's operands are those of qmv_gemv_4bit and
+ * qmv_gemm_4bit; the adapter's part is computed from its operands as they are, with
+ * sums in fp32.  For more than 64 tokens the inner values, scale[a] down[a] x[t], are
+ * carried into the second product as two 16-bit terms: off by 2^-16 of themselves
+ * for bf16, 2^-22 for fp16, where they have to be below 65520 and what is below
+ * 2^-25 is lost.
  *   x      [T, K] device, dtype bf16 or fp16 (fp32: QMV_ERR_UNSUPPORTED)
  *   index  [T] device int32, 4-byte aligned
  *   bias   NULL or [N] in dtype
  *   y      [T, N] device, y_dtype: dtype or fp32
- *   workspace  qmv_lora_4bit_workspace bytes, any contents, 16-byte aligned;
- *          calls that overlap must not share one
  */
 size_t qmv_lora_4bit_workspace(int64_t T, int64_t N, int64_t K, int32_t blocksize, int32_t count,
                                int32_t rank);
@@ -98,8 +103,8 @@ int qmv_lora_4bit_backward(const void *dy, const void *x, qmv_dtype dtype, int64
  * and, where dloss is given, the gradient of sum_t dloss[t] loss[t]:
  *   dx[t] = dloss[t] (sum_v softmax(l)_v W_hat[v] - W_hat[target[t]]).
  * A token whose target is outside [0, V) does not count: its loss is 0, its
- * row of dx is zeros.  The vocabulary is taken in pieces; at no time are there
- * more than a few thousand columns of logits (fewer tokens: more columns).
+ * row of dx is zeros.  The vocabulary is taken in pieces, and tokens 4096 at a
+ * time: at no time are there more than 2^26 logits.
  *   x       [T, K] device, dtype bf16 or fp16 (fp32: QMV_ERR_UNSUPPORTED)
  *   target  [T] device int64, 8-byte aligned
  *   dloss   NULL or [T] device fp32;  dx  NULL or [T, K] device, dtype: both or neither
@@ -107,7 +112,6 @@ int qmv_lora_4bit_backward(const void *dy, const void *x, qmv_dtype dtype, int64
  * Products are those of qmv_gemm_4bit and qmv_gemm_4bit_backward (weights
  * rounded to dtype, sums in fp32); maxima, sums and the target's part of the
  * gradient are fp32, exp(l - max) is rounded to dtype for the second product.
- *   w->rows below 2^31, w->cols below 2^22, T below 2^30 (here and above), else QMV_ERR_UNSUPPORTED
  */
 size_t qmv_cross_entropy_4bit_workspace(int64_t T, int64_t V, int64_t K, int32_t blocksize, int32_t grad);
 int qmv_cross_entropy_4bit(const void *x, qmv_dtype dtype, int64_t T, const qmv_weight_4bit *w,

@@ -623,7 +623,7 @@ __global__ __launch_bounds__(256) void lora_join_kernel(const float *__restrict_
 constexpr int64_t kFew = 64;        // tokens up to which a token is a workgroup's
 constexpr int64_t kTiledFrom = 640, kTiledTiles = 144;  // tokens and tiles from which the tile product is used
 constexpr int64_t kRows = 4096;     // tokens of a fp32 projection in the workspace
-constexpr int64_t kTiledRows = 16384;
+constexpr int64_t kTiledRows = 8192;  // by order: offsets of 8192 rows of 65536 fit 31 bits
 constexpr int64_t kDecoded = (int64_t)1 << 27;  // elements of a decoded piece, about
 
 static int few_pieces(int64_t width) { return (int)((width + kPiece - 1) / kPiece); }

@@ -245,41 +245,40 @@ __global__ __launch_bounds__(256) void loss_finish_kernel(const int64_t *__restr
     z[tid] = !there ? -INFINITY : teacher ? teacher_logit(teacher, teacher_dt, t * k + tid) * inv_tau : 0.f;
   }
   __syncthreads();
-  float zm = -INFINITY, zs = 0.f;
-  bool live = false;
-  for (int j = 0; j < k; ++j) {
-    zm = fmaxf(zm, z[j]);
-    live |= !(z[j] == -INFINITY);  // a NaN counts, and p is NaN then
-  }
-  if (!live) {
+  const auto most = [](float a, float b) { return fmaxf(a, b); };
+  const auto both = [](float a, float b) { return a + b; };
+  const float mz = tid < k ? z[tid] : -INFINITY;
+  if (!__syncthreads_or(!(mz == -INFINITY))) {  // no entry (a NaN counts, and p is NaN then)
     if (tid == 0) store_elem<LDT>(loss, t, 0.f);
     if (dx)
       for (int64_t c = tid; c < K; c += 256) dx[t * K + c] = 0;
     return;
   }
-  if (tid < k) lt[tid] = there ? rs.lt[i * k + tid] : -INFINITY;
-  for (int j = 0; j < k; ++j) zs += expf(z[j] - zm);
+  const float ml = there ? rs.lt[i * k + tid] : -INFINITY;
+  const float zm = block_reduce(wave_max(mz), buf, most);
+  const float ez = tid < k ? expf(mz - zm) : 0.f;
+  const float zs = block_reduce(wave_sum(ez), buf, both);
   if (tid < k) {
-    p[tid] = expf(z[tid] - zm) / zs;
+    lt[tid] = ml;
+    p[tid] = ez / zs;
     own = there;
-    for (int j = 0; j < tid; ++j) own = own && id[j] != id[tid];
+#pragma unroll 8
+    for (int j = 0; j < tid; ++j) own &= id[j] != id[tid];
   }
-  __syncthreads();
   // the loss
   const float m = rs.m[i];
-  float M = m;
-  for (int j = 0; j < k; ++j) M = fmaxf(M, lt[j]);
+  const float M = fmaxf(m, block_reduce(wave_max(ml), buf, most));
   const float rest = rs.s[i] * (m == -INFINITY ? 0.f : expf(m - M));
-  const float mine = own ? expf(lt[tid] - M) : 0.f;
-  const float targets = block_reduce(wave_sum(mine), buf, [](float a, float b) { return a + b; });
+  const float mine = own ? expf(ml - M) : 0.f;
+  const float targets = block_reduce(wave_sum(mine), buf, both);
   const float Z = rest + targets;
   if (!teacher) {
     // (M - l) + log Z; where the target is the largest that is log(1 + rest)
     if (tid == 0) store_elem<LDT>(loss, t, lt[0] == M ? log1pf(rest) : (M - lt[0]) + logf(Z));
   } else {
     float part = 0.f;
-    if (tid < k && p[tid] != 0.f) part = p[tid] * ((z[tid] - zm - logf(zs)) - (lt[tid] - M) + logf(Z));
-    part = block_reduce(wave_sum(part), buf, [](float a, float b) { return a + b; });
+    if (tid < k && p[tid] != 0.f) part = p[tid] * ((mz - zm - logf(zs)) - (ml - M) + logf(Z));
+    part = block_reduce(wave_sum(part), buf, both);
     if (tid == 0) store_elem<LDT>(loss, t, part);
   }
   if (!dx) return;
@@ -290,6 +289,7 @@ __global__ __launch_bounds__(256) void loss_finish_kernel(const int64_t *__restr
     float c = 0.f;
     if (own) {
       float pj = 0.f, others_p = 0.f, others_q = rest;
+#pragma unroll 4
       for (int j = 0; j < k; ++j) {
         const bool same = id[j] == id[tid];
         pj += same ? p[j] : 0.f;
@@ -327,16 +327,16 @@ __global__ __launch_bounds__(256) void loss_finish_kernel(const int64_t *__restr
 #pragma unroll
       for (int e = 0; e < 8; ++e) acc[e] *= scale;
     }
-    const int log2sub = log2bs < 11 ? log2bs : 11, subs = 2048 >> log2sub;  // blocks in the columns
+    const int log2sub = log2bs < 11 ? log2bs : 11, log2n = 11 - log2sub;  // blocks in the columns: 2^log2n
     for (int j0 = 0; j0 < entries; j0 += 64) {
       const int some = min(entries - j0, 64);
       __syncthreads();
 #pragma unroll 4
-      for (int b = tid; b < some * subs; b += 256) {
-        const int j = j0 + b / subs;
-        const int64_t col = base + ((int64_t)(b % subs) << log2sub);
+      for (int b = tid; b < some << log2n; b += 256) {
+        const int at = b & ((1 << log2n) - 1), j = j0 + (b >> log2n);
+        const int64_t col = base + ((int64_t)at << log2sub);
         const float cj = coef[j];
-        by_block[b / subs][b % subs] =
+        by_block[b >> log2n][at] =
             cj == 0.f || col >= K ? 0.f : cj * block_scale<DQ>(sc, (id[j] * K + col) >> log2bs, offset);
       }
       __syncthreads();
@@ -480,7 +480,7 @@ static LossPlan loss_plan(int64_t T, int64_t V, int64_t K, int log2bs, int k, bo
   // The tile product from many tokens on: both sides, us with the gradient, by it / by gemm_4bit's kernels: 256 tokens
   // x 128256 x 4096 1488 / 848, 448 tokens 1663 / 1584, 512 tokens 1680 / 1665, and the latter grows with every
   // token.  Fewer tokens where the backward has no kernel that divides the sum: gemm_4bit's logits, and D by the
-  // tile product: 1 token x 29158 x 640 ONETOKEN / 404, 223 tokens x 56425 x 1152 TWOTOKENS / 832.
+  // tile product: 1 token x 29158 x 640 87 / 404, 223 tokens x 56425 x 1152 263 / 832.
   p.tiled = K <= 65536 && T >= kTiledFrom;
   p.mixed = K <= 65536 && !p.tiled && grad && !fast_backward(64, K, log2bs);
   const int64_t turns = (T + kTokens - 1) / kTokens;

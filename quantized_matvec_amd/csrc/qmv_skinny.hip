@@ -151,7 +151,7 @@ int skinny_parts(int64_t K) {
 }
 
 // Both sides, us without the adding up of parts / gemm_4bit: 14336 x 4096, 16 rows 19.1 / 18.2, 17 rows 19.5 / 21.1,
-// 32 rows 20.2 / 26.4, 64 rows SIXTYFOUR / 44.9; 128256 x 4096, 16 rows 109 / 120, 32 rows 119 / 182
+// 32 rows 20.2 / 26.4, 64 rows 25.7 / 44.9; 128256 x 4096, 16 rows 109 / 120, 32 rows 119 / 182
 bool skinny_fits(int64_t M, int64_t K, int log2bs) {
   return M > 16 && M <= 64 && K % 64 == 0 && log2bs >= 6 && skinny_parts(K) <= 16;
 }

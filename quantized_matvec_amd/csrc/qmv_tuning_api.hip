@@ -49,6 +49,9 @@ int check_rank(int32_t count, int32_t rank) {
   return count > 4096 || rank % 8 || rank > 128 ? QMV_ERR_UNSUPPORTED : QMV_OK;
 }
 
+// the adapters' kernels have a grid dimension along the outputs
+bool wide(int64_t N) { return N >= (1 << 22); }
+
 int check_lora(const qmv_lora *l, Lora *out) {
   if (!l || !l->down || !l->up || !l->scale) return QMV_ERR_INVALID_ARG;
   const int rc = check_rank(l->count, l->rank);
@@ -90,7 +93,7 @@ int loss(const void *x, int dtype, int64_t T, const qmv_weight_4bit *w, const Ta
 extern "C" {
 
 size_t qmv_lora_4bit_workspace(int64_t T, int64_t N, int64_t K, int32_t blocksize, int32_t count, int32_t rank) {
-  if (check_sizes(T, N, K, blocksize) != QMV_OK || check_rank(count, rank) != QMV_OK) return 0;
+  if (check_sizes(T, N, K, blocksize) != QMV_OK || check_rank(count, rank) != QMV_OK || wide(N)) return 0;
   return lora_workspace(T, N, K, log2_exact(blocksize), count, rank, false);
 }
 
@@ -103,6 +106,7 @@ int qmv_lora_4bit(const void *x, qmv_dtype dtype, int64_t T, const qmv_weight_4b
   Weight4 wt;
   Lora l;
   if ((rc = check_weight(w, T, &wt)) != QMV_OK || (rc = check_lora(lora, &l)) != QMV_OK) return rc;
+  if (wide(wt.N)) return QMV_ERR_UNSUPPORTED;
   if (!aligned(x, 16) || !aligned(y, 16) || !aligned(index, 4) || !aligned(bias, 2)) return QMV_ERR_ALIGNMENT;
   rc = check_workspace(workspace, workspace_bytes, lora_workspace(T, wt.N, wt.K, wt.log2bs, l.count, l.rank, false));
   if (rc != QMV_OK) return rc;
@@ -112,7 +116,7 @@ int qmv_lora_4bit(const void *x, qmv_dtype dtype, int64_t T, const qmv_weight_4b
 
 size_t qmv_lora_4bit_backward_workspace(int64_t T, int64_t N, int64_t K, int32_t blocksize, int32_t count,
                                         int32_t rank) {
-  if (check_sizes(T, N, K, blocksize) != QMV_OK || check_rank(count, rank) != QMV_OK || N % 32) return 0;
+  if (check_sizes(T, N, K, blocksize) != QMV_OK || check_rank(count, rank) != QMV_OK || wide(N) || N % 32) return 0;
   return lora_workspace(T, N, K, log2_exact(blocksize), count, rank, true);
 }
 
@@ -125,7 +129,7 @@ int qmv_lora_4bit_backward(const void *dy, const void *x, qmv_dtype dtype, int64
   Weight4 wt;
   Lora l;
   if ((rc = check_weight(w, T, &wt)) != QMV_OK || (rc = check_lora(lora, &l)) != QMV_OK) return rc;
-  if (wt.N % 32) return QMV_ERR_UNSUPPORTED;
+  if (wt.N % 32 || wide(wt.N)) return QMV_ERR_UNSUPPORTED;
   if (!aligned(dy, 16) || !aligned(x, 16) || !aligned(dx, 16) || !aligned(d_down, 16) || !aligned(d_up, 16) ||
       !aligned(index, 4))
     return QMV_ERR_ALIGNMENT;

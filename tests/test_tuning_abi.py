@@ -52,7 +52,7 @@ WEIGHT_FAULTS = [(dict(packed=0), INVALID), (dict(absmax=0), INVALID), (dict(row
                  (dict(absmax=P + 4), ALIGN), (dict(dq=(P, P, P, P, P, 256)), INVALID), (dict(dq=(None, P, P, P, None, 256)), INVALID),
                  (dict(dq=(None, P, P, P, P, 100)), UNSUPPORTED), (dict(dq=(None, P + 1, P, P, P, 256)), ALIGN)]
 LORA_FAULTS = [(dict(down=0), INVALID), (dict(up=0), INVALID), (dict(scale=0), INVALID), (dict(count=0), INVALID), (dict(rank=0), INVALID),
-               (dict(rank=-8), INVALID), (dict(rank=12), UNSUPPORTED), (dict(rank=136), UNSUPPORTED), (dict(count=65536), UNSUPPORTED),
+               (dict(rank=-8), INVALID), (dict(rank=12), UNSUPPORTED), (dict(rank=136), UNSUPPORTED), (dict(count=4097), UNSUPPORTED),
                (dict(down=P + 2), ALIGN), (dict(up=P + 8), ALIGN), (dict(scale=P + 2), ALIGN)]
 
 
@@ -75,6 +75,7 @@ def test_lora_preconditions(lib):
     assert forward(ydt=F16) == UNSUPPORTED and forward(ydt=9) == INVALID
     for name in ("dy", "dx", "dd", "du"):
         assert backward(**{name: None}) == INVALID and backward(**{name: P + 8}) == ALIGN, name
+    assert forward(w=weight(rows=1 << 22)) == UNSUPPORTED and backward(w=weight(rows=1 << 22)) == UNSUPPORTED
     assert backward(gdt=F16) == UNSUPPORTED and backward(w=weight(rows=257)) == UNSUPPORTED
     assert lib.qmv_lora_4bit(P, BF16, 10, None, ref(lora()), P, None, P, BF16, P, BIG, None) == INVALID
     assert lib.qmv_lora_4bit(P, BF16, 10, ref(weight()), None, P, None, P, BF16, P, BIG, None) == INVALID
