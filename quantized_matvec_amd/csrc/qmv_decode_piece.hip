@@ -99,4 +99,23 @@ hipError_t launch_pad_rows(const void *in, int64_t T, int64_t L, int64_t Lp, voi
   return hipGetLastError();
 }
 
+__global__ __launch_bounds__(256) void sum_parts_kernel(float *__restrict__ sums, int parts, int64_t n) {
+  const int64_t i = (int64_t)blockIdx.x * 1024 + threadIdx.x;
+  float sum[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) sum[q] = i + 256 * q < n ? sums[i + 256 * q] : 0.f;
+#pragma unroll 4
+  for (int s = 1; s < parts; ++s)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) sum[q] += sums[s * n + min(i + 256 * q, n - 1)];
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    if (i + 256 * q < n) sums[i + 256 * q] = sum[q];
+}
+
+hipError_t launch_sum_parts(float *sums, int parts, int64_t n, hipStream_t st) {
+  hipLaunchKernelGGL(sum_parts_kernel, dim3((unsigned)((n + 1023) / 1024)), dim3(256), 0, st, sums, parts, n);
+  return hipGetLastError();
+}
+
 }  // namespace qmv

@@ -425,10 +425,9 @@ __device__ __forceinline__ void add_low_rank(tile_acc_t (&acc)[MI][NJ], const Lo
 }
 
 // out[t][c] = round(base[t][c] + bias[c] + the adapter's part): a unit and 128 columns
-// a workgroup, 32 columns a wave; base (in parts, added up in order) is asked for first.  Bound by base and out.
+// a workgroup, 32 columns a wave; base's loads go out first.  Bound by base and out.
 template <int DT, int ODT, bool TRANS>
-__global__ __launch_bounds__(256, 2) void lora_expand_kernel(const float *__restrict__ base, int base_parts,
-                                                             int64_t part, LowRank lr, Places pl,
+__global__ __launch_bounds__(256, 2) void lora_expand_kernel(const float *__restrict__ base, LowRank lr, Places pl,
                                                           const uint16_t *__restrict__ bias,
                                                           typename Storage<ODT>::type *__restrict__ out) {
   if ((int)blockIdx.x >= *pl.n_units) return;
@@ -445,11 +444,6 @@ __global__ __launch_bounds__(256, 2) void lora_expand_kernel(const float *__rest
       token[i][r] = pl.order[min(unit.y + 32 * i + 8 * (r >> 2) + 4 * h + (r & 3), unit.z - 1)];
       old[i][r] = base[token[i][r] * lr.width + cin];
     }
-  for (int s = 1; s < base_parts; ++s)
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) old[i][r] += base[s * part + token[i][r] * lr.width + cin];
   const float more = bias ? bits16_to_f32<DT>(bias[cin]) : 0.f;
   tile_acc_t acc[2][1];
 #pragma unroll
@@ -687,7 +681,7 @@ static ProductPlan product_plan(Carver &c, int64_t T, int64_t N, int64_t K, int 
   const int64_t tiles = ((T + kTileM - 1) / kTileM) * ((width + kTileN - 1) / kTileN);
   const bool can = L <= 65536 && width <= ((int64_t)1 << 30);
   p.tiled = can && T >= kTiledFrom && tiles >= kTiledTiles;
-  const bool parts = can && !p.tiled && backward && T >= kTiledFrom && !fast_backward(N, K, log2bs);
+  const bool parts = can && !p.tiled && backward && !fast_backward(T, N, K, log2bs);
   const int64_t most = p.tiled ? kTiledRows : kRows, turns = (T + most - 1) / most;
   p.tokens = (T + turns - 1) / turns;
   p.Lp = to64(L);
@@ -699,8 +693,6 @@ static ProductPlan product_plan(Carver &c, int64_t T, int64_t N, int64_t K, int 
     if (p.Lp != L) p.x = c.take((size_t)p.tokens * p.Lp * 2);
   }
   if (parts) {
-    // gemm_4bit_backward's other kernel does not divide the sum; us of a call in parts / with it: 2111 tokens, 832 x
-    // 3712, rank 8, 90 / 122; few tokens do not pay for the decoding: 468 tokens, 8768 x 1408, rank 16, 244 / 161
     const int64_t there = ((p.tokens + kTileM - 1) / kTileM) * ((width + kTileN - 1) / kTileN);
     int64_t n = there >= 256 ? 1 : 256 / there;
     if (n > p.Lp / 256) n = p.Lp / 256 > 0 ? p.Lp / 256 : 1;
@@ -723,15 +715,16 @@ static ProductPlan product_plan(Carver &c, int64_t T, int64_t N, int64_t K, int 
   return p;
 }
 
-// Windows of the gradients: about 2048 workgroups, 128 places at least, and no more parts than
-// about 32 MB of them
-static int grad_window(int64_t T, int64_t W, int R) {
-  const int64_t tiles = (W + 127) / 128, part = W * R * 4;
+// Windows of the gradients: about 2048 workgroups, no more parts than about 32 MB of them, and 128
+// places at least; fewer where there are few tokens, whose adapters a workgroup takes one after
+// the other (43 tokens of 43 adapters, 6976 wide: 47 us in one window)
+static int grad_window(int64_t T, int64_t W, int R, int count) {
+  const int64_t tiles = (W + 127) / 128, part = W * R * 4, least = T >= 512 ? 128 : count >= 8 ? 16 : 64;
   int64_t windows = 2048 / tiles;
   if (windows > (32 << 20) / part) windows = (32 << 20) / part;
   if (windows < 4) windows = 4;
-  int64_t w = ((T + windows - 1) / windows + 63) & ~(int64_t)63;
-  if (w < 128) w = 128;
+  int64_t w = ((T + windows - 1) / windows + least - 1) / least * least;
+  if (T >= 512) w = to64(w);
   return (int)(w < T ? w : T);
 }
 
@@ -770,7 +763,7 @@ static LoraPlan lora_plan(int64_t T, int64_t N, int64_t K, int log2bs, int count
       p.v = p.inner;
     }
     p.u = inner_plan(c, T, K, R, count);
-    p.window_down = grad_window(T, K, R), p.window_up = grad_window(T, N, R);
+    p.window_down = grad_window(T, K, R, count), p.window_up = grad_window(T, N, R, count);
     const size_t a = 2 * (size_t)((T + p.window_down - 1) / p.window_down) * K * R * 4;
     const size_t b = 2 * (size_t)((T + p.window_up - 1) / p.window_up) * N * R * 4;
     p.parts = c.take(a > b ? a : b);
@@ -856,6 +849,10 @@ static hipError_t product(const LoraPlan &p, const uint16_t *x, int64_t m, const
       }
     }
     if (pp.tiled) return hipGetLastError();
+    if (pp.parts > 1) {
+      const hipError_t e = launch_sum_parts(base, pp.parts, m * width, st);
+      if (e != hipSuccess) return e;
+    }
   } else {
     const hipError_t e =
         TRANS ? launch_gemm_4bit_backward(x, DT, m, w.N, w.K, w.packed, w.sc, w.dq, w.log2bs, w.qt, base, kF32,
@@ -864,8 +861,7 @@ static hipError_t product(const LoraPlan &p, const uint16_t *x, int64_t m, const
     if (e != hipSuccess) return e;
   }
   const dim3 grid((unsigned)most_units(m, l.count), (unsigned)((width + 127) / 128));
-  hipLaunchKernelGGL((lora_expand_kernel<DT, ODT, TRANS>), grid, dim3(256), 0, st, base, pp.parts ? pp.parts : 1, m * width,
-                     lr, pl, bias, out);
+  hipLaunchKernelGGL((lora_expand_kernel<DT, ODT, TRANS>), grid, dim3(256), 0, st, base, lr, pl, bias, out);
   return hipGetLastError();
 }
 

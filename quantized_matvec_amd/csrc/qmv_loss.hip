@@ -115,21 +115,6 @@ __device__ __forceinline__ void mark_ids(uint32_t *out, const int64_t *ids, int 
   __syncthreads();
 }
 
-// Logits that came in parts, n apart: added up in order, the sum left in the first.
-__global__ __launch_bounds__(256) void loss_sum_kernel(float *__restrict__ logits, int parts, int64_t n) {
-  const int64_t i = (int64_t)blockIdx.x * 1024 + threadIdx.x;
-  float sum[4];
-#pragma unroll
-  for (int q = 0; q < 4; ++q) sum[q] = i + 256 * q < n ? logits[i + 256 * q] : 0.f;
-#pragma unroll 4
-  for (int s = 1; s < parts; ++s)
-#pragma unroll
-    for (int q = 0; q < 4; ++q) sum[q] += logits[s * n + min(i + 256 * q, n - 1)];
-#pragma unroll
-  for (int q = 0; q < 4; ++q)
-    if (i + 256 * q < n) logits[i + 256 * q] = sum[q];
-}
-
 __global__ __launch_bounds__(256) void loss_part_kernel(const float *__restrict__ logits, int64_t v0, int n,
                                                         const int64_t *__restrict__ ids, int k, float inv_tau,
                                                         float *__restrict__ lt, float2 *__restrict__ segments) {
@@ -481,10 +466,10 @@ static LossPlan loss_plan(int64_t T, int64_t V, int64_t K, int log2bs, int k, bo
   // x 128256 x 4096 1488 / 848, 448 tokens 1663 / 1584, 512 tokens 1680 / 1665, and the latter grows with every
   // token.  Fewer tokens where the backward has no kernel that divides the sum: gemm_4bit's logits, and D by the
   // tile product: 1 token x 29158 x 640 87 / 404, 223 tokens x 56425 x 1152 263 / 832.
-  p.tiled = K <= 65536 && T >= kTiledFrom;
-  p.mixed = K <= 65536 && !p.tiled && grad && !fast_backward(64, K, log2bs);
   const int64_t turns = (T + kTokens - 1) / kTokens;
   p.tokens = (T + turns - 1) / turns;
+  p.tiled = K <= 65536 && T >= kTiledFrom;
+  p.mixed = K <= 65536 && !p.tiled && grad && !fast_backward(p.tokens, V & ~(int64_t)63, K, log2bs);
   const size_t n = (size_t)p.tokens;
   // few tiles of D: the piece's terms in parts, each with a D of its own
   auto d_parts = [&]() {
@@ -619,8 +604,8 @@ static hipError_t pieces_plain(const LossPlan &p, const uint16_t *x, int64_t m, 
                           : launch_gemm_4bit(x, DT, m, n, w.K, c.packed, c.sc, c.dq, c.log2bs, c.qt, logits, kF32, nullptr, st);
     if (e != hipSuccess) return e;
     if (skinny && skinny_parts(w.K) > 1)
-      hipLaunchKernelGGL(loss_sum_kernel, dim3((unsigned)((m * n + 1023) / 1024)), dim3(256), 0, st, logits,
-                         skinny_parts(w.K), m * n);
+      e = launch_sum_parts(logits, skinny_parts(w.K), m * n, st);
+    if (e != hipSuccess) return e;
     hipLaunchKernelGGL(loss_part_kernel, dim3(n_segments, (unsigned)m), dim3(256), 0, st, logits, v, n, ids, tg.k, tg.inv_tau,
                        rs.lt, segments);
     float2 *before = carry + (turn ? p.tokens : 0), *after = carry + (turn ? 0 : p.tokens);

@@ -45,8 +45,17 @@ inline hipError_t launch_decode_rows(const Weight4 &w, int dt, void *W, int64_t 
 
 inline int64_t to64(int64_t v) { return (v + 63) & ~(int64_t)63; }
 
-// Whether gemm_4bit_backward takes its fast kernel, which divides the sum among workgroups.
-inline bool fast_backward(int64_t N, int64_t K, int log2bs) { return N % 64 == 0 && K % 256 == 0 && log2bs >= 6; }
+// Whether gemm_4bit_backward is the quickest way to M rows of [N, K] of up to some hundred rows: it has to take its
+// kernel that divides the sum among workgroups, and the last workgroup of each 128 x 256 tile then adds up all parts of
+// it, 2.1 us each.  The other way decodes the weight and multiplies that (qmv_tile.hpp), about 1 us for 2^20 weights and
+// 30 us.  19 rows of 4608 x 768: 98 us by gemm_4bit_backward, 84 of them for 72 parts.
+inline bool fast_backward(int64_t M, int64_t N, int64_t K, int log2bs) {
+  if (N % 64 || K % 256 || log2bs < 6) return false;
+  return (N * K >> 20) >= 166000 / (K * ((M + 127) / 128)) - 24;
+}
+
+// Sums that came in parts, n values apart: added up in order, the sum left in the first.
+hipError_t launch_sum_parts(float *sums, int parts, int64_t n, hipStream_t st);
 
 // Up to 64 rows times a weight, in fp32, in parts [skinny_parts][M][N] that the caller adds up.
 bool skinny_fits(int64_t M, int64_t K, int log2bs);
