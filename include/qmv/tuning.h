@@ -13,7 +13,7 @@
  * never reaches memory, and what it means is stated at each call.  Nothing is
  * summed by atomics: results repeat bit for bit.  Inputs must be finite; one
  * that is not spoils its own token's outputs (and its adapter's gradients), no
- * other token's.  Outputs must not overlap inputs, the workspace or each other.
+ * other token's; an adapter that is not, its own tokens'.  Outputs must not overlap inputs, the workspace or each other.
  *
  * Sizes: T below 2^30, columns below 2^22, rows below 2^31 (with adapters 2^22),
  * else QMV_ERR_UNSUPPORTED.  A workspace may hold anything, is 16-byte aligned

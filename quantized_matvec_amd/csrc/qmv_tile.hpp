@@ -179,7 +179,8 @@ __global__ __launch_bounds__(256, 1) void tile_kernel(TileArgs g, Epi epi) {
     if (kt + 3 < KT) step(kt + 3, u1, u2, u3, u4, u0);
     __builtin_amdgcn_s_waitcnt((7 << 4) | (15 << 8));  // no load into LDS outlives the kernel
   }
-  epi.begin(acc, g, M, m0, n0, wm, wn, lane);
+  const int mfirst = m0 + 128 * wm, mpast = mfirst + 128 < M ? mfirst + 128 : M;  // of this wave
+  const bool more = epi.begin(acc, g.N, mfirst, mpast, n0 + 128 * wn, lane);
   if constexpr (Epi::kPlain) {
     // C = sums, or C f[row] + sums, in parts of 32 x 128: bounded resources (what is not there, or
     // no rows yet, reads as 0 and is not written), so no branches, and the loads of a part are in
@@ -231,13 +232,16 @@ __global__ __launch_bounds__(256, 1) void tile_kernel(TileArgs g, Epi epi) {
   };
   if (mrows == kTileM && ncols == kTileN) store(std::true_type{});
   else store(std::false_type{});
+  if (more) epi.end(g.N, mfirst, mpast, n0 + 128 * wn, lane);
 }
 
-// What becomes of the sums: begin() may add to them, row() gives what store() needs of a row.
+// What becomes of the sums: begin() may add to them, row() gives what store() needs of a row, and end() follows
+// the stores where begin() asks for it.  Both get the tile product's columns, the wave's rows and its first column.
 struct EpilogueBase {
   static constexpr bool kPlain = false;  // into C in fp32 as they are, of rows C, ld apart (256 of them: below 2^31 bytes)
   static constexpr bool kAdds = false;   // plain, C f + sums, but for `first`
-  __device__ __forceinline__ void begin(tile_acc_t (&)[4][4], const TileArgs &, int, int, int, int, int, int) const {}
+  __device__ __forceinline__ bool begin(tile_acc_t (&)[4][4], int, int, int, int, int) const { return false; }
+  __device__ __forceinline__ void end(int, int, int, int, int) const {}
 };
 struct EpilogueF32 : EpilogueBase {
   static constexpr bool kPlain = true;

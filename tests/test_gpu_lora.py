@@ -232,6 +232,28 @@ def test_a_row_that_is_not_finite_stays_alone():
         assert torch.equal(y[rest], ref[rest]) and not torch.isfinite(y[1]).any()
 
 
+@pytest.mark.parametrize("T,N,K", [(6, 192, 320), (90, 192, 320), (300, 192, 320), (700, 12320, 64)])
+def test_an_adapter_that_is_not_finite_spoils_its_own_tokens_only(T, N, K):
+    """Its tokens share tiles with others' and with tokens that have no adapter."""
+    g = torch.Generator().manual_seed(T)
+    index = torch.randint(-1, 3, (T,), generator=g)
+    index[:3] = torch.tensor([0, 1, -1])
+    others = (index != 1).cuda()
+
+    def spoil(c):
+        down, up = c["down"].clone(), c["up"].clone()
+        down[1, 3, 5], up[1, 7, 2], up[1, 9, 4] = float("inf"), float("inf"), float("nan")
+        return dict(c, down=down, up=up, adapters=qmv.LoraAdapters(down, up, c["scale"]))
+
+    c = case(T, N, K, 3, 16, BF, index)
+    assert torch.equal(forward(spoil(c))[others], forward(c)[others])
+    c = case(T, K, N, 3, 16, BF, index, bs=32)
+    want, got = backward(c), backward(spoil(c))
+    assert torch.equal(got[0][others], want[0][others])
+    for a in (0, 2):
+        assert torch.equal(got[1][a], want[1][a]) and torch.equal(got[2][a], want[2][a])
+
+
 @pytest.mark.parametrize("T,N,K", [(5, 192, 320), (90, 192, 320), (600, 192, 320), (700, 12320, 64)])
 def test_repeats_and_graphs(T, N, K):
     """The same bits every time, in a captured graph too, whose replays follow
