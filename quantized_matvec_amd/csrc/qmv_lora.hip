@@ -3,7 +3,8 @@
 // and, with g = dy and v[t] = scale[a] up[a]^T g[t],
 //   dx[t] = W^^T g[t] + down[a]^T v[t],   d_down[a] = sum v[t] x[t]^T,   d_up[a] = sum g[t] u[t]^T.
 //
-// A few tokens: the projection in fp32 by gemv_4bit's or gemm_4bit's kernels, then
+// A few tokens: the projection in fp32 by gemv_4bit's kernels, gemm_4bit's or those of
+// qmv_skinny.hip, then
 // a workgroup for each token and part of the columns.  More: tokens are put in
 // order of their adapters, so that tiles of the matrix cores meet one adapter,
 // or few; u and v, a handful of values a token, are summed in fp32 and carried
@@ -739,7 +740,8 @@ static ProductPlan product_plan(Carver &c, int64_t T, int64_t N, int64_t K, int 
   const int64_t tiles = ((T + kTileM - 1) / kTileM) * ((width + kTileN - 1) / kTileN);
   const bool can = L <= 65536 && width <= ((int64_t)1 << 30);
   p.tiled = can && T >= kTiledFrom && tiles >= kTiledTiles;
-  const bool parts = can && !p.tiled && backward && !fast_backward(T, N, K, log2bs);
+  // the plain epilogue's offsets: 256 rows of fp32 sums in less than 2^31 bytes
+  const bool parts = can && width <= ((int64_t)1 << 20) && !p.tiled && backward && !fast_backward(T, N, K, log2bs);
   const int64_t most = p.tiled ? kTiledRows : kRows, turns = (T + most - 1) / most;
   p.tokens = (T + turns - 1) / turns;
   p.Lp = to64(L);

@@ -232,6 +232,21 @@ def test_a_row_that_is_not_finite_stays_alone():
         assert torch.equal(y[rest], ref[rest]) and not torch.isfinite(y[1]).any()
 
 
+def test_widest_backward():
+    """More columns than 256 rows of fp32 sums have room for in 2^31 bytes; the last of them."""
+    T, N, K, rank, last = 300, 32, (1 << 21) + 288, 8, 320
+    g = torch.Generator(device="cuda").manual_seed(1)
+    rnd = lambda *s: torch.randn(*s, generator=g, device="cuda").to(BF)
+    packed, state = qmv.quantize_4bit(rnd(N, K), 32, "nf4")
+    dy, x, down, up = rnd(T, N), rnd(T, K), rnd(2, rank, K), rnd(2, N, rank)
+    index = (torch.arange(T, device="cuda") % 3 - 1).int()
+    scale = torch.ones(2, device="cuda")
+    dx, _, _ = qmv.lora_4bit_backward(dy, x, packed, state, qmv.LoraAdapters(down, up, scale), index)
+    W = qmv.dequantize_4bit(packed, state, out_dtype=torch.float32)
+    for cut in (slice(0, last), slice(K - last, K)):  # the forward's formula, with the two factors in each other's place
+        R.check_lora(dx[:, cut], dy, W[:, cut].T, up.transpose(1, 2), down[..., cut].transpose(1, 2), scale, index, what="dx")
+
+
 @pytest.mark.parametrize("T,N,K", [(6, 192, 320), (90, 192, 320), (300, 192, 320), (700, 12320, 64)])
 def test_an_adapter_that_is_not_finite_spoils_its_own_tokens_only(T, N, K):
     """Its tokens share tiles with others' and with tokens that have no adapter."""
