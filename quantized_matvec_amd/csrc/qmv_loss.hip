@@ -227,7 +227,7 @@ __global__ __launch_bounds__(256) void loss_finish_kernel(const int64_t *__restr
     const int64_t v = ids[t * k + tid];
     there = v >= 0 && v < V;
     id[tid] = there ? v : -1;
-    z[tid] = !there ? -INFINITY : teacher ? teacher_logit(teacher, teacher_dt, t * k + tid) * inv_tau : 0.f;
+    z[tid] = !there ? -INFINITY : teacher ? teacher_logit(teacher, teacher_dt, t * k + tid) : 0.f;
   }
   __syncthreads();
   const auto most = [](float a, float b) { return fmaxf(a, b); };
@@ -241,7 +241,8 @@ __global__ __launch_bounds__(256) void loss_finish_kernel(const int64_t *__restr
   }
   const float ml = there ? rs.lt[i * k + tid] : -INFINITY;
   const float zm = block_reduce(wave_max(mz), buf, most);
-  const float ez = tid < k ? expf(mz - zm) : 0.f;
+  // the difference before the temperature: a type's lowest value may not be divided by it
+  const float dz = (mz - zm) * inv_tau, ez = tid < k ? expf(dz) : 0.f;
   const float zs = block_reduce(wave_sum(ez), buf, both);
   if (tid < k) {
     lt[tid] = ml;
@@ -262,7 +263,7 @@ __global__ __launch_bounds__(256) void loss_finish_kernel(const int64_t *__restr
     if (tid == 0) store_elem<LDT>(loss, t, lt[0] == M ? log1pf(rest) : (M - lt[0]) + logf(Z));
   } else {
     float part = 0.f;
-    if (tid < k && p[tid] != 0.f) part = p[tid] * ((mz - zm - logf(zs)) - (ml - M) + logf(Z));
+    if (tid < k && p[tid] != 0.f) part = p[tid] * ((dz - logf(zs)) - (ml - M) + logf(Z));
     part = block_reduce(wave_sum(part), buf, both);
     if (tid == 0) store_elem<LDT>(loss, t, part);
   }

@@ -192,6 +192,22 @@ def test_distill_rows_with_gaps(T, whole):
     assert (loss[3::8] == 0).all() and (loss[5::8] == 0).all() and (dx[3::8] == 0).all() and (dx[5::8] == 0).all()
 
 
+@pytest.mark.parametrize("T,whole", [(8, "table"), (504, True)])
+def test_distill_with_lowest_values(T, whole):
+    """fp32's lowest value as a mask: it counts beside others of its kind, and not beside larger ones, at any temperature."""
+    low = torch.finfo(F32).min
+    V, K, tau = 300, 64, 0.5
+    w = whole_weight(V, K, table=whole == "table")
+    x = rows(T, K, BF, whole=True)
+    z = torch.tensor([[low, low, low, low], [low, 1, 2, low], [low, low, low, 3], [0, low, -float("inf"), 0]] * (T // 4)).cuda()
+    ids = torch.randint(V, (T, 4), generator=torch.Generator().manual_seed(2)).cuda()
+    dl = dlosses(T)
+    loss, dx = qmv.distill_4bit(x, w[0], w[1], ids, z, tau, dl, F32)
+    # the bound takes the logits' size as that of the largest: lowest values as -inf, but where there is nothing else
+    plain = torch.where((z == low).all(1, keepdim=True), 0.0, torch.where(z == low, -float("inf"), z))
+    R.check_loss(loss, dx, x, w[2], ids, plain, tau, dl, exact(whole, T), "lowest")
+
+
 def test_distill_of_one_certain_entry_is_cross_entropy():
     T, V, K = 60, 400, 128
     packed, state, W = weight(V, K)
