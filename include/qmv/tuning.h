@@ -15,7 +15,7 @@
  * that is not spoils its own token's outputs (and its adapter's gradients), no
  * other token's; an adapter that is not, its own tokens'.  Outputs must not overlap inputs, the workspace or each other.
  *
- * Sizes: T below 2^30, columns below 2^22, rows below 2^31 (with adapters 2^22),
+ * Sizes: T below 2^30 (lora_4bit_backward: 2^22), columns below 2^22, rows below 2^31 (with adapters 2^22),
  * else QMV_ERR_UNSUPPORTED.  A workspace may hold anything, is 16-byte aligned
  * and as large as its size query says for the call's sizes (QMV_ERR_WORKSPACE);
  * calls that overlap must not share one.

@@ -51,6 +51,8 @@ int check_rank(int32_t count, int32_t rank) {
 
 // the adapters' kernels have a grid dimension along the outputs
 bool wide(int64_t N) { return N >= (1 << 22); }
+// the backward puts all tokens in order at once, and each 256 of them count all
+bool many(int64_t T) { return T >= (1 << 22); }
 
 int check_lora(const qmv_lora *l, Lora *out) {
   if (!l || !l->down || !l->up || !l->scale) return QMV_ERR_INVALID_ARG;
@@ -116,7 +118,7 @@ int qmv_lora_4bit(const void *x, qmv_dtype dtype, int64_t T, const qmv_weight_4b
 
 size_t qmv_lora_4bit_backward_workspace(int64_t T, int64_t N, int64_t K, int32_t blocksize, int32_t count,
                                         int32_t rank) {
-  if (check_sizes(T, N, K, blocksize) != QMV_OK || check_rank(count, rank) != QMV_OK || wide(N) || N % 32) return 0;
+  if (check_sizes(T, N, K, blocksize) != QMV_OK || check_rank(count, rank) != QMV_OK || wide(N) || N % 32 || many(T)) return 0;
   return lora_workspace(T, N, K, log2_exact(blocksize), count, rank, true);
 }
 
@@ -129,7 +131,7 @@ int qmv_lora_4bit_backward(const void *dy, const void *x, qmv_dtype dtype, int64
   Weight4 wt;
   Lora l;
   if ((rc = check_weight(w, T, &wt)) != QMV_OK || (rc = check_lora(lora, &l)) != QMV_OK) return rc;
-  if (wt.N % 32 || wide(wt.N)) return QMV_ERR_UNSUPPORTED;
+  if (wt.N % 32 || wide(wt.N) || many(T)) return QMV_ERR_UNSUPPORTED;
   if (!aligned(dy, 16) || !aligned(x, 16) || !aligned(dx, 16) || !aligned(d_down, 16) || !aligned(d_up, 16) ||
       !aligned(index, 4))
     return QMV_ERR_ALIGNMENT;

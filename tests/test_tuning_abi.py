@@ -128,3 +128,9 @@ def test_python_layer_refuses():
         qmv.cross_entropy_4bit(x, packed, state, torch.zeros(4, dtype=torch.int64))
     with pytest.raises(ValueError):
         qmv.distill_4bit(x, packed, state, torch.zeros(4, 2, dtype=torch.int64), torch.zeros(4, 2))
+
+
+def test_most_tokens_of_the_adapters_backward(lib):
+    for T, want in (((1 << 22) - 1, WORKSPACE), (1 << 22, UNSUPPORTED)):
+        assert lib.qmv_lora_4bit_backward(P, P, BF16, T, ref(weight()), ref(lora()), P, P, P, P, BF16, P, 16, None) == want
+        assert (lib.qmv_lora_4bit_backward_workspace(T, 256, 128, 64, 3, 16) > 0) == (want == WORKSPACE)
