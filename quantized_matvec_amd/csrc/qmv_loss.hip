@@ -105,7 +105,7 @@ __device__ __forceinline__ float block_reduce(float v, float *buf, F op) {  // 2
 // logits); loss_merge_kernel puts them together with what was before the piece
 // and, with a gradient, writes P = exp(l - m) in 16 bits, [T, np] with np the
 // multiple of 64 below n (the columns from np on go to `tail`).  Two launches,
-// but no workgroup reads more than 32 kB.
+// but no workgroup reads more than 32 kB: 17 tokens x 32000 5.9 and 2.5 us, 96 x 32003 with P 7.4 and 11.7.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ void mark_ids(uint32_t *out, const int64_t *ids, int k, int64_t v0, int n) {  // one barrier
   for (int j = threadIdx.x; j < k; j += 256) {
@@ -204,7 +204,8 @@ __global__ __launch_bounds__(256) void loss_add_kernel(float *__restrict__ D, co
   }
 }
 
-// The loss of a token, and its row of dx from D.
+// The loss of a token, and its row of dx from D: a workgroup a token.  Bound by D's read for one id (4096 tokens x 4096
+// 37 us), by the ids' rows of codes, scattered over the weight, for many (2048 tokens x 64 ids x 4096 161 us: 268 MB).
 template <int DT, int LDT, bool DQ>
 __global__ __launch_bounds__(256) void loss_finish_kernel(const int64_t *__restrict__ ids, const void *teacher,
                                                           int teacher_dt, int k, float inv_tau, int64_t V, RowState rs,
@@ -357,7 +358,8 @@ __global__ __launch_bounds__(256) void loss_finish_kernel(const int64_t *__restr
 // Many tokens: a piece's logits and D by the tile product.
 //
 // One row of a piece in the registers of a workgroup of 256, 512 or 1024 threads,
-// 32 columns each; rows are those that count, list[i] the token of row i.
+// 32 columns each; rows are those that count, list[i] the token of row i.  One read of
+// the logits: 2867 rows x 16384 59.5 us with P, 282 MB at 4.7 TB/s; 2048 rows without 31 us.
 // ---------------------------------------------------------------------------
 template <int DT, bool GRAD>
 __global__ __launch_bounds__(1024) void loss_rows_kernel(const float *__restrict__ logits, int64_t ld, int64_t v0, int n,
