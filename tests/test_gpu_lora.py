@@ -82,7 +82,7 @@ def test_odd_widths_forward(N, K, T):
 
 
 # enough tokens and columns for the tile product (640 tokens, 144 tiles of 256 x 256), whole tiles and
-# parts of them, of the outputs (forward: N, backward: K) or sums; turns of 16384 and of 4096 tokens
+# parts of them, of the outputs (forward: N, backward: K) or sums; turns of 8192 and of 4096 tokens
 @pytest.mark.parametrize("T,N,K,rank", [(640, 12320, 64, 16), (700, 12544, 192, 8), (1100, 7456, 128, 40), (768, 12288, 64, 128),
                                         (16400, 768, 64, 16), (4100, 96, 96, 8), (5000, 320, 32, 24)])
 @pytest.mark.parametrize("dtype", [BF, HF])
