@@ -65,8 +65,9 @@ typedef struct {
  * qmv_gemm_4bit; the adapter's part is computed from its operands as they are, with
  * sums in fp32.  For more than 64 tokens the inner values, scale[a] down[a] x[t], are
  * carried into the second product as two 16-bit terms: off by 2^-16 of themselves
- * for bf16, 2^-22 for fp16, where they have to be below 65520 and what is below
- * 2^-25 is lost.
+ * for bf16.  For fp16 both terms are held times a power of two chosen by the token's
+ * largest inner value: off by 2^-22 of themselves or 2^-39 of that largest one, whichever is
+ * more, where that is between 2^-64 and 2^92.
  *   x      [T, K] device, dtype bf16 or fp16 (fp32: QMV_ERR_UNSUPPORTED)
  *   index  [T] device int32, 4-byte aligned
  *   bias   NULL or [N] in dtype
@@ -83,7 +84,9 @@ int qmv_lora_4bit(const void *x, qmv_dtype dtype, int64_t T, const qmv_weight_4b
  * y, with u = scale down x and v = scale up^T dy of each token:
  *   dx[t] = W_hat^T dy[t] + down[a]^T v[t]
  *   d_down[a] = sum of v[t] x[t]^T,  d_up[a] = sum of dy[t] u[t]^T   over the
- * tokens of adapter a (zeros for an adapter without tokens).
+ * tokens of adapter a (zeros for an adapter without tokens).  u and v are two 16-bit
+ * terms in every product here, for any T, as in lora_4bit; in fp16 sums over an adapter's
+ * tokens take them off by 2^-22 of themselves or 2^-37 of the adapter's largest.
  *   dy     [T, N], x [T, K] device, dtype bf16 or fp16; N a multiple of 32
  *          (QMV_ERR_UNSUPPORTED)
  *   dx     [T, K] device, dtype

@@ -8,7 +8,7 @@
 // a workgroup for each token and part of the columns.  More: tokens are put in
 // order of their adapters, so that tiles of the matrix cores meet one adapter,
 // or few; u and v, a handful of values a token, are summed in fp32 and carried
-// into the second products as two 16-bit terms.  Many: the weight is decoded
+// into the second products as two 16-bit terms (fp16: times a power of two).  Many: the weight is decoded
 // once, and the adapters' part is added to the tile product's sums before they
 // are rounded.
 #include "qmv_tile.hpp"
@@ -349,27 +349,60 @@ __global__ __launch_bounds__(256, 2) void lora_shrink_kernel(const uint16_t *__r
 }
 
 // The parts added up in order, as two 16-bit terms [T][Rp] (Rp: R up to a multiple
-// of 16, zeros past R): the first is off by half a step, the second by half a step of that
+// of 16, zeros past R): the first is off by half a step, the second by half a step of that.
+// fp16 reaches from 2^-24 to 65504 only, and v, a product of two small numbers where a
+// training starts, lies below that: there a place's values are held times a power of two,
+// its gain, that brings the largest of them to 2^14 or more.  Then what is 2^-17 of the
+// largest or more keeps its 22 bits, and nothing is off by more than 2^-39 of the largest; the
+// products are divided by the gain in fp32, exactly.  Each place has a gain of its own, so that
+// no token's part depends on another's.  Gains end at 2^+-78: projections, which are whole
+// multiples of 2^-48 up to 2^48, can be multiplied by one and divided again.
+// A place's values are 16 lanes', 16 places a workgroup: u and v of 4096 tokens, rank 16 4.9 us.
 struct Split {
   const float *parts;
   int pieces;
   uint16_t *hi, *lo;
+  float *gain;  // [T], fp16 only
 };
-template <int DT>
+constexpr int kMostGain = 78;
+
+__device__ __forceinline__ float one_over(float power_of_two) { return __uint_as_float(0x7f000000u - __float_as_uint(power_of_two)); }
+
+template <int DT, int NT>
 __global__ __launch_bounds__(256) void lora_split_kernel(Split one, Split two, int64_t T, int R, int Rp, int count,
                                                          const int32_t *__restrict__ start) {
   const Split s = blockIdx.y ? two : one;
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= T * Rp) return;
-  const int64_t p = i / Rp;
-  const int r = (int)(i % Rp);
-  float sum = 0.f;
-  if (r < R && p < start[count])
-#pragma unroll 8
-    for (int k = 0; k < s.pieces; ++k) sum += s.parts[(k * T + p) * R + r];
-  const uint32_t hi = f32_to_bits16<DT>(sum);
-  s.hi[i] = (uint16_t)hi;
-  s.lo[i] = (uint16_t)f32_to_bits16<DT>(sum - bits16_to_f32<DT>(hi));
+  const int64_t p = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
+  const int l16 = threadIdx.x & 15;
+  if (p >= T) return;
+  const bool there = p < start[count];
+  float v[NT];
+#pragma unroll
+  for (int j = 0; j < NT; ++j) v[j] = 0.f;
+  if (there)
+#pragma unroll 4
+    for (int k = 0; k < s.pieces; ++k)
+#pragma unroll
+      for (int j = 0; j < NT; ++j) v[j] += s.parts[(k * T + p) * R + min(16 * j + l16, R - 1)];
+  float gain = 1.f;
+  if constexpr (DT == kF16) {
+    float most = 0.f;  // of the finite ones: the others spoil their token whatever the gain
+#pragma unroll
+    for (int j = 0; j < NT; ++j) most = fmaxf(most, fabsf(v[j]) < INFINITY ? fabsf(v[j]) : 0.f);
+    most = group_max(most, 16);
+    const int e = 14 - ((int)(__float_as_uint(most) >> 23) - 127);
+    if (there) gain = __uint_as_float((uint32_t)(127 + max(-kMostGain, min(e, kMostGain))) << 23);
+    if (l16 == 0) s.gain[p] = gain;
+  }
+#pragma unroll
+  for (int j = 0; j < NT; ++j) {
+    const int r = 16 * j + l16;
+    if (r >= Rp) break;
+    const float value = r < R ? v[j] * gain : 0.f;
+    const uint32_t hi = f32_to_bits16<DT>(value);
+    s.hi[p * Rp + r] = (uint16_t)hi;
+    s.lo[p * Rp + r] = (uint16_t)f32_to_bits16<DT>(value - bits16_to_f32<DT>(hi));
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -383,6 +416,7 @@ __global__ __launch_bounds__(256) void lora_split_kernel(Split one, Split two, i
 // ---------------------------------------------------------------------------
 struct LowRank {
   const uint16_t *hi, *lo;  // [T][Rp]
+  const float *gain;        // [T], fp16: what hi and lo have been multiplied by
   const uint16_t *factor;   // up [count][width][R], or down [count][R][width]
   int64_t width;
   int R, Rp, count;
@@ -495,13 +529,15 @@ __global__ __launch_bounds__(256, 2) void lora_expand_kernel(const float *__rest
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, h = lane >> 5, l32 = lane & 31;
   const int64_t c0 = (int64_t)blockIdx.y * 128 + 32 * wave, c = c0 + l32, cin = min(c, lr.width - 1);
   if (c0 >= lr.width) return;
-  float old[2][16];
+  float old[2][16], gain[2][16];
   int64_t token[2][16];
 #pragma unroll
   for (int i = 0; i < 2; ++i)
 #pragma unroll
     for (int r = 0; r < 16; ++r) {
-      token[i][r] = pl.order[min(unit.y + 32 * i + 8 * (r >> 2) + 4 * h + (r & 3), unit.z - 1)];
+      const int p = min(unit.y + 32 * i + 8 * (r >> 2) + 4 * h + (r & 3), unit.z - 1);
+      token[i][r] = pl.order[p];
+      gain[i][r] = DT == kF16 ? lr.gain[p] : 1.f;
       old[i][r] = base[token[i][r] * lr.width + cin];
     }
   const float more = bias ? bits16_to_f32<DT>(bias[cin]) : 0.f;
@@ -517,7 +553,7 @@ __global__ __launch_bounds__(256, 2) void lora_expand_kernel(const float *__rest
 #pragma unroll
     for (int r = 0; r < 16; ++r)
       if (unit.y + 32 * i + 8 * (r >> 2) + 4 * h + (r & 3) < unit.z)
-        store_elem<ODT>(out, token[i][r] * lr.width + c, acc[i][0][r] + old[i][r] + more);
+        store_elem<ODT>(out, token[i][r] * lr.width + c, acc[i][0][r] * one_over(gain[i][r]) + old[i][r] + more);
 }
 
 // The tile product's sums, rows by place, with the adapters' part and the bias; row's token
@@ -529,15 +565,34 @@ struct EpilogueLora : EpilogueBase {
   const uint16_t *bias;
   OT *out;
   int64_t ld;
+  struct Row {
+    OT *out;
+    float scale;  // 1 / gain
+  };
   __device__ __forceinline__ bool begin(tile_acc_t (&acc)[4][4], int N, int m, int end, int n, int lane) const {
+    if constexpr (DT == kF16) {  // the sums so far times their rows' gains (there is room for whole tiles of these)
+      if (m < end)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const float4 g = *reinterpret_cast<const float4 *>(lr.gain + m + 32 * i + 8 * q + 4 * (lane >> 5));
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              acc[i][j][4 * q] *= g.x, acc[i][j][4 * q + 1] *= g.y, acc[i][j][4 * q + 2] *= g.z, acc[i][j][4 * q + 3] *= g.w;
+          }
+    }
     return add_low_rank<DT, TRANS, true>(acc, lr, m, end, n, N, lane);
   }
   __device__ __forceinline__ void end(int N, int m, int past, int n, int lane) const {
     mark_low_rank<DT, ODT, TRANS, 4>(lr, m, past, n, N, lane, order, out, ld);
   }
-  __device__ __forceinline__ OT *row(int m) const { return out + order[m] * ld; }
-  __device__ __forceinline__ void store(OT *row, int n, float v) const {
-    store_elem<ODT>(row, n, bias ? v + bits16_to_f32<DT>(bias[n]) : v);
+  __device__ __forceinline__ Row row(int m) const {
+    return Row{out + order[m] * ld, DT == kF16 ? one_over(lr.gain[m]) : 1.f};
+  }
+  __device__ __forceinline__ void store(const Row &row, int n, float v) const {
+    v *= row.scale;
+    store_elem<ODT>(row.out, n, bias ? v + bits16_to_f32<DT>(bias[n]) : v);
   }
 };
 
@@ -551,17 +606,34 @@ struct EpilogueLora : EpilogueBase {
 // A wave has 32 columns and all ranks.  An adapter whose places lie in one
 // window is done then; a part of a run that goes on is left in fp32 (a window
 // has two at most: one that began before it, and one that goes on after), and
-// lora_join_kernel adds an adapter's parts in order.  Bound by the read of g and the
+// lora_join_kernel adds an adapter's parts in order.  In fp16 the places' gains differ, and a
+// sum over places needs one: the smallest of the run, to which the others' terms are brought on
+// their way into LDS (off by at most 2^-37 of the run's largest value; 1537 tokens x 14336, rank 64
+// 26 instead of 21 us).  Bound by the read of g and the
 // parts' writes: 4096 tokens x 14336, rank 16 27.5 us (4.3 TB/s of g).
 // ---------------------------------------------------------------------------
+// Eight fp16 values held times `own`, brought to the gain `all`, which is no larger.  Both are powers of two; the factor is
+// below fp16's smallest normal number for a place far below the run's largest: then in two steps, and
+// from 2^-39 on, where nothing of a value up to 2^15 is left, zero (which keeps a NaN, and makes one of an infinity)
+__device__ __forceinline__ u32x4_t to_gain(const u32x4_t &v, float own, float all) {
+  typedef __attribute__((ext_vector_type(8))) _Float16 half8_t;
+  const int down = (int)((__float_as_uint(own) - __float_as_uint(all)) >> 23);
+  const int one = min(down, 14), two = min(down - one, 24);
+  const _Float16 a = (_Float16)__uint_as_float((uint32_t)(127 - one) << 23);
+  const _Float16 b = down < 39 ? (_Float16)__uint_as_float((uint32_t)(127 - two) << 23) : (_Float16)0.f;
+  return __builtin_bit_cast(u32x4_t, __builtin_bit_cast(half8_t, v) * a * b);
+}
+
 template <int DT, int ODT, int NT, bool UP>
 __global__ __launch_bounds__(256, 2) void lora_grad_kernel(const uint16_t *__restrict__ gp, int64_t W,
                                                         const uint16_t *__restrict__ hi, const uint16_t *__restrict__ lo,
-                                                        int R, int Rp, int count, int window, Places pl,
+                                                        const float *__restrict__ gain, int R, int Rp, int count,
+                                                        int window, Places pl,
                                                         float *__restrict__ parts,
                                                         typename Storage<ODT>::type *__restrict__ out) {
   constexpr int kG = 128 + 16, kH = 32 * NT + 16;  // pitches: rows 8 (mod 64) banks apart
   __shared__ __attribute__((aligned(16))) uint16_t gs[64 * kG], hs[2][64 * kH];
+  __shared__ float least[4];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, l32 = lane & 31, h = lane >> 5;
   const int64_t w0 = (int64_t)blockIdx.x * 128;
   const int first = blockIdx.y * window, there = pl.start[count];
@@ -585,6 +657,7 @@ __global__ __launch_bounds__(256, 2) void lora_grad_kernel(const uint16_t *__res
     // read at the run's last place, and zeroed on its way into LDS.  (As vectors: taken apart into
     // words they would be copied, each with a wait, before the loop's end.)
     u32x4_t gv[4], hv[2][NT];
+    float own[NT];
     int token[4];
     auto find = [&](int q) __attribute__((always_inline)) {
 #pragma unroll
@@ -596,7 +669,9 @@ __global__ __launch_bounds__(256, 2) void lora_grad_kernel(const uint16_t *__res
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
         const int c = 256 * j + tid;
-        const int64_t from = (int64_t)min(q + c / (4 * NT), end - 1) * Rp + min(8 * (c % (4 * NT)), Rp - 8);
+        const int at = min(q + c / (4 * NT), end - 1);
+        const int64_t from = (int64_t)at * Rp + min(8 * (c % (4 * NT)), Rp - 8);
+        if constexpr (DT == kF16) own[j] = gain[at];
         hv[0][j] = *reinterpret_cast<const u32x4_t *>(hi + from);
         hv[1][j] = *reinterpret_cast<const u32x4_t *>(lo + from);
       }
@@ -604,6 +679,15 @@ __global__ __launch_bounds__(256, 2) void lora_grad_kernel(const uint16_t *__res
     find(p);
     load(p);
     find(p + 64);
+    float all = 1.f;  // the run's gain
+    if constexpr (DT == kF16) {
+      all = INFINITY;
+      for (int q = p + tid; q < end; q += 256) all = fminf(all, gain[q]);
+      all = -wave_max(-all);
+      if (lane == 0) least[wave] = all;
+      __syncthreads();  // read by all before the next run's: the steps' barriers are between
+      all = fminf(fminf(least[0], least[1]), fminf(least[2], least[3]));
+    }
     for (int q = p; q < end; q += 64) {
       __syncthreads();
 #pragma unroll
@@ -615,6 +699,10 @@ __global__ __launch_bounds__(256, 2) void lora_grad_kernel(const uint16_t *__res
       for (int j = 0; j < NT; ++j) {
         const int c = 256 * j + tid, row = c / (4 * NT), at = row * kH + 8 * (c % (4 * NT));
         const uint32_t in = q + row < end ? ~0u : 0u;
+        if constexpr (DT == kF16) {
+          hv[0][j] = to_gain(hv[0][j], own[j], all);
+          hv[1][j] = to_gain(hv[1][j], own[j], all);
+        }
         *reinterpret_cast<u32x4_t *>(hs[0] + at) = hv[0][j] & in;
         *reinterpret_cast<u32x4_t *>(hs[1] + at) = hv[1][j] & in;
       }
@@ -635,6 +723,7 @@ __global__ __launch_bounds__(256, 2) void lora_grad_kernel(const uint16_t *__res
     }
     const bool whole = begin >= first && past <= last;
     float *keep = parts + (int64_t)(2 * blockIdx.y + (begin >= first)) * W * R;
+    const float scale = one_over(all);
 #pragma unroll
     for (int j = 0; j < NT; ++j)
 #pragma unroll
@@ -644,8 +733,9 @@ __global__ __launch_bounds__(256, 2) void lora_grad_kernel(const uint16_t *__res
         const int rank = 32 * j + (UP ? l32 : in);
         if (w >= W || rank >= R) continue;
         const int64_t at = UP ? w * R + rank : rank * W + w;
-        if (whole) store_elem<ODT>(out, (int64_t)a * W * R + at, acc[j][r]);
-        else keep[at] = acc[j][r];
+        const float sum = DT == kF16 ? acc[j][r] * scale : acc[j][r];
+        if (whole) store_elem<ODT>(out, (int64_t)a * W * R + at, sum);
+        else keep[at] = sum;
       }
     p = end;
   }
@@ -699,7 +789,7 @@ static int inner_piece(int64_t L, int pieces) { return (int)(((L + pieces - 1) /
 
 struct InnerPlan {
   int pieces, piece;
-  size_t parts, hi, lo;
+  size_t parts, hi, lo, gain;
 };
 static InnerPlan inner_plan(Carver &c, int64_t T, int64_t L, int R, int count) {
   InnerPlan p{};
@@ -708,6 +798,7 @@ static InnerPlan inner_plan(Carver &c, int64_t T, int64_t L, int R, int count) {
   const int64_t Rp = (R + 15) & ~15;
   p.parts = c.take((size_t)p.pieces * T * R * 4);
   p.hi = c.take((size_t)T * Rp * 2), p.lo = c.take((size_t)T * Rp * 2);
+  p.gain = c.take((size_t)((T + kTileM - 1) / kTileM) * kTileM * 4);  // read by whole tiles
   return p;
 }
 
@@ -860,14 +951,14 @@ static void shrink(const uint16_t *x, int64_t T, int64_t L, const uint16_t *fact
 
 static Split split_of(const InnerPlan &p, char *ws) {
   return Split{reinterpret_cast<float *>(ws + p.parts), p.pieces, reinterpret_cast<uint16_t *>(ws + p.hi),
-               reinterpret_cast<uint16_t *>(ws + p.lo)};
+               reinterpret_cast<uint16_t *>(ws + p.lo), reinterpret_cast<float *>(ws + p.gain)};
 }
 
 template <int DT>
 static void split(const Split &one, const Split *two, int64_t T, const Lora &l, const Places &pl, hipStream_t st) {
   const int Rp = (l.rank + 15) & ~15;
-  hipLaunchKernelGGL(lora_split_kernel<DT>, dim3((unsigned)((T * Rp + 255) / 256), two ? 2 : 1), dim3(256), 0, st, one,
-                     two ? *two : one, T, l.rank, Rp, l.count, pl.start);
+  QMV_RANKS(Rp / 16, hipLaunchKernelGGL((lora_split_kernel<DT, NT>), dim3((unsigned)((T + 15) / 16), two ? 2 : 1), dim3(256), 0,
+                                        st, one, two ? *two : one, T, l.rank, Rp, l.count, pl.start))
 }
 
 static void order(const int32_t *index, int64_t T, const Lora &l, const Places &pl, hipStream_t st) {
@@ -882,7 +973,7 @@ static hipError_t product(const LoraPlan &p, const uint16_t *x, int64_t m, const
   const int64_t L = TRANS ? w.N : w.K, width = TRANS ? w.K : w.N;
   const Split s = split_of(p.inner, ws);
   const int Rp = (l.rank + 15) & ~15;
-  const LowRank lr{s.hi, s.lo, TRANS ? l.down : l.up, width, l.rank, Rp, l.count, pl.adapter, pl.start};
+  const LowRank lr{s.hi, s.lo, s.gain, TRANS ? l.down : l.up, width, l.rank, Rp, l.count, pl.adapter, pl.start};
   const ProductPlan &pp = p.product;
   float *base = reinterpret_cast<float *>(ws + pp.base);
   if (pp.tiled || pp.parts) {
@@ -994,7 +1085,7 @@ static hipError_t lora_backward_t(const uint16_t *dy, const uint16_t *x, int64_t
     constexpr bool UP = decltype(up)::value;
     const dim3 grid((unsigned)((W + 127) / 128), (unsigned)((T + window - 1) / window));
     QMV_RANKS((R + 31) / 32, hipLaunchKernelGGL((lora_grad_kernel<DT, ODT, (NT > 4 ? 4 : NT), UP>), grid, dim3(256), 0, st,
-                                                g, W, h.hi, h.lo, R, Rp, l.count, window, pl, parts, static_cast<OT *>(out)))
+                                                g, W, h.hi, h.lo, h.gain, R, Rp, l.count, window, pl, parts, static_cast<OT *>(out)))
     const int64_t n = W * R;
     hipLaunchKernelGGL((lora_join_kernel<ODT>), dim3((unsigned)((n + 1023) / 1024), (unsigned)l.count), dim3(256), 0, st,
                        parts, n, window, pl.start, static_cast<OT *>(out));
