@@ -22,7 +22,7 @@ constexpr int64_t kTokens = 4096;  // most tokens taken at a time
 constexpr int kTail = 64;
 constexpr int kMostPiece = 32768;   // of the tile product's pieces
 constexpr int64_t kTiledFrom = 448;  // tokens from which it is used
-constexpr int64_t kLogits = (int64_t)1 << 26;  // logits of a piece where it is not
+constexpr int64_t kLogits = (int64_t)1 << 26;  // logits of a piece where it is not, all slices of the sum together
 
 // What exp(l - m) is multiplied by before its rounding.  fp16 has no normal
 // numbers below 2^-14: with 2^14 (sums are fp32, and D is divided by it at the
@@ -501,12 +501,13 @@ static LossPlan loss_plan(int64_t T, int64_t V, int64_t K, int log2bs, int k, bo
     }
   } else {
     p.parts = 1;
-    int64_t piece = (kLogits / p.tokens) & ~(int64_t)4095;  // rows_of wants 4096 rows
+    const int64_t slices = skinny_fits(p.tokens, K, log2bs) ? skinny_parts(K) : 1;  // each with logits of its own
+    int64_t piece = (kLogits / (p.tokens * slices)) & ~(int64_t)4095;  // rows_of wants 4096 rows
     if (piece < 4096) piece = 4096;
     if (p.mixed && piece > kMostPiece) piece = kMostPiece;
     p.piece = (int)(V < piece ? V : piece);
     if (p.mixed) d_parts();
-    p.logits = c.take(n * p.piece * 4 * (skinny_fits(p.tokens, K, log2bs) ? skinny_parts(K) : 1));
+    p.logits = c.take(n * p.piece * 4 * slices);
     p.segments = c.take(n * ((p.piece + kSegment - 1) / kSegment) * 8);
     p.carry = c.take(n * 16);
     if (grad) {
