@@ -197,6 +197,8 @@ double_quant = _double_quant
 
 def dequantize_absmax(state: QuantState) -> torch.Tensor:
     ref = state.absmax if state.absmax is not None else state.absmax_q
+    for name in ("absmax", "absmax_q", "absmax2", "offset", "code2"):
+        _check_dense(name, getattr(state, name))
     out = torch.empty(state.nblocks, dtype=torch.float32, device=ref.device)
     c = state._c()
     _check(lib().qmv_dequantize_absmax(ctypes.byref(c), state.nblocks, out.data_ptr(),
@@ -219,10 +221,15 @@ def dequantize_4bit(packed: torch.Tensor, state: QuantState, out: Optional[torch
     return out
 
 
+def _check_dense(name: str, t: Optional[torch.Tensor]) -> None:
+    if t is not None and not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous, got strides {t.stride()}")
+
+
 def _check_state(packed: torch.Tensor, state: QuantState, device=None) -> None:
     """Refuses a packed tensor or QuantState whose sizes or devices do not
-    match, before anything reaches a kernel (which would otherwise read past
-    the ends of the buffers)."""
+    match, or whose scales have gaps, before anything reaches a kernel (which
+    would otherwise read other values, or past the ends of the buffers)."""
     if packed.dtype != torch.uint8 or packed.numel() != (state.numel + 1) // 2:
         raise ValueError(f"packed must hold ceil(numel / 2) = {(state.numel + 1) // 2} uint8 "
                          f"bytes, got {packed.numel()} of {packed.dtype}")
@@ -244,6 +251,7 @@ def _check_state(packed: torch.Tensor, state: QuantState, device=None) -> None:
             raise ValueError(f"{name} must hold {n} values of {dt}, got {t.numel()} of {t.dtype}")
         if t.device != dev:
             raise ValueError(f"{name} is on {t.device}, the operands on {dev}")
+        _check_dense(name, t)
     if packed.device != dev:
         raise ValueError(f"packed is on {packed.device}, the operands on {dev}")
 

@@ -87,14 +87,14 @@ def _weight(packed: torch.Tensor, state: QuantState, device):
     rows, cols = shape
     n, bs = rows * cols, state.blocksize
     nb = -(-n // bs)
+    dense = lambda t, n, dtype: _holds(t, n, dtype, device) and t.is_contiguous()
     q, a2, off, c2, bs2 = state.absmax_q, state.absmax2, state.offset, state.code2, state.blocksize2
     if state.absmax is not None:
-        fits = q is None and a2 is None and off is None and c2 is None and _holds(state.absmax, nb, torch.float32, device)
+        fits = q is None and a2 is None and off is None and c2 is None and dense(state.absmax, nb, torch.float32)
         scales = _Absmax(state.absmax.data_ptr(), None, None, None, None, 0) if fits else None
     else:
-        fits = (q is not None and a2 is not None and off is not None and c2 is not None and _holds(q, nb, torch.uint8, device)
-                and _holds(a2, -(-nb // bs2), torch.float32, device) and _holds(off, 1, torch.float32, device)
-                and _holds(c2, 256, torch.float32, device))
+        fits = (q is not None and a2 is not None and off is not None and c2 is not None and dense(q, nb, torch.uint8)
+                and dense(a2, -(-nb // bs2), torch.float32) and dense(off, 1, torch.float32) and dense(c2, 256, torch.float32))
         scales = _Absmax(None, q.data_ptr(), a2.data_ptr(), c2.data_ptr(), off.data_ptr(), bs2) if fits else None
     if not fits or not _holds(packed, (n + 1) // 2, torch.uint8, device):
         _check_state(packed, state, device)  # says what does not fit
