@@ -62,7 +62,8 @@ typedef struct {
  *   y[t] = W_hat x[t] + bias + up[a] (scale[a] down[a] x[t]),
  * rounded once to y_dtype; a token whose index is outside [0, count) has no
  * adapter.  The projection's operands are those of qmv_gemv_4bit and
- * qmv_gemm_4bit; the adapter's part is computed from its operands as they are, with
+ * qmv_gemm_4bit (the table's values or the weights rounded to dtype, see
+ * cross_entropy_4bit); the adapter's part is computed from its operands as they are, with
  * sums in fp32.  For more than 64 tokens the inner values, scale[a] down[a] x[t], are
  * carried into the second product as two 16-bit terms: off by 2^-16 of themselves
  * for bf16.  For fp16 both terms are held times a power of two chosen by the token's
@@ -107,14 +108,17 @@ int qmv_lora_4bit_backward(const void *dy, const void *x, qmv_dtype dtype, int64
  *   dx[t] = dloss[t] (sum_v softmax(l)_v W_hat[v] - W_hat[target[t]]).
  * A token whose target is outside [0, V) does not count: its loss is 0, its
  * row of dx is zeros.  The vocabulary is taken in pieces, and tokens 4096 at a
- * time: at no time are there more than 2^26 logits.
+ * time: at no time are there more than 2^26 logits (those of 17 to 64 tokens come in
+ * slices of the sum, which count here each).
  *   x       [T, K] device, dtype bf16 or fp16 (fp32: QMV_ERR_UNSUPPORTED)
  *   target  [T] device int64, 8-byte aligned
  *   dloss   NULL or [T] device fp32;  dx  NULL or [T, K] device, dtype: both or neither
  *   loss    [T] device, loss_dtype: dtype or fp32
- * Products are those of qmv_gemm_4bit and qmv_gemm_4bit_backward (weights
- * rounded to dtype, sums in fp32); maxima, sums and the target's part of the
- * gradient are fp32, exp(l - max) is rounded to dtype for the second product.
+ * Products have the operands of qmv_gemm_4bit and qmv_gemm_4bit_backward, with sums
+ * in fp32: weights rounded to dtype, or, in the kernels for up to 64 tokens' logits,
+ * the table's values rounded to dtype and the block's scale applied in fp32 (one
+ * rounding of the weight either way).  Maxima, sums and the target's part of the gradient are fp32,
+ * exp(l - max) is rounded to dtype for the second product.
  */
 size_t qmv_cross_entropy_4bit_workspace(int64_t T, int64_t V, int64_t K, int32_t blocksize, int32_t grad);
 int qmv_cross_entropy_4bit(const void *x, qmv_dtype dtype, int64_t T, const qmv_weight_4bit *w,
@@ -128,8 +132,11 @@ int qmv_cross_entropy_4bit(const void *x, qmv_dtype dtype, int64_t T, const qmv_
  * is in [0, V), p = softmax(z) and q = softmax(W_hat x[t] / temperature):
  *   loss[t] = sum_j p_j (log p_j - log q_ids[j])
  *   dx[t]   = dloss[t] / temperature (sum_v q_v W_hat[v] - sum_j p_j W_hat[ids[j]]).
- * An entry of -inf has p = 0; an id that comes twice has the sum of its p in
- * the gradient.  A token without an entry of finite logit has loss 0 and zeros in dx.
+ * An entry of -inf has p = 0.  A token without an entry of finite logit has loss 0
+ * and zeros in dx.  An id that comes twice is two entries: in the loss each has its
+ * own log p_j, so that this is less than the divergence from the distribution with
+ * their p summed to P (by the sum of p_j log(P / p_j)), and may be negative; the
+ * gradient is the same.  For the divergence the ids of a token have to differ.
  *   ids      [T, k] device int64, 8-byte aligned;  teacher [T, k] device, any type
  *   k        1 .. 128 (QMV_ERR_UNSUPPORTED);  temperature finite, > 0
  * The rest as for cross_entropy_4bit.

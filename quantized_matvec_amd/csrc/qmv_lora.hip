@@ -519,7 +519,7 @@ __device__ __forceinline__ void mark_low_rank(const LowRank &lr, int p0, int end
 
 // out[t][c] = round(base[t][c] + bias[c] + the adapter's part): a unit and 128 columns
 // a workgroup, 32 columns a wave; base's loads go out first.  Bound by base and out, and few
-// workgroups: 301 tokens x 8192, rank 64 13.9 us.
+// workgroups: 301 tokens x 8192, rank 64, fp16 14.6 us.
 template <int DT, int ODT, bool TRANS>
 __global__ __launch_bounds__(256, 2) void lora_expand_kernel(const float *__restrict__ base, LowRank lr, Places pl,
                                                           const uint16_t *__restrict__ bias,

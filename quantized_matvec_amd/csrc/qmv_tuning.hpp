@@ -47,8 +47,13 @@ inline int64_t to64(int64_t v) { return (v + 63) & ~(int64_t)63; }
 
 // Whether gemm_4bit_backward is the quickest way to M rows of [N, K] of up to some hundred rows: it has to take its
 // kernel that divides the sum among workgroups, and the last workgroup of each 128 x 256 tile then adds up all parts of
-// it, 2.1 us each.  The other way decodes the weight and multiplies that (qmv_tile.hpp), about 1 us for 2^20 weights and
-// 30 us.  19 rows of 4608 x 768: 98 us by gemm_4bit_backward, 84 of them for 72 parts.
+// it, about 1.2 us each (19 rows of 4608 x 768: 98 us, 84 of them for 72 parts).  The other way decodes the weight and
+// multiplies that (qmv_tile.hpp).  The rule is a line between 2.5 us for each of 256 / tiles parts (also where N / 64
+// is less, the most there can be) and 1 us for 2^20 weights and 24 us.  Both sides, us of lora_4bit_backward with rank 16
+// by gemm_4bit_backward / by the other: 19 rows of 4608 x 768 135 / 73, 200 rows of 8192 x 4096 101 / 112.  Over
+// K from 256 to 8192, N from 512 to 32768 and 19 to 600 rows it is 3 % above the faster side on average; farthest are
+// 600 rows (14336 x 4096 237 / 171: takes the first) and small weights (64 rows of 512 x 768, a loss with its gradient,
+// 51 / 61: takes the second).
 inline bool fast_backward(int64_t M, int64_t N, int64_t K, int log2bs) {
   if (N % 64 || K % 256 || log2bs < 6) return false;
   return (N * K >> 20) >= 166000 / (K * ((M + 127) / 128)) - 24;

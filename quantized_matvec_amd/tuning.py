@@ -293,7 +293,8 @@ def distill_4bit(x: torch.Tensor, packed: torch.Tensor, state: QuantState, ids: 
     """Divergence [T] of softmax(x @ W_hat^T / temperature) from the
     distribution softmax(teacher / temperature) over the ids of a teacher's
     largest logits: ``ids`` int64 [T, k] (an id outside [0, V) is no entry) and
-    ``teacher`` [T, k], k up to 128.  ``dloss`` and the result as for
+    ``teacher`` [T, k], k up to 128.  The ids of a row differ: one that comes
+    twice is two entries, each with its own log p in the loss.  ``dloss`` and the result as for
     cross_entropy_4bit."""
     x2, packed, w, dloss, loss, dx = _loss_operands(x, packed, state, dloss, loss_dtype, dx)
     T = x2.shape[0]
